@@ -458,6 +458,163 @@ qe_status qe_restore(qe_handle h, const void* host, size_t bytes);
  * stream without waiting. */
 qe_status qe_decode_step_noalloc(qe_handle h, int layer, const void* q, void* out);
 
+/* ---------------------------------------------------------------- paged cache
+ *
+ * Not part of the method on the pages (which leave paging, prefix sharing and prefill to the
+ * serving system, H2O page §6, KV Cache evolution page §10): what comes before the tiered cache.
+ * Sequences of different lengths keep their exact keys and values in pages of one pool, share
+ * the pages of common prefixes, and are prefilled in chunks; qe_pages_gather hands a prefilled
+ * prompt to qe_append in the layout it takes.  One step of a serving loop is
+ *   qe_pages_resize (pages for the new tokens), then per layer qe_pages_append (rotary
+ *   positions, keys and values into the pages) and qe_pages_attend (the chunk's attention).
+ *
+ * These calls have no handle: the caller owns every buffer, describes it in the structs below,
+ * and passes the stream.  All pointers are device memory of device `device` unless stated; the
+ * structs are host memory and only read during the call.  The calls enqueue their work and
+ * return without waiting, allocate nothing, may be captured into CUDA graphs, keep nothing
+ * between calls, and leave the current device as it was.  Lengths, tables and positions are
+ * read on the device when the work runs, so a replayed graph sees their new values.
+ * On failure qe_last_error(NULL) has the message (of the calling thread).
+ *
+ * What the host cannot check is checked on the device: a page index outside [0, n_pages), a row
+ * outside [0, n_rows), a length outside [0, max_pages * page_size], a q_start that decreases or
+ * passes total_q, a call that needs more free pages than there are.  Such an entry is skipped
+ * (a key on a bad page counts as zeros, a bad row as empty; a resize or fork short of pages does nothing
+ * at all) and sets a bit of *err (QE_PAGES_ERR_*), which stays set until the caller clears it.
+ *
+ * Workspaces are scratch: nothing in them needs to be set before a call or kept after it.  Work
+ * that may overlap on the GPU (other streams, graphs replayed side by side) needs workspaces of
+ * its own. */
+
+enum { QE_DTYPE_BF16 = 0, QE_DTYPE_FP16 = 1 };
+enum {
+  QE_PAGES_ERR_PAGE = 1,      /* a page index outside the pool, or a count of references that went wrong */
+  QE_PAGES_ERR_ROW = 2,       /* a row index, length or q_start out of range, or a row named twice */
+  QE_PAGES_ERR_NO_PAGES = 4,  /* not enough free pages: the call changed nothing */
+  QE_PAGES_ERR_TIMEOUT = 8    /* a bounded device wait expired: that call's outputs are undefined */
+};
+
+/* The pool.  Element (layer, page, head, token, channel) of the keys is at
+ * k + layer * layer_stride + page * page_stride + head * head_stride + token * token_stride + channel
+ * (elements), of the values at the same place of v.  Pointers and strides are multiples of 16 bytes
+ * (8 elements); the pages, heads and tokens of a layer do not overlap.  Sizes that can be served:
+ * page_size 16, 32, 64, 128 or 256; head_dim 64 or 128. */
+typedef struct {
+  void* k;
+  void* v;
+  int dtype;              /* QE_DTYPE_* */
+  int device;             /* CUDA device ordinal of every buffer */
+  int n_layers, n_pages, n_kv_heads, page_size, head_dim;
+  long long layer_stride, page_stride, head_stride, token_stride;
+  unsigned* err;          /* device word, or NULL: nothing is reported */
+} qe_pages;
+
+/* The sequences.  Row r holds the tokens [0, kv_len[r]) of one sequence, on the pages
+ * table[r * row_stride + i], i < ceil(kv_len[r] / page_size); entries behind them are -1 after
+ * the calls that manage pages.  refs[p] is how many table entries name page p, 0 for a free page
+ * (qe_pages_append, _attend and _gather do not read it; it may be NULL for them).  A page that two rows
+ * share is full: the calls below keep it so. */
+typedef struct {
+  int* table;
+  int* kv_len;            /* [n_rows] */
+  int* refs;              /* [n_pages] */
+  long long row_stride;   /* elements */
+  int n_rows, max_pages;
+} qe_page_table;
+
+/* Rotary positions of several axes.  Channel pair i < rot_dim / 2 of a head is rotated by the
+ * angle positions[axis[i]][token] * inv_freq[i]: (x, y) -> (x cos - y sin, x sin + y cos).  A pair is
+ * channels (2i, 2i + 1), or (i, i + rot_dim / 2) with halves = 1; channels from rot_dim on are left as
+ * they are.  The angle is reduced exactly (64-bit fixed point turns), at any int32 position. */
+typedef struct {
+  int rot_dim;            /* even, 0 .. head_dim; with halves or not a multiple of 16 */
+  int halves;
+  int n_axes;             /* 1 .. 8 */
+  signed char axis[64];
+  double inv_freq[64];
+} qe_rope;
+
+/* The new tokens of n_seqs sequences, packed: tokens [q_start[i], q_start[i + 1]) belong to row
+ * rows[i] (row i where rows is NULL) and are the last of its kv_len tokens: token j of a chunk of m
+ * sits at position kv_len - m + j (kv_len counts them already).  total_q is the number of packed tokens
+ * (the end of q_start); tokens at or behind q_start[n_seqs] are left alone. */
+typedef struct {
+  const int* q_start;     /* [n_seqs + 1] */
+  const int* rows;        /* [n_seqs], or NULL */
+  int n_seqs, total_q;
+} qe_chunks;
+
+typedef struct {
+  const void *k, *v;      /* [total_q][n_kv_heads][head_dim], strides in elements, multiples of 8 */
+  long long k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+  const void* q;          /* [total_q][n_q_heads][head_dim], or NULL: keys and values only */
+  void* q_out;            /* rotated queries; may be q itself */
+  long long q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride;
+  int n_q_heads;
+  const qe_rope* rope;    /* host; NULL: nothing is rotated */
+  const int* positions;   /* [n_axes][total_q] int32, rows pos_stride apart; NULL: the cache position on every axis */
+  long long pos_stride;
+} qe_pages_append_args;
+
+/* Rotate the chunk's queries and keys and write its keys and values to their pages of one
+ * layer.  The pages must be there (qe_pages_resize).  Tokens before position 0 (a chunk longer than its
+ * kv_len) have no place in the cache: their queries are rotated (at position NULL: as position 0) and
+ * their keys dropped.  Rotation is in float32, rounded once to the pool's type. */
+qe_status qe_pages_append(const qe_pages* pages, int layer, const qe_page_table* seqs, const qe_chunks* chunks,
+                          const qe_pages_append_args* args, void* stream);
+
+typedef struct {
+  const void* q;          /* [total_q][n_q_heads][head_dim] of the pool's type */
+  void* out;              /* the same shape and type */
+  float* lse;             /* [total_q][n_q_heads] natural log of the sum of exp(scaled logits), or NULL */
+  long long q_token_stride, q_head_stride, out_token_stride, out_head_stride;   /* elements, multiples of 8 */
+  int n_q_heads;          /* a multiple of n_kv_heads, at most 128 of them per KV head */
+  int causal;             /* 1: query j of a chunk of m sees keys [0, kv_len - m + j]; 0: all kv_len (cross attention) */
+  int max_q_len;          /* the longest chunk, a hint that picks the tile (results are right for any): 0 = unknown */
+  float scale;            /* of the logits, > 0 */
+} qe_pages_attend_args;
+
+/* Attention of a chunk of new tokens over the cached pages of one layer:
+ * out = softmax(scale q K^T + mask) V per query head, over the keys and values of its KV head.  A query that
+ * sees no key gets zeros (and lse = -inf).  Any finite inputs; what lies in the pages behind kv_len may
+ * be anything.  The probabilities meet the values rounded to the pool's type, all sums are float32.
+ * Deterministic for the same lengths.  n_seqs up to 65536. */
+qe_status qe_pages_attend(const qe_pages* pages, int layer, const qe_page_table* seqs, const qe_chunks* chunks,
+                          const qe_pages_attend_args* args, void* workspace, size_t bytes, void* stream);
+qe_status qe_pages_attend_workspace(const qe_pages* pages, size_t* bytes);
+
+/* Set the length of n rows (rows[i] to new_len[i], device int32): pages are taken (the lowest free
+ * ones, in the order of the call) or given back; a length of 0 frees the row.  Where the page that ends up partly
+ * filled is shared, the row gets a copy of its own.  Pages given back are free from the next call on. */
+qe_status qe_pages_resize(const qe_pages* pages, const qe_page_table* seqs, const int* rows, const int* new_len, int n,
+                          void* workspace, size_t bytes, void* stream);
+
+/* Make the empty row dst[i] a copy of row src[i], i < n, sharing all full pages; a last page that is
+ * not full is copied (its used rows, all layers) to the lowest free page.  The same source may
+ * appear many times; all sources are read as they were before the call. */
+qe_status qe_pages_fork(const qe_pages* pages, const qe_page_table* seqs, const int* src, const int* dst, int n,
+                        void* workspace, size_t bytes, void* stream);
+
+/* Move the live pages (refs > 0) together: with n_live of them, each live page of index >= n_live goes
+ * to the free page of index < n_live of the same rank, all layers, and the tables follow.
+ * table_out (rows row_stride apart) and refs_out take the new table and counts; NULL or the old pointers: in place.
+ * n_live: device int32, or NULL.  The moved pages' old places keep their contents until they are used again. */
+qe_status qe_pages_compact(const qe_pages* pages, const qe_page_table* seqs, int* table_out, int* refs_out, int* n_live,
+                           void* workspace, size_t bytes, void* stream);
+
+/* Bytes of workspace that qe_pages_resize / fork (n entries) and qe_pages_compact (n = 0) need. */
+qe_status qe_pages_manage_workspace(const qe_pages* pages, const qe_page_table* seqs, int n, size_t* bytes);
+
+/* Copy page src[i] to page dst[i], i < n (device int32), all layers.  No page may be a destination twice, or both a
+ * source and a destination. */
+qe_status qe_pages_copy(const qe_pages* pages, const int* src, const int* dst, int n, void* stream);
+
+/* Tokens [start, start + n_tokens) of n_seqs rows (rows, or all from row 0 where NULL) of one layer, dense:
+ * k_out, v_out [n_seqs][n_kv_heads][n_tokens][head_dim], the layout qe_append takes.  Tokens behind a row's kv_len
+ * are zeros. */
+qe_status qe_pages_gather(const qe_pages* pages, int layer, const qe_page_table* seqs, const int* rows, int n_seqs,
+                          int start, int n_tokens, void* k_out, void* v_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

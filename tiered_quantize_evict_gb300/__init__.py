@@ -31,6 +31,8 @@ EXPORTED = [
     "qe_get_token_tiers", "qe_get_token_scores", "qe_get_token_counts", "qe_get_token",
     "qe_verify", "qe_verify_commit", "qe_debug_inject", "qe_snapshot_size", "qe_snapshot", "qe_restore",
     "qe_launch_overhead",
+    "qe_pages_append", "qe_pages_attend", "qe_pages_attend_workspace", "qe_pages_resize", "qe_pages_fork",
+    "qe_pages_compact", "qe_pages_manage_workspace", "qe_pages_copy", "qe_pages_gather",
 ]
 QE_DEBUG_FAIL_DEVICE_ALLOC, QE_DEBUG_FAIL_HOST_STORE, QE_DEBUG_EXPIRE_WAIT, QE_DEBUG_VERIFY_PATH = 1, 2, 3, 4
 QE_VERIFY_MAX = 16
@@ -83,6 +85,14 @@ class QEError(RuntimeError):
 _lib: Optional[ctypes.CDLL] = None
 
 
+def __getattr__(name: str):
+    """PagePool, PageTable and Rope (the paged cache) import torch, so they are loaded when first asked for."""
+    if name in ("PagePool", "PageTable", "Rope"):
+        from . import paged
+        return getattr(paged, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
 def load_library() -> ctypes.CDLL:
     """Load libqe.so (raises if it is missing: there is no CPU path)."""
     global _lib
@@ -123,6 +133,15 @@ def load_library() -> ctypes.CDLL:
     "qe_snapshot_size": ([P, ctypes.POINTER(ctypes.c_size_t)], I),
     "qe_snapshot": ([P, P, ctypes.c_size_t], I),
     "qe_restore": ([P, P, ctypes.c_size_t], I),
+        "qe_pages_append": ([P, I, P, P, P, P], I),
+        "qe_pages_attend": ([P, I, P, P, P, P, S, P], I),
+        "qe_pages_attend_workspace": ([P, P], I),
+        "qe_pages_resize": ([P, P, P, P, I, P, S, P], I),
+        "qe_pages_fork": ([P, P, P, P, I, P, S, P], I),
+        "qe_pages_compact": ([P, P, P, P, P, P, S, P], I),
+        "qe_pages_manage_workspace": ([P, P, I, P], I),
+        "qe_pages_copy": ([P, P, P, I, P], I),
+        "qe_pages_gather": ([P, I, P, P, I, I, I, P, P, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)

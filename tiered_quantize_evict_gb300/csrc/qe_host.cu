@@ -20,6 +20,7 @@
 #include "qe.h"
 #include "qe_handle.hpp"
 #include "qe_kernels.cuh"
+#include "qe_pages.cuh"
 
 namespace {
 
@@ -47,6 +48,7 @@ bool inject_alloc_failure() {
   g_fired.store(1);
   return true;
 }
+void set_global_error(const char* msg) { g_init_error = msg; }
 const char* injected_note() { return g_fired.exchange(0) ? " (injected by qe_debug_inject)" : ""; }
 }  // namespace qe
 

@@ -1,0 +1,521 @@
+// qe_pages.cu -- the paged cache's kernels besides attention: appending with rotary positions,
+// resizing, forking and compacting rows, copying pages, gathering rows.
+//
+// All of it moves data (no contraction): each kernel is bound by memory, or by launch latency when small.
+#include <climits>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "qe_common.cuh"
+#include "qe_pages.cuh"
+
+namespace qe {
+
+// ---------------------------------------------------------------------------- append
+template <bool FP16>
+__device__ __forceinline__ float2 pages_unpack(unsigned x) {
+  if constexpr (FP16) {
+    const __half2 h = *reinterpret_cast<const __half2*>(&x);
+    return __half22float2(h);
+  }
+  return make_float2(bf16lo_to_f32(x), bf16hi_to_f32(x));
+}
+template <bool FP16>
+__device__ __forceinline__ unsigned pages_pack(float lo, float hi) {
+  if constexpr (FP16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const unsigned*>(&h);
+  }
+  return pack_bf16x2(lo, hi);
+}
+
+constexpr int APPEND_MAX_TOKENS = 8;
+
+// A block rotates and stores tokens_per_block packed tokens.  The angle of (token, pair) is taken once
+// for all heads: position * turn mod 2^64 is the exact fraction of a turn (64-bit integers wrap at
+// whole turns), whose upper 32 bits, as a signed number of 2^-31 half turns, go to sincospif -- no
+// 64-bit floating point, and no loss at far positions.
+template <bool FP16>
+__global__ void __launch_bounds__(256) pages_append_kernel(const __grid_constant__ PagesAppendParams p) {
+  __shared__ float2 s_cs[APPEND_MAX_TOKENS][64];
+  __shared__ int s_pos[APPEND_MAX_TOKENS];         // cache position, < 0: none; INT_MIN: not a token of the call
+  __shared__ long long s_at[APPEND_MAX_TOKENS];    // offset of head 0 in the pool, < 0: dropped
+  const int t0 = blockIdx.x * p.tokens_per_block;
+  const int nt = min(p.tokens_per_block, p.c.total - t0);
+  if (blockIdx.x == 0) check_starts(p.pg, p.c);
+  if (threadIdx.x < nt) {
+    const int tok = t0 + threadIdx.x;
+    int lo = 0, hi = p.c.n;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (p.c.q_start[mid + 1] <= tok) lo = mid + 1; else hi = mid;
+    }
+    int pos = INT_MIN;
+    long long at = -1;
+    if (lo < p.c.n) {
+      const SeqInfo s = seq_info(p.pg, p.t, p.c, lo, true);
+      if (tok >= s.q0 && tok < s.q0 + s.m) {
+        pos = s.len - s.m + (tok - s.q0);
+        if (pos >= 0 && s.len > 0) {
+          const int page = page_at(p.pg, p.t, s.row, pos);
+          if (page >= 0) at = p.layer * p.pg.ls + page * p.pg.ps + (pos & (p.pg.S - 1)) * p.pg.ts;
+        }
+      }
+    }
+    s_pos[threadIdx.x] = pos;
+    s_at[threadIdx.x] = at;
+  }
+  __syncthreads();
+  const int half = p.R / 2;
+  for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
+    const int t = i / half, c = i - t * half;
+    const long long pos = p.positions ? p.positions[p.axis[c] * p.pos_stride + t0 + t] : max(s_pos[t], 0);
+    const int x = (int)(((unsigned long long)pos * p.turn[c]) >> 32);
+    float sn, cs;
+    sincospif((float)x * 0x1p-31f, &sn, &cs);
+    s_cs[t][c] = make_float2(cs, sn);
+  }
+  __syncthreads();
+  // one item: 8 adjacent channels, or with halves 8 channels of the first half and their partners
+  const int nv = p.halves ? p.R / 16 + (p.pg.D - p.R) / 8 : p.pg.D / 8;
+  const int Hq = p.q ? p.Hq : 0, heads = Hq + 2 * p.pg.H;
+  for (int i = threadIdx.x; i < nt * heads * nv; i += blockDim.x) {
+    const int th = i / nv, t = th / heads, h = th - t * heads;
+    int v = i - th * nv;
+    if (s_pos[t] == INT_MIN) continue;
+    const uint16_t* src;
+    uint16_t* dst;
+    const long long tok = t0 + t;
+    if (h < Hq) {
+      src = p.q + tok * p.qts + h * p.qhs;
+      dst = p.q_out + tok * p.ots + h * p.ohs;
+    } else {
+      if (s_at[t] < 0) continue;
+      const bool key = h < Hq + p.pg.H;
+      const int kh = h - Hq - (key ? 0 : p.pg.H);
+      src = key ? p.k + tok * p.kts + kh * p.khs : p.v + tok * p.vts + kh * p.vhs;
+      dst = (key ? p.pg.k : p.pg.v) + s_at[t] + kh * p.pg.hs;
+    }
+    const bool rot = h < Hq + p.pg.H;
+    const float2* cs = s_cs[t];
+    if (!p.halves) {
+      uint4 x = *reinterpret_cast<const uint4*>(src + v * 8);
+      if (rot) {
+        unsigned* w = &x.x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (v * 4 + k < half) {
+            const float2 a = pages_unpack<FP16>(w[k]), c = cs[v * 4 + k];
+            w[k] = pages_pack<FP16>(a.x * c.x - a.y * c.y, a.x * c.y + a.y * c.x);
+          }
+      }
+      *reinterpret_cast<uint4*>(dst + v * 8) = x;
+    } else if (v < p.R / 16) {
+      uint4 x = *reinterpret_cast<const uint4*>(src + v * 8);
+      uint4 y = *reinterpret_cast<const uint4*>(src + half + v * 8);
+      if (rot) {
+        unsigned *a = &x.x, *b = &y.x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 xa = pages_unpack<FP16>(a[k]), ya = pages_unpack<FP16>(b[k]);
+          const float2 c0 = cs[v * 8 + 2 * k], c1 = cs[v * 8 + 2 * k + 1];
+          a[k] = pages_pack<FP16>(xa.x * c0.x - ya.x * c0.y, xa.y * c1.x - ya.y * c1.y);
+          b[k] = pages_pack<FP16>(xa.x * c0.y + ya.x * c0.x, xa.y * c1.y + ya.y * c1.x);
+        }
+      }
+      *reinterpret_cast<uint4*>(dst + v * 8) = x;
+      *reinterpret_cast<uint4*>(dst + half + v * 8) = y;
+    } else {   // channels behind the rotated ones
+      v = p.R / 8 + (v - p.R / 16);
+      *reinterpret_cast<uint4*>(dst + v * 8) = *reinterpret_cast<const uint4*>(src + v * 8);
+    }
+  }
+}
+
+cudaError_t launch_pages_append(const PagesAppendParams& p0, int fp16, int n_sm, cudaStream_t st) {
+  PagesAppendParams p = p0;
+  // few tokens: a block each, so that they spread over the SMs; many: 8 a block, one table search for 8
+  int tb = p.c.total / (2 * n_sm);
+  tb = tb < 1 ? 1 : (tb > APPEND_MAX_TOKENS ? APPEND_MAX_TOKENS : tb);
+  p.tokens_per_block = tb;
+  const int blocks = (p.c.total + tb - 1) / tb;
+  if (fp16) pages_append_kernel<true><<<blocks, 256, 0, st>>>(p);
+  else pages_append_kernel<false><<<blocks, 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------- planning
+//
+// One block plans a call, so that everything it decides is in one order: which entries are valid, how many
+// pages each needs, and the lowest free pages for them.  The second kernel does the work with all SMs.
+//
+// Workspace: header, row moves [n], owners [n_rows], pages taken [n_pages], pairs [n_pages or n],
+// new places [n_pages].
+struct PlanHeader {
+  int n_pairs;     // pages to copy
+  int go;          // 0: the call changes nothing
+  int n_live;
+  int pad;
+};
+
+struct PlanSpace {
+  PlanHeader* head;
+  PagesRowMove* mv;
+  int* owner;
+  int* taken;
+  PagesPair* pair;
+  int* place;
+};
+static size_t plan_layout(void* ws, int n_pages, int n_rows, int n, PlanSpace* o) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = at;
+    at += (bytes + 15) / 16 * 16;
+    return static_cast<char*>(ws) + r;
+  };
+  PlanSpace s;
+  s.head = reinterpret_cast<PlanHeader*>(take(sizeof(PlanHeader)));
+  s.mv = reinterpret_cast<PagesRowMove*>(take(sizeof(PagesRowMove) * (size_t)n));
+  s.owner = reinterpret_cast<int*>(take(sizeof(int) * (size_t)n_rows));
+  s.taken = reinterpret_cast<int*>(take(sizeof(int) * (size_t)n_pages));
+  s.pair = reinterpret_cast<PagesPair*>(take(sizeof(PagesPair) * (size_t)(n_pages > n ? n_pages : n)));
+  s.place = reinterpret_cast<int*>(take(sizeof(int) * (size_t)n_pages));
+  if (o) *o = s;
+  return at;
+}
+size_t pages_manage_bytes(int n_pages, int n_rows, int n) { return plan_layout(nullptr, n_pages, n_rows, n, nullptr); }
+
+constexpr int PLAN_THREADS = 1024;
+
+// exclusive sum over the block's threads; the block's total through *total
+__device__ __forceinline__ int plan_scan(int x, int* total) {
+  __shared__ int s_w[PLAN_THREADS / 32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int y = x;
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const int z = __shfl_up_sync(~0u, y, k);
+    if (lane >= k) y += z;
+  }
+  if (lane == 31) s_w[w] = y;
+  __syncthreads();
+  int v = s_w[lane];
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const int z = __shfl_up_sync(~0u, v, k);
+    if (lane >= k) v += z;
+  }
+  *total = __shfl_sync(~0u, v, 31);
+  const int before = w ? __shfl_sync(~0u, v, w - 1) : 0;
+  __syncthreads();
+  return before + y - x;
+}
+
+// the `need` lowest free pages, in order, into taken; how many there are
+__device__ int plan_take(const PagesView& pg, const int* refs, int need, int* taken) {
+  int got = 0;
+  for (int b = 0; b < pg.P && got < need; b += PLAN_THREADS) {
+    const int i = b + threadIdx.x;
+    const bool free = i < pg.P && refs[i] == 0;
+    int tot;
+    const int r = plan_scan(free, &tot);
+    if (free && got + r < need) taken[got + r] = i;
+    got += tot;
+  }
+  return got;
+}
+
+// FORK: row a[i] -> row b[i]; else: row a[i] gets length b[i]
+template <bool FORK>
+__global__ void __launch_bounds__(PLAN_THREADS) pages_plan_kernel(const PagesView pg, const TableView t, const int* a, const int* b,
+                                                                  int n, const PlanSpace ws) {
+  const long long most = (long long)t.cols << pg.lgS;
+  const int tid = threadIdx.x;
+  for (int i = tid; i < n; i += PLAN_THREADS) {
+    const int row = FORK ? b[i] : a[i];
+    if (row >= 0 && row < t.rows) ws.owner[row] = INT_MAX;
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += PLAN_THREADS) {
+    const int row = FORK ? b[i] : a[i];
+    if (row >= 0 && row < t.rows) atomicMin(&ws.owner[row], i);
+  }
+  __syncthreads();
+  int need = 0, pairs = 0;
+  for (int base = 0; base < n; base += PLAN_THREADS) {
+    const int i = base + tid;
+    PagesRowMove m{-1, -1, 0, 0, 0, -1};
+    int want = 0, copy = 0, from = -1, used = 0;
+    if (i < n) {
+      const int row = FORK ? b[i] : a[i], src = FORK ? a[i] : row;
+      bool ok = row >= 0 && row < t.rows && src >= 0 && src < t.rows && ws.owner[row] == i;
+      if (ok) {
+        const int old_len = t.kv_len[row], len = FORK ? t.kv_len[src] : b[i];
+        ok = old_len >= 0 && old_len <= most && len >= 0 && len <= most && !(FORK && old_len != 0);
+        if (ok) {
+          m.row = row;
+          m.src = FORK ? src : -1;
+          m.old_len = old_len;
+          m.new_len = len;
+          // the page that ends up partly filled (fork), or was or becomes so (resize) and must be the row's own
+          const int edge = FORK ? len : min(old_len, len);
+          used = edge & (pg.S - 1);
+          if (used && (FORK || old_len != len)) {
+            from = page_at(pg, t, src, edge);
+            copy = from >= 0 && (FORK || t.refs[from] > 1);
+          }
+          if (!FORK) want = max(0, (int)(((long long)len + pg.S - 1) >> pg.lgS) - (int)(((long long)old_len + pg.S - 1) >> pg.lgS));
+        }
+      }
+      if (!ok) pages_report(pg, QE_PAGES_ERR_ROW);
+    }
+    int tot, ptot;
+    const int at = need + plan_scan(want + copy, &tot);
+    const int pr = pairs + plan_scan(copy, &ptot);
+    if (i < n) {
+      m.first_new = at + copy;
+      m.copy_page = copy ? at : -1;   // an index into the pages taken until they are known
+      ws.mv[i] = m;
+      if (copy) ws.pair[pr] = PagesPair{from, at, used, 0};
+    }
+    need += tot;
+    pairs += ptot;
+  }
+  const int got = plan_take(pg, t.refs, need, ws.taken);
+  __syncthreads();
+  const bool go = got >= need;
+  if (go) {
+    for (int i = tid; i < n; i += PLAN_THREADS)
+      if (ws.mv[i].copy_page >= 0) ws.mv[i].copy_page = ws.taken[ws.mv[i].copy_page];
+    for (int i = tid; i < pairs; i += PLAN_THREADS) ws.pair[i].dst = ws.taken[ws.pair[i].dst];
+  }
+  if (tid == 0) {
+    *ws.head = PlanHeader{go ? pairs : 0, go, 0, 0};
+    if (!go) pages_report(pg, QE_PAGES_ERR_NO_PAGES);
+  }
+}
+
+__device__ __forceinline__ void ref_down(const PagesView& pg, int* refs, int page) {
+  if (page < 0 || page >= pg.P) {
+    pages_report(pg, QE_PAGES_ERR_PAGE);
+    return;
+  }
+  if (atomicSub(&refs[page], 1) <= 0) {   // more references given up than counted
+    atomicAdd(&refs[page], 1);
+    pages_report(pg, QE_PAGES_ERR_PAGE);
+  }
+}
+
+// Copies of whole or partly used pages: a unit is one head of one page of one layer, of the keys or the values.
+__device__ void copy_pairs(const PagesView& pg, const PagesPair* pair, const int* src, const int* dst, int n, unsigned bid,
+                           unsigned blocks) {
+  const int vpr = pg.D / 8;
+  const long long units = (long long)n * pg.L * 2 * pg.H;
+  for (long long u = bid; u < units; u += blocks) {
+    const int h = (int)(u % pg.H);
+    long long r = u / pg.H;
+    const int kv = (int)(r & 1);
+    r >>= 1;
+    const int l = (int)(r % pg.L), i = (int)(r / pg.L);
+    const int s = pair ? pair[i].src : src[i], d = pair ? pair[i].dst : dst[i], rows = pair ? pair[i].rows : pg.S;
+    if (s < 0 || s >= pg.P || d < 0 || d >= pg.P) {
+      if (threadIdx.x == 0) pages_report(pg, QE_PAGES_ERR_PAGE);
+      continue;
+    }
+    if (s == d) continue;
+    uint16_t* base = (kv ? pg.v : pg.k) + l * pg.ls + h * pg.hs;
+    const uint16_t* from = base + s * pg.ps;
+    uint16_t* to = base + d * pg.ps;
+    for (int v = threadIdx.x; v < rows * vpr; v += blockDim.x) {
+      const int tk = v / vpr, c = (v - tk * vpr) * 8;
+      *reinterpret_cast<uint4*>(to + tk * pg.ts + c) = *reinterpret_cast<const uint4*>(from + tk * pg.ts + c);
+    }
+  }
+}
+
+// The work of a planned resize or fork: table entries, reference counts, lengths, page copies.
+template <bool FORK>
+__global__ void __launch_bounds__(256) pages_apply_kernel(const PagesView pg, const TableView t, int n, const PlanSpace ws) {
+  const PlanHeader head = *ws.head;
+  if (!head.go) return;
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const PagesRowMove m = ws.mv[i];
+    if (m.row < 0) continue;
+    int* row = t.table + (long long)m.row * t.stride;
+    const int oldp = (int)(((long long)m.old_len + pg.S - 1) >> pg.lgS), newp = (int)(((long long)m.new_len + pg.S - 1) >> pg.lgS);
+    if (FORK) {
+      const int* from = t.table + (long long)m.src * t.stride;
+      const int full = m.new_len >> pg.lgS;
+      for (int j = threadIdx.x; j < t.cols; j += blockDim.x) {
+        int e = -1;
+        if (j < full) {
+          e = from[j];
+          if (e >= 0 && e < pg.P) atomicAdd(&t.refs[e], 1);
+          else {
+            e = -1;
+            pages_report(pg, QE_PAGES_ERR_PAGE);
+          }
+        } else if (j < newp && m.copy_page >= 0) {
+          e = m.copy_page;
+          t.refs[e] = 1;
+        }
+        row[j] = e;
+      }
+    } else {
+      const int edge = min(m.old_len, m.new_len) >> pg.lgS;
+      if (threadIdx.x == 0 && m.copy_page >= 0) {
+        ref_down(pg, t.refs, row[edge]);
+        row[edge] = m.copy_page;
+        t.refs[m.copy_page] = 1;
+      }
+      for (int j = min(oldp, newp) + threadIdx.x; j < max(oldp, newp); j += blockDim.x) {
+        if (j >= oldp) {
+          const int e = ws.taken[m.first_new + j - oldp];
+          row[j] = e;
+          t.refs[e] = 1;
+        } else {
+          ref_down(pg, t.refs, row[j]);
+          row[j] = -1;
+        }
+      }
+    }
+    if (threadIdx.x == 0) t.kv_len[m.row] = m.new_len;
+  }
+  copy_pairs(pg, ws.pair, nullptr, nullptr, head.n_pairs, blockIdx.x, gridDim.x);
+}
+
+template <bool FORK>
+static cudaError_t launch_planned(const PagesView& pg, const TableView& t, const int* a, const int* b, int n, void* ws, int n_sm,
+                                  cudaStream_t st) {
+  PlanSpace s;
+  plan_layout(ws, pg.P, t.rows, n, &s);
+  pages_plan_kernel<FORK><<<1, PLAN_THREADS, 0, st>>>(pg, t, a, b, n, s);
+  pages_apply_kernel<FORK><<<n_sm * 8, 256, 0, st>>>(pg, t, n, s);
+  return cudaGetLastError();
+}
+cudaError_t launch_pages_resize(const PagesView& pg, const TableView& t, const int* rows, const int* new_len, int n, void* ws,
+                                int n_sm, cudaStream_t st) {
+  return launch_planned<false>(pg, t, rows, new_len, n, ws, n_sm, st);
+}
+cudaError_t launch_pages_fork(const PagesView& pg, const TableView& t, const int* src, const int* dst, int n, void* ws, int n_sm,
+                              cudaStream_t st) {
+  return launch_planned<true>(pg, t, src, dst, n, ws, n_sm, st);
+}
+
+// ---------------------------------------------------------------------------- compact
+__global__ void __launch_bounds__(PLAN_THREADS) pages_plan_compact_kernel(const PagesView pg, const TableView t, const PlanSpace ws,
+                                                                          int* n_live_out) {
+  const int tid = threadIdx.x;
+  int live = 0;
+  for (int i = tid; i < pg.P; i += PLAN_THREADS) live += t.refs[i] > 0;
+  int n_live;
+  plan_scan(live, &n_live);
+  int holes = 0, movers = 0;
+  for (int base = 0; base < pg.P; base += PLAN_THREADS) {
+    const int i = base + tid;
+    const int r = i < pg.P ? t.refs[i] : 0;
+    const bool hole = i < n_live && r <= 0, mover = i >= n_live && r > 0;
+    int th, tm;
+    const int h = holes + plan_scan(hole, &th), m = movers + plan_scan(mover, &tm);
+    if (hole) ws.taken[h] = i;
+    if (mover) {
+      ws.place[i] = m;   // its rank until the holes are all known
+      ws.pair[m].src = i;
+      ws.pair[m].rows = pg.S;
+      ws.pair[m].refs = r;
+    } else if (i < pg.P) {
+      ws.place[i] = r > 0 ? i : -1;
+    }
+    holes += th;
+    movers += tm;
+  }
+  __syncthreads();
+  for (int i = tid; i < movers; i += PLAN_THREADS) {   // as many holes as movers
+    const int d = ws.taken[i];
+    ws.pair[i].dst = d;
+    ws.place[ws.pair[i].src] = d;
+  }
+  if (tid == 0) {
+    *ws.head = PlanHeader{movers, 1, n_live, 0};
+    if (n_live_out) *n_live_out = n_live;
+  }
+}
+
+__global__ void __launch_bounds__(256) pages_compact_kernel(const PagesView pg, const TableView t, const PlanSpace ws, int* table_out,
+                                                            int* refs_out) {
+  const PlanHeader head = *ws.head;
+  const long long nt = (long long)gridDim.x * blockDim.x, id = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  for (long long i = id; i < (long long)t.rows * t.cols; i += nt) {
+    const long long r = i / t.cols, at = r * t.stride + (i - r * t.cols);
+    const int e = t.table[at];
+    int to = e;
+    if (e >= 0) {
+      to = e < pg.P ? ws.place[e] : -1;
+      if (to < 0) {   // an entry that names no live page
+        pages_report(pg, QE_PAGES_ERR_PAGE);
+        to = -1;
+      }
+    }
+    table_out[at] = to;
+  }
+  for (long long i = id; i < pg.P; i += nt) {
+    if (i >= head.n_live) refs_out[i] = 0;
+    else if (ws.place[i] == (int)i) refs_out[i] = t.refs[i];
+  }
+  for (long long i = id; i < head.n_pairs; i += nt) refs_out[ws.pair[i].dst] = ws.pair[i].refs;
+  copy_pairs(pg, ws.pair, nullptr, nullptr, head.n_pairs, blockIdx.x, gridDim.x);
+}
+
+cudaError_t launch_pages_compact(const PagesView& pg, const TableView& t, int* table_out, int* refs_out, int* n_live, void* ws,
+                                 int n_sm, cudaStream_t st) {
+  PlanSpace s;
+  plan_layout(ws, pg.P, t.rows, 0, &s);
+  pages_plan_compact_kernel<<<1, PLAN_THREADS, 0, st>>>(pg, t, s, n_live);
+  pages_compact_kernel<<<n_sm * 8, 256, 0, st>>>(pg, t, s, table_out, refs_out);
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------- copy, gather
+__global__ void __launch_bounds__(256) pages_copy_kernel(const PagesView pg, const int* src, const int* dst, int n) {
+  copy_pairs(pg, nullptr, src, dst, n, blockIdx.x, gridDim.x);
+}
+cudaError_t launch_pages_copy(const PagesView& pg, const int* src, const int* dst, int n, int n_sm, cudaStream_t st) {
+  const long long units = (long long)n * pg.L * 2 * pg.H;
+  const int blocks = (int)(units < n_sm * 8 ? units : n_sm * 8);
+  pages_copy_kernel<<<blocks, 256, 0, st>>>(pg, src, dst, n);
+  return cudaGetLastError();
+}
+
+// a unit is one head of one page's worth of tokens of one row, of the keys or the values
+__global__ void __launch_bounds__(256) pages_gather_kernel(const PagesView pg, const TableView t, int layer, const int* rows, int n,
+                                                           int start, int n_tok, uint16_t* k, uint16_t* v) {
+  const int first = start >> pg.lgS, last = (start + n_tok - 1) >> pg.lgS, np = last - first + 1, vpr = pg.D / 8;
+  const long long units = (long long)n * np * 2 * pg.H;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const int h = (int)(u % pg.H);
+    long long r = u / pg.H;
+    const int kv = (int)(r & 1);
+    r >>= 1;
+    const int j = first + (int)(r % np), s = (int)(r / np);
+    const int row = rows ? rows[s] : s;
+    const int len = row_len(pg, t, row, threadIdx.x == 0);
+    const int p0 = j << pg.lgS;
+    const int page = p0 < len ? page_at(pg, t, row, p0) : -1;
+    const uint16_t* from = (kv ? pg.v : pg.k) + layer * pg.ls + (long long)max(page, 0) * pg.ps + h * pg.hs;
+    uint16_t* to = (kv ? v : k) + ((long long)s * pg.H + h) * n_tok * pg.D;
+    for (int i = threadIdx.x; i < pg.S * vpr; i += blockDim.x) {
+      const int tk = i / vpr, c = (i - tk * vpr) * 8, pos = p0 + tk;
+      if (pos < start || pos >= start + n_tok) continue;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (page >= 0 && pos < len) x = *reinterpret_cast<const uint4*>(from + tk * pg.ts + c);
+      *reinterpret_cast<uint4*>(to + (long long)(pos - start) * pg.D + c) = x;
+    }
+  }
+}
+cudaError_t launch_pages_gather(const PagesView& pg, const TableView& t, int layer, const int* rows, int n, int start, int n_tok,
+                                uint16_t* k, uint16_t* v, int n_sm, cudaStream_t st) {
+  pages_gather_kernel<<<n_sm * 8, 256, 0, st>>>(pg, t, layer, rows, n, start, n_tok, k, v);
+  return cudaGetLastError();
+}
+
+}  // namespace qe
