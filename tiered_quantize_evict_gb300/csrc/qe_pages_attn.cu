@@ -1,82 +1,911 @@
-// qe_pages_attn.cu -- attention of a chunk of new tokens over the cached pages.
+// qe_pages_attn.cu -- attention of a chunk of new tokens over the cached pages, on the 5th-generation
+// tensor cores (tcgen05.mma, operands by TMA, accumulators and probabilities in tensor memory).
 //
-// For query row (token t of a chunk of m, head h) with V visible keys (causal: kv_len - m + j + 1):
-//   out = sum_i exp(s_i - M) v_i / sum_i exp(s_i - M),  s_i = scale q . k_i,  M = max s_i,
-// in one pass over the keys with a running maximum, sum and accumulator in float32.
+// For the row of token t (of a chunk of m) and query head h, with V visible keys (causal: kv_len - m + t + 1):
+//   out = sum_i 2^(x_i - M) v_i / sum_i 2^(x_i - M),   x_i = scale log2(e) q . k_i,
+// in one pass over the keys in blocks of 128 with a running reference M, sum and accumulator in float32.
+//
+// Tiles.  A tile is NH halves of 128 rows: T tokens x the G query heads of one KV head per half (row t G + g,
+// T = floor(128 / G)), so a block's keys and values are read once for all of them.  NH = 2 for chunks: while one half's
+// softmax runs, the other half's products keep the tensor cores busy.  NH = 1 for a few rows (decode, drafts): bound by
+// the memory the cache is read from, so one half and the S buffers of both to run ahead.
+//
+// Split.  All (tile, block) pairs of the call form one line, cut into equal pieces, one per CTA (one CTA per SM): long
+// caches with few rows are split along the keys, prompts are balanced whatever their causal shape.  A tile inside a piece is
+// finished by its CTA; one that is cut leaves (M, sum, accumulator) parts that the join kernel merges.  The line is computed
+// from the lengths on the device by every CTA alike (a sum of floors in closed form per sequence).
+//
+// CTA: 12 warps.  Warps 0-3 and 4-7: softmax of half 0 and 1, a thread per row (with NH = 1 the second four idle).
+// Warp 8: TMA of keys and values, page by page, into a ring of slots.  Warp 9: tensor-core issue.  Warp 10: TMA of the
+// queries.  Warp 11: tensor memory.
+//  * S = Q K^T (M 128, N 128): both operands in shared memory, 128-byte swizzle, K-major.
+//  * P overwrites its S in tensor memory in the pool's type; O += P V (N = head_dim) takes P from there and V as the
+//    MN-major operand (its rows are tokens).
+//  * The reference M is raised only when a row's maximum passes it by 2^8 (then the softmax warps rescale O in tensor
+//    memory); up to that P and the sums are larger than 1, exactly as precise.
+//  * P is rounded to the pool's type (the tensor cores' operand): a relative 2^-9 (bf16), 2^-12 (fp16) per probability at
+//    most half a step, as the result itself is; the sum is of the unrounded ones.
+// mbarriers: kfull / kempty per slot, qfull / qempty per query buffer, s[i] (S i complete; tensor-core commit),
+// p[i] (P i written; one arrival per softmax warp), o[h] (the P V before it complete).  Every wait is bounded (0.2 s); one that expires sets
+// QE_PAGES_ERR_TIMEOUT and an abort flag that ends all loops, and the CTA leaves after what it issued has landed.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <atomic>
 
 #include "qe_common.cuh"
 #include "qe_pages.cuh"
 
 namespace qe {
 
-template <bool FP16>
-__device__ __forceinline__ float pages_to_f(uint16_t x) {
-  if constexpr (FP16) return __half2float(__ushort_as_half(x));
-  return __uint_as_float((unsigned)x << 16);
-}
-template <bool FP16>
-__device__ __forceinline__ uint16_t pages_from_f(float x) {
-  if constexpr (FP16) return __half_as_ushort(__float2half_rn(x));
-  return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+constexpr int PA_THREADS = 384;
+constexpr int PA_BN = 128;                       // keys of a block
+constexpr unsigned long long PA_WAIT_NS = 200000000ull;
+constexpr float PA_LAZY = 8.f;                   // log2 of how far a row's maximum may pass its reference
+
+template <int D>
+struct PaShape {
+  static constexpr int CB = D / 64;              // column blocks of 128 bytes
+  static constexpr int TILE = 128 * D * 2;       // a query buffer, or a slot: 128 rows
+  static constexpr int SLOTS = (7 * 32768 - 2 * TILE) / TILE;
+  static constexpr int SMEM = (2 + SLOTS) * TILE + 1024;
+  static constexpr int TM_O = 256;               // tensor memory: S0 at column 0, S1 at 128, O0 here, O1 at + D
+};
+
+// what a CTA's piece of the line starts with (read by the join kernel)
+struct PaRec {
+  long long begin;     // place of the tile's first block on the line
+  long long total;     // length of the line
+  int pieces;          // CTAs that have a piece
+  int nb, b;           // blocks of the tile, and the one the piece starts with
+  int tok, ntok;       // the tile's first packed token, and how many
+  int kvh;
+};
+
+struct PaParams {
+  PagesView pg;
+  TableView t;
+  ChunksView c;
+  uint16_t* out;
+  float* lse;
+  long long ots, ohs;
+  int Hq, G, T, causal, min_blocks;
+  float scale, scale2;     // of the logits; and times log2(e)
+  PaRec* rec;              // [CTAs]
+  float2* part_ml;         // [CTAs][2][NH][128]: reference, sum
+  float* part_o;           // [CTAs][2][NH][128][D]
+};
+
+// ---------------------------------------------------------------------------- the line of blocks
+
+// sum over i < n of floor((a i + b) / 128): Euclid's recursion on (128, a)
+__device__ inline unsigned long long floor_sum128(unsigned long long n, unsigned long long a, unsigned long long b) {
+  unsigned long long m = 128, ans = 0;
+  if (n == 0) return 0;
+  while (true) {
+    if (a >= m) {
+      ans += n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      ans += n * (b / m);
+      b %= m;
+    }
+    const unsigned long long y = a * n + b;
+    if (y < m) return ans;
+    n = y / m;
+    b = y % m;
+    const unsigned long long z = m;
+    m = a;
+    a = z;
+  }
 }
 
-// One warp per (packed token, query head); lane l holds channels l, l + 32, ...
-template <int D, bool FP16>
-__global__ void __launch_bounds__(256) pages_attend_kernel(const PagesAttendParams p) {
-  constexpr int E = D / 32;
-  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int tok = (int)(w / p.Hq), h = (int)(w - (long long)tok * p.Hq);
-  if (blockIdx.x == 0) check_starts(p.pg, p.c);
-  if (tok >= p.c.total) return;
-  int lo = 0, hi = p.c.n;   // the sequence whose packed tokens hold tok
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (p.c.q_start[mid + 1] <= tok) lo = mid + 1; else hi = mid;
-  }
-  if (lo >= p.c.n) return;
-  const SeqInfo s = seq_info(p.pg, p.t, p.c, lo, lane == 0);
-  if (tok < s.q0 || tok >= s.q0 + s.m) return;
-  const int vis = p.causal ? max(0, s.len - s.m + (tok - s.q0) + 1) : s.len;
-  const int kvh = h / (p.Hq / p.pg.H);
-  float q[E], o[E] = {};
-#pragma unroll
-  for (int e = 0; e < E; ++e) q[e] = pages_to_f<FP16>(p.q[tok * p.qts + h * p.qhs + e * 32 + lane]) * p.scale;
-  float m = -INFINITY, l = 0.f;
-  int page = -1;
-  for (int i = 0; i < vis; ++i) {
-    if ((i & (p.pg.S - 1)) == 0) page = page_at(p.pg, p.t, s.row, i);
-    const long long at = p.layer * p.pg.ls + max(page, 0) * p.pg.ps + kvh * p.pg.hs + (i & (p.pg.S - 1)) * p.pg.ts;
-    float dot = 0.f;
-    if (page >= 0)
-#pragma unroll
-      for (int e = 0; e < E; ++e) dot += q[e] * pages_to_f<FP16>(p.pg.k[at + e * 32 + lane]);
-#pragma unroll
-    for (int k = 16; k; k >>= 1) dot += __shfl_xor_sync(~0u, dot, k);
-    const float mn = fmaxf(m, dot), f = __expf(m - mn), pr = __expf(dot - mn);
-    m = mn;
-    l = l * f + pr;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + (page >= 0 ? pr * pages_to_f<FP16>(p.pg.v[at + e * 32 + lane]) : 0.f);
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int e = 0; e < E; ++e) p.out[tok * p.ots + h * p.ohs + e * 32 + lane] = pages_from_f<FP16>(o[e] * inv);
-  if (p.lse && lane == 0) p.lse[(long long)tok * p.Hq + h] = l == 0.f ? -INFINITY : m + logf(l);
+struct PaSeq {
+  SeqInfo s;
+  int tiles;
+};
+template <int NH>
+__device__ __forceinline__ PaSeq pa_seq(const PaParams& p, int i, bool report) {
+  PaSeq r;
+  r.s = seq_info(p.pg, p.t, p.c, i, report);
+  const int tt = NH * p.T;
+  r.tiles = (r.s.m + tt - 1) / tt;
+  return r;
+}
+// blocks of tile j (at least one, so that rows without keys are written too)
+template <int NH>
+__device__ __forceinline__ int pa_blocks(const PaParams& p, const SeqInfo& s, int j) {
+  const int end = p.causal ? s.len - s.m + min(s.m, (j + 1) * NH * p.T) : s.len;
+  return max(1, (end + PA_BN - 1) >> 7);
+}
+// blocks of the tiles before tile j (j < tiles: those are all whole)
+template <int NH>
+__device__ __forceinline__ long long pa_before(const PaParams& p, const SeqInfo& s, int j) {
+  if (!p.causal || j == 0) return (long long)j * max(1, (s.len + PA_BN - 1) >> 7);
+  const int tt = NH * p.T, off = s.len - s.m;
+  const int none = off < 0 ? min(j, -off / tt) : 0;   // tiles that see no key
+  return none + (long long)floor_sum128(j - none, tt, (long long)off + (long long)(none + 1) * tt + PA_BN - 1);
+}
+template <int NH>
+__device__ __forceinline__ long long pa_head_blocks(const PaParams& p, const PaSeq& q) {
+  return q.tiles == 0 ? 0 : pa_before<NH>(p, q.s, q.tiles - 1) + pa_blocks<NH>(p, q.s, q.tiles - 1);
 }
 
-cudaError_t launch_pages_attend(const PagesAttendParams& p, int fp16, cudaStream_t st) {
-  const long long blocks = ((long long)p.c.total * p.Hq + 7) / 8;
-  if (p.pg.D == 128) {
-    if (fp16) pages_attend_kernel<128, true><<<(unsigned)blocks, 256, 0, st>>>(p);
-    else pages_attend_kernel<128, false><<<(unsigned)blocks, 256, 0, st>>>(p);
+// A place on the line.
+template <int NH>
+struct PaCursor {
+  int i, h, j, b, nb;   // sequence, KV head, tile, block; blocks of the tile
+  PaSeq q;
+  __device__ __forceinline__ void set(const PaParams& p, int i_, int h_, int j_, int b_) {
+    i = i_;
+    h = h_;
+    j = j_;
+    b = b_;
+    q = pa_seq<NH>(p, i, false);
+    nb = pa_blocks<NH>(p, q.s, j);
+  }
+  __device__ __forceinline__ void next_tile(const PaParams& p) {
+    b = 0;
+    if (++j >= q.tiles) {
+      j = 0;
+      if (++h >= p.pg.H) {
+        h = 0;
+        do {
+          if (++i >= p.c.n) return;   // the end of the line
+          q = pa_seq<NH>(p, i, false);
+        } while (q.tiles == 0);
+      }
+    }
+    nb = pa_blocks<NH>(p, q.s, j);
+  }
+  __device__ __forceinline__ void next(const PaParams& p) {
+    if (++b >= nb) next_tile(p);
+  }
+  __device__ __forceinline__ bool second_half(const PaParams& p) const { return NH == 2 && j * 2 * p.T + p.T < q.s.m; }
+};
+
+struct PaStart {
+  int i, h, j, b;
+  int n;              // blocks of the piece
+};
+
+// Every CTA finds its piece: sums the sequences' blocks, cuts the line, finds the tile its cut falls in.
+template <int NH>
+__device__ void pa_find(const PaParams& p, PaStart* out, long long* s_w, long long* s_rem) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int W = PA_THREADS / 32;
+  const int c = blockIdx.x;
+  // exclusive prefix of x over the block, and the total
+  auto scan = [&](long long x, long long& total) {
+    long long y = x;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const long long z = __shfl_up_sync(~0u, y, k);
+      if (lane >= k) y += z;
+    }
+    if (lane == 31) s_w[warp] = y;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const long long z = s_w[k];
+      if (k < warp) before += z;
+      all += z;
+    }
+    total = all;
+    __syncthreads();
+    return before + y - x;
+  };
+  if (tid == 0) out->n = 0;
+  long long line = 0, first_pre = 0, first_x = 0;
+  for (int base = 0; base < p.c.n; base += PA_THREADS) {
+    const int i = base + tid;
+    const long long x = i < p.c.n ? pa_head_blocks<NH>(p, pa_seq<NH>(p, i, c == 0)) * p.pg.H : 0;
+    long long tot;
+    const long long pre = scan(x, tot);
+    if (base == 0) {
+      first_pre = pre;
+      first_x = x;
+    }
+    line += tot;
+  }
+  long long pieces = line / p.min_blocks;
+  pieces = pieces < 1 ? 1 : (pieces > gridDim.x ? gridDim.x : pieces);
+  const long long p0 = line * c / pieces, p1 = line * (c + 1) / pieces;
+  if (c >= pieces || line == 0) {
+    if (tid == 0) p.rec[c] = PaRec{0, 0, 0, 0, 0, 0, 0, 0};
+    __syncthreads();
+    return;
+  }
+  long long at = 0;
+  for (int base = 0; base < p.c.n; base += PA_THREADS) {
+    const int i = base + tid;
+    long long pre = first_pre, x = first_x;
+    if (base > 0) {
+      x = i < p.c.n ? pa_head_blocks<NH>(p, pa_seq<NH>(p, i, false)) * p.pg.H : 0;
+      long long tot;
+      pre = at + scan(x, tot);
+      at += tot;
+    } else if (p.c.n > PA_THREADS) {
+      long long tot;
+      scan(x, tot);
+      at = tot;
+    }
+    if (p0 >= pre && p0 < pre + x) {
+      out->i = i;
+      out->n = (int)(p1 - p0);
+      *s_rem = p0 - pre;
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int i = out->i;
+    const PaSeq q = pa_seq<NH>(p, i, false);
+    const long long head = pa_head_blocks<NH>(p, q);
+    long long rem = *s_rem;
+    const int h = (int)(rem / head);
+    rem -= h * head;
+    int lo = 0, hi = q.tiles;   // the last tile that begins at or before rem: 32 places a round
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, cand = lo + lane * step;
+      const bool le = cand < hi && pa_before<NH>(p, q.s, cand) <= rem;
+      const int top = 31 - __clz(__ballot_sync(~0u, le));
+      lo += top * step;
+      hi = min(hi, lo + step);
+    }
+    const int b = (int)(rem - pa_before<NH>(p, q.s, lo));
+    if (lane == 0) {
+      out->h = h;
+      out->j = lo;
+      out->b = b;
+      const int tt = NH * p.T;
+      p.rec[c] = PaRec{p0 - b, line, (int)pieces, pa_blocks<NH>(p, q.s, lo), b, q.s.q0 + lo * tt, min(tt, q.s.m - lo * tt), h};
+    }
+  }
+  __syncthreads();
+}
+
+// ---------------------------------------------------------------------------- instructions
+
+__device__ __forceinline__ void pa_mma_ss(unsigned d, unsigned long long a, unsigned long long b, unsigned idesc, bool acc) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0)
+      : "memory");
+}
+__device__ __forceinline__ void pa_mma_ts(unsigned d, unsigned a, unsigned long long b, unsigned idesc, bool acc) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0)
+      : "memory");
+}
+__device__ __forceinline__ void pa_commit(unsigned bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void pa_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void pa_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void pa_arrive(unsigned bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void pa_tma4(unsigned dst, const CUtensorMap* map, int x, int y, int z, int w, unsigned bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void pa_tma3(unsigned dst, const CUtensorMap* map, int x, int y, int z, unsigned bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// 32 float32 columns of this thread's tensor-memory lane; pa_wait_ld before their use
+__device__ __forceinline__ void pa_ld32(unsigned t, unsigned* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+      "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void pa_st32(unsigned t, const unsigned* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+      "%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+      "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void pa_st16(unsigned t, const unsigned* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t), "r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// waits for this thread's tensor-memory loads; the registers pass through empty asm, so no use moves before it
+template <int N>
+__device__ __forceinline__ void pa_wait_ld(unsigned* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+__device__ __forceinline__ void pa_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+struct PaWait {
+  const PagesView* pg;
+  volatile int* abort;
+  // Bounded wait for the phase; false when it expired or the CTA is leaving.
+  __device__ __forceinline__ bool operator()(unsigned bar, unsigned parity) const {
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+      if (*abort) return false;
+      if (globaltimer_ns() - t0 > PA_WAIT_NS) {
+        pages_report(*pg, QE_PAGES_ERR_TIMEOUT);
+        *abort = 1;
+        return false;
+      }
+    }
+    return true;
+  }
+  // the same on the way out, for what has been issued
+  __device__ __forceinline__ void drain(unsigned bar, unsigned parity) const {
+    const unsigned long long t0 = globaltimer_ns();
+    while (!mbar_try_wait_sleep(bar, parity, 20000u))
+      if (globaltimer_ns() - t0 > PA_WAIT_NS) return;
+  }
+};
+
+template <bool FP16>
+__device__ __forceinline__ unsigned pa_pack(float lo, float hi) {
+  unsigned d;
+  if constexpr (FP16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// shared-memory descriptors: 128-byte swizzle, 8-row groups 1024 bytes apart.  K-major operands (Q, K); and V with
+// channels as the rows of the operand (MN-major: 64 channels to a column block, blocks 128 tokens x 128 bytes apart).
+constexpr unsigned long long PA_DESC_K = (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+constexpr unsigned long long PA_DESC_V = (1024ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+
+// ---------------------------------------------------------------------------- the kernel
+
+template <int D, int NH, bool FP16>
+__global__ void __launch_bounds__(PA_THREADS, 1)
+    pages_attend_kernel(const __grid_constant__ PaParams p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                        const __grid_constant__ CUtensorMap mv) {
+  using Sh = PaShape<D>;
+  constexpr int NS = Sh::SLOTS;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) unsigned long long b_kfull[NS], b_kempty[NS], b_qfull[2], b_qempty[2], b_s[2], b_p[2], b_o[2], b_end;
+  __shared__ unsigned s_tmem;
+  __shared__ int s_abort;
+  __shared__ PaStart s_start;
+  __shared__ long long s_w[PA_THREADS / 32], s_rem;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const unsigned sm = (smem_u32(smem_raw) + 1023) & ~1023u;
+  const unsigned sm_q = sm, sm_kv = sm + 2 * Sh::TILE;
+  const PaWait wait{&p.pg, &s_abort};
+
+  griddep_launch_dependents();
+  if (warp == 11) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(smem_u32(&b_kfull[i]), 1);
+      mbar_init(smem_u32(&b_kempty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&b_qfull[i]), 1);
+      mbar_init(smem_u32(&b_qempty[i]), 1);
+      mbar_init(smem_u32(&b_s[i]), 1);
+      mbar_init(smem_u32(&b_p[i]), 4);
+      mbar_init(smem_u32(&b_o[i]), 1);
+    }
+    mbar_init(smem_u32(&b_end), 1);
+    mbar_fence_init();
+    s_abort = 0;
+  }
+  pa_fence_before();
+  griddep_wait();
+  pa_find<NH>(p, &s_start, s_w, &s_rem);   // ends with a barrier
+  pa_fence_after();
+  const unsigned tm = s_tmem;
+  const int N = s_start.n;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (N > 0 && warp == 8) {
+      // ============================== keys and values
+      PaCursor<NH> cur;
+      cur.set(p, s_start.i, s_start.h, s_start.j, s_start.b);
+      const int rows = min(p.pg.S, PA_BN);               // tokens of a piece: a page, or a block's part of one
+      const int np = PA_BN / rows;
+      const int piece = lane % np, cb = lane / np;       // lane -> (page of the block, column block)
+      const bool mine = cb < Sh::CB;
+      // page of this lane's piece, or n_pages (out of the pool: the copy fills zeros) where there is none
+      auto page_of = [&]() {
+        const int key = cur.b * PA_BN + piece * rows;
+        if (key >= cur.q.s.len) return p.pg.P;
+        const int g = page_at(p.pg, p.t, cur.q.s.row, key);
+        return g < 0 ? p.pg.P : g;
+      };
+      int slot = 0, ph = 1, issued = 0;
+      int page = page_of();
+      bool ok = true;
+      for (int n = 0; n < N && ok; ++n) {
+        const int tk = (cur.b * PA_BN) & (p.pg.S - 1), h = cur.h, now = page;
+        cur.next(p);
+        if (n + 1 < N) page = page_of();
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          ok = ok && wait(smem_u32(&b_kempty[slot]), ph);
+          if (!__all_sync(~0u, ok)) {
+            ok = false;
+            break;
+          }
+          const unsigned full = smem_u32(&b_kfull[slot]);
+          if (lane == 0) mbar_expect_tx(full, Sh::TILE);
+          __syncwarp();
+          if (mine) pa_tma4(sm_kv + slot * Sh::TILE + cb * 16384 + piece * rows * 128, kv ? &mv : &mk, cb * 64, tk, h, now, full);
+          ++issued;
+          if (++slot == NS) {
+            slot = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (!ok && lane == 0)   // leaving early: the copies in flight land first
+        for (int i = max(0, issued - NS); i < issued; ++i) wait.drain(smem_u32(&b_kfull[i % NS]), (i / NS) & 1);
+    } else if (N > 0 && warp == 9) {
+      // ============================== tensor cores
+      if (lane == 0) {
+        constexpr unsigned FMT = FP16 ? 0u : (1u << 7) | (1u << 10);
+        constexpr unsigned ID_S = (1u << 4) | FMT | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+        constexpr unsigned ID_O = (1u << 4) | FMT | (1u << 16) | (((unsigned)D >> 3) << 17) | ((128u >> 4) << 24);
+        PaCursor<NH> cur;
+        cur.set(p, s_start.i, s_start.h, s_start.j, s_start.b);
+        int pp[2] = {0, 0}, qp[2] = {0, 0}, tile = 0;
+        bool was_first = false, was_last = false, was_two = false, ok = true;
+        // keys of block n are in ring place 2 n, values in 2 n + 1
+        auto slot_of = [](long long place) { return (int)(place % NS); };
+        auto parity_of = [](long long place) { return (unsigned)((place / NS) & 1); };
+        auto qk = [&](int qb, int sb, long long place) {   // S sb = Q qb K^T
+          const unsigned long long a = PA_DESC_K | ((sm_q + qb * Sh::TILE) >> 4), b = PA_DESC_K | ((sm_kv + slot_of(place) * Sh::TILE) >> 4);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const unsigned o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+            pa_mma_ss(tm + sb * 128, a + o, b + o, ID_S, k > 0);
+          }
+          pa_commit(smem_u32(&b_s[sb]));
+        };
+        auto pv = [&](int sb, int oh, long long place, bool acc) {   // O oh += P sb V
+          const unsigned long long b = PA_DESC_V | ((sm_kv + slot_of(place) * Sh::TILE) >> 4);
+#pragma unroll
+          for (int k = 0; k < PA_BN / 16; ++k)
+            pa_mma_ts(tm + Sh::TM_O + oh * D, tm + sb * 128 + k * 8, b + ((k * 2048) >> 4), ID_O, acc || k > 0);
+        };
+        for (int n = 0; n <= N && ok; ++n) {
+          const bool more = n < N, first = more && (n == 0 || cur.b == 0), last = more && (n == N - 1 || cur.b == cur.nb - 1);
+          const bool two = more && cur.second_half(p);
+          const long long kplace = 2ll * n, vplace = 2ll * n - 1;
+          if constexpr (NH == 2) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (n > 0 && ok) {
+                if (h == 0) ok = wait(smem_u32(&b_kfull[slot_of(vplace)]), parity_of(vplace));
+                if (ok && (h == 0 || was_two)) {
+                  ok = wait(smem_u32(&b_p[h]), pp[h]);
+                  pp[h] ^= 1;
+                  if (!ok) break;
+                  pa_fence_after();
+                  pv(h, h, vplace, !was_first);
+                  if (was_last) pa_commit(smem_u32(&b_o[h]));
+                }
+                if (ok && h == 1) pa_commit(smem_u32(&b_kempty[slot_of(vplace)]));
+              }
+              if (more && ok && (h == 0 || two)) {
+                if (first) {
+                  ok = wait(smem_u32(&b_qfull[h]), qp[h]);
+                  qp[h] ^= 1;
+                }
+                if (ok && h == 0) ok = wait(smem_u32(&b_kfull[slot_of(kplace)]), parity_of(kplace));
+                if (!ok) break;
+                pa_fence_after();
+                qk(h, h, kplace);
+                if (last) pa_commit(smem_u32(&b_qempty[h]));
+              }
+            }
+            if (more && ok) pa_commit(smem_u32(&b_kempty[slot_of(kplace)]));
+          } else {
+            if (more) {
+              const int qb = tile & 1;
+              if (first) {
+                ok = wait(smem_u32(&b_qfull[qb]), qp[qb]);
+                qp[qb] ^= 1;
+              }
+              ok = ok && wait(smem_u32(&b_kfull[slot_of(kplace)]), parity_of(kplace));
+              if (!ok) break;
+              pa_fence_after();
+              qk(qb, n & 1, kplace);
+              pa_commit(smem_u32(&b_kempty[slot_of(kplace)]));
+              if (last) {
+                pa_commit(smem_u32(&b_qempty[qb]));
+                ++tile;
+              }
+            }
+            if (n > 0) {
+              const int sb = (n - 1) & 1;
+              ok = wait(smem_u32(&b_kfull[slot_of(vplace)]), parity_of(vplace)) && wait(smem_u32(&b_p[sb]), pp[sb]);
+              pp[sb] ^= 1;
+              if (!ok) break;
+              pa_fence_after();
+              pv(sb, 0, vplace, !was_first);
+              pa_commit(smem_u32(&b_kempty[slot_of(vplace)]));
+              pa_commit(smem_u32(&b_o[0]));
+            }
+          }
+          was_first = first;
+          was_last = last;
+          was_two = two;
+          if (more) cur.next(p);
+        }
+        pa_commit(smem_u32(&b_end));   // everything issued is complete before tensor memory goes
+        wait.drain(smem_u32(&b_end), 0);
+      }
+    } else if (N > 0 && warp == 10) {
+      // ============================== queries
+      if (lane == 0) {
+        PaCursor<NH> cur;
+        cur.set(p, s_start.i, s_start.h, s_start.j, s_start.b);
+        int ph[2] = {1, 1}, tile = 0;
+        bool sent[2] = {false, false}, ok = true;
+        for (int n = 0; n < N && ok;) {
+          const int halves = cur.second_half(p) ? 2 : 1;
+          for (int h = 0; h < halves; ++h) {
+            const int qb = NH == 2 ? h : tile & 1;
+            ok = wait(smem_u32(&b_qempty[qb]), ph[qb]);
+            ph[qb] ^= 1;
+            if (!ok) break;
+            const unsigned full = smem_u32(&b_qfull[qb]);
+            mbar_expect_tx(full, p.T * p.G * 128 * Sh::CB);
+            for (int cb = 0; cb < Sh::CB; ++cb)
+              pa_tma3(sm_q + qb * Sh::TILE + cb * 16384, &mq, cb * 64, cur.h * p.G, cur.q.s.q0 + (cur.j * NH + h) * p.T, full);
+            sent[qb] = true;
+          }
+          n += cur.nb - cur.b;
+          ++tile;
+          cur.next_tile(p);
+        }
+        if (!ok)
+          for (int qb = 0; qb < 2; ++qb)
+            if (sent[qb]) wait.drain(smem_u32(&b_qfull[qb]), ph[qb]);
+      }
+    }
   } else {
-    if (fp16) pages_attend_kernel<64, true><<<(unsigned)blocks, 256, 0, st>>>(p);
-    else pages_attend_kernel<64, false><<<(unsigned)blocks, 256, 0, st>>>(p);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int half = warp >> 2;
+    if (N > 0 && half < NH) {
+      // ============================== softmax: this thread's row
+      const int r = tid & 127, w4 = warp & 3;
+      const unsigned lane_off = (unsigned)(w4 * 32) << 16;
+      const unsigned t_o = tm + Sh::TM_O + half * D + lane_off;
+      PaCursor<NH> cur;
+      cur.set(p, s_start.i, s_start.h, s_start.j, s_start.b);
+      const int rt = r / p.G, rg = r - rt * p.G;
+      int sp[2] = {0, 0}, tiles = 0;
+      float ref = -INFINITY, sum = 0.f;
+      int vis = 0, tok = 0, b0 = 0;
+      bool live = false, ok = true;
+      for (int n = 0; n < N; ++n, cur.next(p)) {
+        const bool first = n == 0 || cur.b == 0, last = n == N - 1 || cur.b == cur.nb - 1;
+        if (NH == 2 && half == 1 && !cur.second_half(p)) continue;
+        if (first) {
+          const int t = (cur.j * NH + half) * p.T + rt;
+          live = rt < p.T && t < cur.q.s.m;
+          vis = !live ? 0 : (p.causal ? cur.q.s.len - cur.q.s.m + t + 1 : cur.q.s.len);
+          tok = cur.q.s.q0 + t;
+          b0 = cur.b;
+          ref = -INFINITY;
+          sum = 0.f;
+        }
+        const int sb = NH == 2 ? half : n & 1;
+        ok = wait(smem_u32(&b_s[sb]), sp[sb]);
+        sp[sb] ^= 1;
+        if (!__all_sync(~0u, ok)) break;
+        pa_fence_after();
+        const unsigned t_s = tm + sb * 128 + lane_off;
+        const int left = vis - cur.b * PA_BN;           // visible keys of this block
+        if (__any_sync(~0u, live)) {
+          unsigned s[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) pa_ld32(t_s + c * 32, s + c * 32);
+          pa_wait_ld<128>(s);
+          if (__any_sync(~0u, left < PA_BN)) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c >= left) s[c] = 0xFF800000u;        // -inf, whatever lies there
+          }
+          float mx[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(s[c]);
+#pragma unroll
+          for (int c = 4; c < 128; c += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mx[k] = c + 4 + k < 128 ? fmaxf(fmaxf(mx[k], __uint_as_float(s[c + k])), __uint_as_float(s[c + 4 + k]))
+                                      : fmaxf(mx[k], __uint_as_float(s[c + k]));
+          const float m = fmaxf(ref, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          if (first) {
+            ref = m;
+          } else if (__any_sync(~0u, (m - ref) * p.scale2 > PA_LAZY)) {   // false for -inf - -inf
+            const float f = m == -INFINITY ? 1.f : ex2((ref - m) * p.scale2);
+            ref = m;
+            sum *= f;
+            if constexpr (NH == 1) {   // the P V before this block's may still be running
+              ok = wait(smem_u32(&b_o[0]), (n - 1) & 1);
+              if (!__all_sync(~0u, ok)) break;
+              pa_fence_after();
+            }
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              unsigned o[32];
+              pa_ld32(t_o + c * 32, o);
+              pa_wait_ld<32>(o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              pa_st32(t_o + c * 32, o);
+            }
+          }
+          const float base = ref == -INFINITY ? 0.f : -ref * p.scale2;
+          const unsigned long long sc2 = f2_pack(p.scale2, p.scale2), ba2 = f2_pack(base, base);
+          unsigned long long acc[2] = {0ull, 0ull};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            unsigned pk[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const unsigned long long x =
+                  f2_fma((unsigned long long)s[c * 32 + 2 * k] | ((unsigned long long)s[c * 32 + 2 * k + 1] << 32), sc2, ba2);
+              const float e0 = ex2(f2_lo(x)), e1 = ex2(f2_hi(x));
+              acc[k & 1] = f2_add(acc[k & 1], f2_pack(e0, e1));
+              pk[k] = pa_pack<FP16>(e0, e1);
+            }
+            pa_st16(t_s + c * 16, pk);
+          }
+          const unsigned long long a = f2_add(acc[0], acc[1]);
+          sum += f2_lo(a) + f2_hi(a);
+          pa_wait_st();
+        }
+        pa_fence_before();
+        if (cur.b * PA_BN + PA_BN > cur.q.s.len) {
+          // the values behind the sequence's end may be anything: zeros, so that 0 x NaN does not reach the sum
+          const long long place = 2ll * n + 1;
+          const int slot = (int)(place % NS);
+          ok = wait(smem_u32(&b_kfull[slot]), (unsigned)((place / NS) & 1));
+          if (!__all_sync(~0u, ok)) break;
+          if (cur.b * PA_BN + r >= cur.q.s.len) {
+            const unsigned row = sm_kv + slot * Sh::TILE + r * 128;
+#pragma unroll
+            for (int cb = 0; cb < Sh::CB; ++cb)
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row + cb * 16384 + k * 16), "r"(0) : "memory");
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        __syncwarp();
+        if (lane == 0) pa_arrive(smem_u32(&b_p[sb]));
+        if (!last) continue;
+
+        // ------------------------------ the tile's end in this piece
+        ok = wait(smem_u32(&b_o[half]), NH == 2 ? tiles & 1 : n & 1);
+        ++tiles;
+        if (!__all_sync(~0u, ok)) break;
+        pa_fence_after();
+        const bool whole = b0 == 0 && cur.b == cur.nb - 1;
+        if (__any_sync(~0u, live)) {
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          const int head = cur.h * p.G + rg;
+          uint16_t* dst = p.out + tok * p.ots + head * p.ohs;
+          const long long part = (((long long)blockIdx.x * 2 + (b0 == 0 ? 1 : 0)) * NH + half) * 128 + r;
+          float* po = p.part_o + part * D;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            unsigned o[32];
+            pa_ld32(t_o + c * 32, o);
+            pa_wait_ld<32>(o);
+            if (live && whole) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint4 x;
+                unsigned* y = &x.x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  y[e] = pa_pack<FP16>(__uint_as_float(o[k * 8 + 2 * e]) * inv, __uint_as_float(o[k * 8 + 2 * e + 1]) * inv);
+                *reinterpret_cast<uint4*>(dst + c * 32 + k * 8) = x;
+              }
+            } else if (live) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint4*>(po + c * 32 + k * 4) = make_uint4(o[k * 4], o[k * 4 + 1], o[k * 4 + 2], o[k * 4 + 3]);
+            }
+          }
+          if (live && whole && p.lse) p.lse[(long long)tok * p.Hq + head] = sum == 0.f ? -INFINITY : ref * p.scale + logf(sum);
+          if (live && !whole) p.part_ml[part] = make_float2(sum == 0.f ? -INFINITY : ref * p.scale2, sum);
+        }
+        pa_fence_before();
+      }
+    }
   }
-  return cudaGetLastError();
+  __syncthreads();
+  if (warp == 11) {
+    pa_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
+  }
+}
+
+// Joins the parts of the tiles that were cut: block c takes the tile its piece starts inside of, if no earlier piece
+// starts inside of it too.  A warp per row, lanes over the channels.
+template <int D, int NH, bool FP16>
+__global__ void __launch_bounds__(512) pages_join_kernel(const __grid_constant__ PaParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int c = blockIdx.x;
+  const PaRec r = p.rec[c];
+  if (r.pieces == 0 || r.b == 0) return;
+  const long long before = r.total * (c - 1) / r.pieces;   // where the piece before starts
+  if (before > r.begin) return;
+  int end = c + 1;   // the pieces [c, end) hold the rest of the tile
+  while (end < r.pieces && r.total * end / r.pieces < r.begin + r.nb) ++end;
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  for (int x = threadIdx.x >> 5; x < r.ntok * p.G; x += blockDim.x >> 5) {
+    const int t = x / p.G, g = x - t * p.G, h = t / p.T, row = (t - h * p.T) * p.G + g;
+    auto part = [&](int q) { return (((long long)q * 2 + (q < c ? 1 : 0)) * NH + h) * 128 + row; };
+    float m = -INFINITY;
+    for (int q = c - 1 + lane; q < end; q += 32) m = fmaxf(m, p.part_ml[part(q)].x);
+#pragma unroll
+    for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, k));
+    float sum = 0.f, o[E] = {};
+    if (m != -INFINITY) {
+#pragma unroll 4
+      for (int q = c - 1; q < end; ++q) {
+        const float2 ml = p.part_ml[part(q)];
+        if (ml.x == -INFINITY) continue;
+        const float f = ex2(ml.x - m);
+        sum += ml.y * f;
+        const float* po = p.part_o + part(q) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += po[e] * f;
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const long long tok = r.tok + t;
+    const int head = r.kvh * p.G + g;
+    unsigned* dst = reinterpret_cast<unsigned*>(p.out + tok * p.ots + head * p.ohs + lane * E);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) dst[e] = pa_pack<FP16>(o[2 * e] * inv, o[2 * e + 1] * inv);
+    if (p.lse && lane == 0) p.lse[tok * p.Hq + head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+  }
+}
+
+// ---------------------------------------------------------------------------- launch
+
+// parts of NH halves of 128 rows, two per CTA; records
+size_t pages_attend_bytes(int n_sm, int D) {
+  return (size_t)n_sm * (sizeof(PaRec) + 2 * 2 * 128 * (sizeof(float2) + sizeof(float) * D)) + 64;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static EncodeFn encode_fn() {
+  static std::atomic<EncodeFn> fn{nullptr};
+  EncodeFn f = fn.load();
+  if (f) return f;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
+    return nullptr;
+  f = reinterpret_cast<EncodeFn>(p);
+  fn.store(f);
+  return f;
+}
+
+template <int D, int NH, bool FP16>
+static cudaError_t launch_t(const PaParams& p, const CUtensorMap* maps, int device, int n_sm, cudaStream_t st) {
+  static std::atomic<unsigned long long> ready{0};   // devices whose copy of the kernel has its attribute
+  if (device >= 64 || !(ready.load() >> device & 1)) {
+    const cudaError_t e = cudaFuncSetAttribute(pages_attend_kernel<D, NH, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, PaShape<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    if (device < 64) ready.fetch_or(1ull << device);
+  }
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(n_sm);
+  cfg.blockDim = dim3(PA_THREADS);
+  cfg.dynamicSmemBytes = PaShape<D>::SMEM;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, pages_attend_kernel<D, NH, FP16>, p, maps[0], maps[1], maps[2]);
+  if (e != cudaSuccess) return e;
+  cfg.blockDim = dim3(512);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, pages_join_kernel<D, NH, FP16>, p);
+}
+
+cudaError_t launch_pages_attend(const PagesAttendParams& a, int fp16, int device, int n_sm, void* ws, cudaStream_t st) {
+  const EncodeFn enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const PagesView& g = a.pg;
+  PaParams p{};
+  p.pg = g;
+  p.t = a.t;
+  p.c = a.c;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.ots = a.ots;
+  p.ohs = a.ohs;
+  p.Hq = a.Hq;
+  p.G = a.Hq / g.H;
+  p.causal = a.causal;
+  p.scale = a.scale;
+  p.scale2 = a.scale * 1.44269504088896341f;
+  // One half where the chunk's rows fit it (a few rows: bound by reading the cache), else two.  The tile takes no more
+  // tokens than the longest chunk, so that its query copy does not read the next sequences' rows.
+  const int fit = 128 / p.G;
+  const bool one = a.max_q_len > 0 && a.max_q_len <= fit;
+  p.T = one ? a.max_q_len : fit;
+  p.min_blocks = 2;
+  const int nh = one ? 1 : 2;
+  char* at = static_cast<char*>(ws);
+  p.part_o = reinterpret_cast<float*>(at);
+  at += (size_t)n_sm * 2 * nh * 128 * g.D * sizeof(float);
+  p.part_ml = reinterpret_cast<float2*>(at);
+  at += (size_t)n_sm * 2 * nh * 128 * sizeof(float2);
+  p.rec = reinterpret_cast<PaRec*>(at);
+
+  CUtensorMap maps[3];
+  const CUtensorMapDataType ty = fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  auto bytes = [&](long long stride) { return (cuuint64_t)(stride > 0 ? stride * 2 : g.D * 2); };   // (an axis of one entry: any)
+  {
+    const cuuint64_t dim[3] = {(cuuint64_t)g.D, (cuuint64_t)a.Hq, (cuuint64_t)a.c.total};
+    const cuuint64_t str[2] = {bytes(a.Hq > 1 ? a.qhs : 0), bytes(a.c.total > 1 ? a.qts : 0)};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.T};
+    if (enc(&maps[0], ty, 3, const_cast<uint16_t*>(a.q), dim, str, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  for (int i = 0; i < 2; ++i) {
+    const cuuint64_t dim[4] = {(cuuint64_t)g.D, (cuuint64_t)g.S, (cuuint64_t)g.H, (cuuint64_t)g.P};
+    const cuuint64_t str[3] = {bytes(g.ts), bytes(g.hs), bytes(g.ps)};
+    const cuuint32_t box[4] = {64, (cuuint32_t)(g.S < 128 ? g.S : 128), 1, 1};
+    if (enc(&maps[1 + i], ty, 4, (i ? g.v : g.k) + a.layer * g.ls, dim, str, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  if (g.D == 128) {
+    if (one) return fp16 ? launch_t<128, 1, true>(p, maps, device, n_sm, st) : launch_t<128, 1, false>(p, maps, device, n_sm, st);
+    return fp16 ? launch_t<128, 2, true>(p, maps, device, n_sm, st) : launch_t<128, 2, false>(p, maps, device, n_sm, st);
+  }
+  if (one) return fp16 ? launch_t<64, 1, true>(p, maps, device, n_sm, st) : launch_t<64, 1, false>(p, maps, device, n_sm, st);
+  return fp16 ? launch_t<64, 2, true>(p, maps, device, n_sm, st) : launch_t<64, 2, false>(p, maps, device, n_sm, st);
 }
 
 }  // namespace qe

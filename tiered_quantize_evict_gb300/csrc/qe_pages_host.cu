@@ -211,7 +211,9 @@ qe_status qe_pages_attend_workspace(const qe_pages* pages, size_t* bytes) {
   qe::PagesView pg{};
   QE_TRY(check_pages(pages, &pg));
   if (!bytes) return fail(QE_ERR_INVALID_ARG, "bytes is null");
-  *bytes = 16;
+  int n_sm = 0;
+  QE_TRY(sm_count(pages->device, &n_sm));
+  *bytes = qe::pages_attend_bytes(n_sm, pg.D);
   return QE_OK;
 }
 
@@ -232,7 +234,9 @@ qe_status qe_pages_attend(const qe_pages* pages, int layer, const qe_page_table*
   QE_TRY(check_rows("q", a->q, a->q_token_stride, a->q_head_stride, p.c.total, a->n_q_heads, p.pg.D));
   QE_TRY(check_rows("out", a->out, a->out_token_stride, a->out_head_stride, p.c.total, a->n_q_heads, p.pg.D));
   if (misaligned(a->lse, 4)) return fail(QE_ERR_INVALID_ARG, "lse must be 4-byte aligned");
-  QE_TRY(check_workspace(workspace, bytes, 16));
+  int n_sm = 0;
+  QE_TRY(sm_count(pages->device, &n_sm));
+  QE_TRY(check_workspace(workspace, bytes, qe::pages_attend_bytes(n_sm, p.pg.D)));
   p.q = static_cast<const uint16_t*>(a->q);
   p.out = static_cast<uint16_t*>(a->out);
   p.lse = a->lse;
@@ -243,10 +247,12 @@ qe_status qe_pages_attend(const qe_pages* pages, int layer, const qe_page_table*
   p.layer = layer;
   p.Hq = a->n_q_heads;
   p.causal = a->causal != 0;
+  p.max_q_len = a->max_q_len;
   p.scale = a->scale;
   DeviceGuard guard(pages->device);
   if (guard.err != cudaSuccess) return cuda_fail(guard.err, "cudaSetDevice");
-  return launched(qe::launch_pages_attend(p, pages->dtype == QE_DTYPE_FP16, static_cast<cudaStream_t>(stream)), "qe_pages_attend");
+  return launched(qe::launch_pages_attend(p, pages->dtype == QE_DTYPE_FP16, pages->device, n_sm, workspace, static_cast<cudaStream_t>(stream)),
+                  "qe_pages_attend");
 }
 
 qe_status qe_pages_manage_workspace(const qe_pages* pages, const qe_page_table* seqs, int n, size_t* bytes) {
