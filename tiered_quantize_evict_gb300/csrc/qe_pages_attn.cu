@@ -16,8 +16,8 @@
 // from the lengths on the device by every CTA alike (a sum of floors in closed form per sequence).
 //
 // CTA: 12 warps.  Warps 0-3 and 4-7: softmax of half 0 and 1, a thread per row (with NH = 1 the second four idle).
-// Warp 8: TMA of keys and values, page by page, into a ring of slots.  Warp 9: tensor-core issue.  Warp 10: TMA of the
-// queries.  Warp 11: tensor memory.
+// Warp 8: TMA of keys and values, page by page, into a ring of slots.  Warps 9, 10: tensor-core issue of half 0 and 1.
+// Warp 11: tensor memory, TMA of the queries.
 //  * S = Q K^T (M 128, N 128): both operands in shared memory, 128-byte swizzle, K-major.
 //  * P overwrites its S in tensor memory in the pool's type; O += P V (N = head_dim) takes P from there and V as the
 //    MN-major operand (its rows are tokens).
@@ -26,7 +26,7 @@
 //  * P is rounded to the pool's type (the tensor cores' operand): a relative 2^-9 (bf16), 2^-12 (fp16) per probability at
 //    most half a step, as the result itself is; the sum is of the unrounded ones.
 // mbarriers: kfull / kempty per slot, qfull / qempty per query buffer, s[i] (S i complete; tensor-core commit),
-// p[i] (P i written; one arrival per softmax warp), o[h] (the P V before it complete).  Every wait is bounded (0.2 s); one that expires sets
+// p[i][0], p[i][1] (P i's first and second half of the keys written; one arrival per softmax warp), o[h] (the P V before it complete).  Every wait is bounded (0.2 s); one that expires sets
 // QE_PAGES_ERR_TIMEOUT and an abort flag that ends all loops, and the CTA leaves after what it issued has landed.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -80,7 +80,7 @@ struct PaParams {
 // ---------------------------------------------------------------------------- the line of blocks
 
 // sum over i < n of floor((a i + b) / 128): Euclid's recursion on (128, a)
-__device__ inline unsigned long long floor_sum128(unsigned long long n, unsigned long long a, unsigned long long b) {
+__device__ __noinline__ unsigned long long floor_sum128(unsigned long long n, unsigned long long a, unsigned long long b) {
   unsigned long long m = 128, ans = 0;
   if (n == 0) return 0;
   while (true) {
@@ -160,9 +160,6 @@ struct PaCursor {
     }
     nb = pa_blocks<NH>(p, q.s, j);
   }
-  __device__ __forceinline__ void next(const PaParams& p) {
-    if (++b >= nb) next_tile(p);
-  }
   __device__ __forceinline__ bool second_half(const PaParams& p) const { return NH == 2 && j * 2 * p.T + p.T < q.s.m; }
 };
 
@@ -173,7 +170,7 @@ struct PaStart {
 
 // Every CTA finds its piece: sums the sequences' blocks, cuts the line, finds the tile its cut falls in.
 template <int NH>
-__device__ void pa_find(const PaParams& p, PaStart* out, long long* s_w, long long* s_rem) {
+__device__ __noinline__ void pa_find(const PaParams& p, PaStart* out, long long* s_w, long long* s_rem) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int W = PA_THREADS / 32;
   const int c = blockIdx.x;
@@ -281,6 +278,12 @@ __device__ __forceinline__ void pa_mma_ts(unsigned d, unsigned a, unsigned long 
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0)
       : "memory");
 }
+// one lane of a converged warp
+__device__ __forceinline__ bool pa_elect() {
+  unsigned r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r)::"memory");
+  return r != 0;
+}
 __device__ __forceinline__ void pa_commit(unsigned bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
@@ -344,9 +347,11 @@ struct PaWait {
   volatile int* abort;
   // Bounded wait for the phase; false when it expired or the CTA is leaving.
   __device__ __forceinline__ bool operator()(unsigned bar, unsigned parity) const {
-    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+    return mbar_try_wait(bar, parity) || slow(bar, parity);
+  }
+  __device__ __forceinline__ bool slow(unsigned bar, unsigned parity) const {
     const unsigned long long t0 = globaltimer_ns();
-    while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+    while (!mbar_try_wait(bar, parity)) {
       if (*abort) return false;
       if (globaltimer_ns() - t0 > PA_WAIT_NS) {
         pages_report(*pg, QE_PAGES_ERR_TIMEOUT);
@@ -386,7 +391,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   using Sh = PaShape<D>;
   constexpr int NS = Sh::SLOTS;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) unsigned long long b_kfull[NS], b_kempty[NS], b_qfull[2], b_qempty[2], b_s[2], b_p[2], b_o[2], b_end;
+  __shared__ __align__(8) unsigned long long b_kfull[NS], b_kempty[NS], b_qfull[2], b_qempty[2], b_s[2], b_p[2][2], b_o[2], b_end;
   __shared__ unsigned s_tmem;
   __shared__ int s_abort;
   __shared__ PaStart s_start;
@@ -405,16 +410,17 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(smem_u32(&b_kfull[i]), 1);
-      mbar_init(smem_u32(&b_kempty[i]), 1);
+      mbar_init(smem_u32(&b_kempty[i]), NH);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&b_qfull[i]), 1);
       mbar_init(smem_u32(&b_qempty[i]), 1);
       mbar_init(smem_u32(&b_s[i]), 1);
-      mbar_init(smem_u32(&b_p[i]), 4);
+      mbar_init(smem_u32(&b_p[i][0]), 4);
+      mbar_init(smem_u32(&b_p[i][1]), 4);
       mbar_init(smem_u32(&b_o[i]), 1);
     }
-    mbar_init(smem_u32(&b_end), 1);
+    mbar_init(smem_u32(&b_end), NH);
     mbar_fence_init();
     s_abort = 0;
   }
@@ -445,11 +451,12 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       int slot = 0, ph = 1, issued = 0;
       int page = page_of();
       bool ok = true;
+#pragma unroll 1
       for (int n = 0; n < N && ok; ++n) {
         const int tk = (cur.b * PA_BN) & (p.pg.S - 1), h = cur.h, now = page;
-        cur.next(p);
-        if (n + 1 < N) page = page_of();
-#pragma unroll
+        if (++cur.b >= cur.nb) cur.next_tile(p);
+        if (n + 1 < N) page = page_of();                 // the next block's, read ahead
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           ok = ok && wait(smem_u32(&b_kempty[slot]), ph);
           if (!__all_sync(~0u, ok)) {
@@ -469,111 +476,145 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       }
       if (!ok && lane == 0)   // leaving early: the copies in flight land first
         for (int i = max(0, issued - NS); i < issued; ++i) wait.drain(smem_u32(&b_kfull[i % NS]), (i / NS) & 1);
-    } else if (N > 0 && warp == 9) {
-      // ============================== tensor cores
-      if (lane == 0) {
-        constexpr unsigned FMT = FP16 ? 0u : (1u << 7) | (1u << 10);
-        constexpr unsigned ID_S = (1u << 4) | FMT | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-        constexpr unsigned ID_O = (1u << 4) | FMT | (1u << 16) | (((unsigned)D >> 3) << 17) | ((128u >> 4) << 24);
-        PaCursor<NH> cur;
-        cur.set(p, s_start.i, s_start.h, s_start.j, s_start.b);
-        int pp[2] = {0, 0}, qp[2] = {0, 0}, tile = 0;
-        bool was_first = false, was_last = false, was_two = false, ok = true;
-        // keys of block n are in ring place 2 n, values in 2 n + 1
-        auto slot_of = [](long long place) { return (int)(place % NS); };
-        auto parity_of = [](long long place) { return (unsigned)((place / NS) & 1); };
-        auto qk = [&](int qb, int sb, long long place) {   // S sb = Q qb K^T
-          const unsigned long long a = PA_DESC_K | ((sm_q + qb * Sh::TILE) >> 4), b = PA_DESC_K | ((sm_kv + slot_of(place) * Sh::TILE) >> 4);
+    } else if (N > 0 && warp - 9 < NH) {
+      // ============================== tensor cores: a warp per half, so that the waits and the issue of one half pass while
+      // the products of the other run.  The whole warp walks the loop (addresses and descriptors stay uniform), one lane issues.
+      const int h = warp - 9;
+      constexpr unsigned FMT = FP16 ? 0u : (1u << 7) | (1u << 10);
+      constexpr unsigned ID_S = (1u << 4) | FMT | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+      constexpr unsigned ID_O = (1u << 4) | FMT | (1u << 16) | (((unsigned)D >> 3) << 17) | ((128u >> 4) << 24);
+      PaCursor<NH> cur;
+      cur.set(p, s_start.i, s_start.h, s_start.j, s_start.b);
+      // The ring is consumed in its order: K 0, then V n - 1 and K n in turn.
+      int slot = 0, ph = 0, pp = 0, qp = 0, tile = 0, left = 0;   // (bit i of pp, qp: the parity of p[i], qfull[i])
+      bool was_first = false, was_last = false, was_mine = false, mine = false, ok = true;
+      auto step = [&]() {
+        if (++slot == NS) {
+          slot = 0;
+          ph ^= 1;
+        }
+      };
+      const unsigned t_o = tm + Sh::TM_O + h * D;
+      auto qk = [&](int qb, int sb, int kslot, bool q_done) {   // S sb = Q qb K^T (by one lane)
+        const unsigned long long a = PA_DESC_K | ((sm_q + qb * Sh::TILE) >> 4), b = PA_DESC_K | ((sm_kv + kslot * Sh::TILE) >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const unsigned o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-            pa_mma_ss(tm + sb * 128, a + o, b + o, ID_S, k > 0);
+        for (int k = 0; k < D / 16; ++k) {
+          const unsigned o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+          pa_mma_ss(tm + sb * 128, a + o, b + o, ID_S, k > 0);
+        }
+        pa_commit(smem_u32(&b_s[sb]));
+        pa_commit(smem_u32(&b_kempty[kslot]));
+        if (q_done) pa_commit(smem_u32(&b_qempty[qb]));
+      };
+      auto pv = [&](int part, int sb, int vslot, bool acc) {   // O += P sb V over one half of the keys (by one lane)
+        const unsigned long long b = (PA_DESC_V | ((sm_kv + vslot * Sh::TILE) >> 4)) + part * 512;
+#pragma unroll
+        for (int k = 0; k < PA_BN / 32; ++k)
+          pa_mma_ts(t_o, tm + sb * 128 + part * 32 + k * 8, b + k * 128, ID_O, acc || k > 0);
+      };
+#pragma unroll 1
+      for (int n = 0; n <= N; ++n) {
+        const bool more = n < N, first = left == 0;
+        if (first && more) {
+          if (n > 0) cur.next_tile(p);
+          left = min(cur.nb - cur.b, N - n);
+          mine = h == 0 || cur.second_half(p);
+        }
+        const bool last = left == 1;
+        const int vslot = slot;
+        if constexpr (NH == 2) {
+          // what has to be there: values, keys and queries, long before the probabilities
+          if (n > 0) {
+            ok = ok && wait(smem_u32(&b_kfull[slot]), ph);
+            step();
           }
-          pa_commit(smem_u32(&b_s[sb]));
-        };
-        auto pv = [&](int sb, int oh, long long place, bool acc) {   // O oh += P sb V
-          const unsigned long long b = PA_DESC_V | ((sm_kv + slot_of(place) * Sh::TILE) >> 4);
-#pragma unroll
-          for (int k = 0; k < PA_BN / 16; ++k)
-            pa_mma_ts(tm + Sh::TM_O + oh * D, tm + sb * 128 + k * 8, b + ((k * 2048) >> 4), ID_O, acc || k > 0);
-        };
-        for (int n = 0; n <= N && ok; ++n) {
-          const bool more = n < N, first = more && (n == 0 || cur.b == 0), last = more && (n == N - 1 || cur.b == cur.nb - 1);
-          const bool two = more && cur.second_half(p);
-          const long long kplace = 2ll * n, vplace = 2ll * n - 1;
-          if constexpr (NH == 2) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (n > 0 && ok) {
-                if (h == 0) ok = wait(smem_u32(&b_kfull[slot_of(vplace)]), parity_of(vplace));
-                if (ok && (h == 0 || was_two)) {
-                  ok = wait(smem_u32(&b_p[h]), pp[h]);
-                  pp[h] ^= 1;
-                  if (!ok) break;
-                  pa_fence_after();
-                  pv(h, h, vplace, !was_first);
-                  if (was_last) pa_commit(smem_u32(&b_o[h]));
-                }
-                if (ok && h == 1) pa_commit(smem_u32(&b_kempty[slot_of(vplace)]));
-              }
-              if (more && ok && (h == 0 || two)) {
-                if (first) {
-                  ok = wait(smem_u32(&b_qfull[h]), qp[h]);
-                  qp[h] ^= 1;
-                }
-                if (ok && h == 0) ok = wait(smem_u32(&b_kfull[slot_of(kplace)]), parity_of(kplace));
-                if (!ok) break;
-                pa_fence_after();
-                qk(h, h, kplace);
-                if (last) pa_commit(smem_u32(&b_qempty[h]));
-              }
+          if (more) {
+            ok = ok && wait(smem_u32(&b_kfull[slot]), ph);
+            if (first && mine) {
+              ok = ok && wait(smem_u32(&b_qfull[h]), qp & 1);
+              qp ^= 1;
             }
-            if (more && ok) pa_commit(smem_u32(&b_kempty[slot_of(kplace)]));
-          } else {
-            if (more) {
-              const int qb = tile & 1;
-              if (first) {
-                ok = wait(smem_u32(&b_qfull[qb]), qp[qb]);
-                qp[qb] ^= 1;
-              }
-              ok = ok && wait(smem_u32(&b_kfull[slot_of(kplace)]), parity_of(kplace));
-              if (!ok) break;
-              pa_fence_after();
-              qk(qb, n & 1, kplace);
-              pa_commit(smem_u32(&b_kempty[slot_of(kplace)]));
-              if (last) {
-                pa_commit(smem_u32(&b_qempty[qb]));
-                ++tile;
-              }
+          }
+          if (!__all_sync(~0u, ok)) break;
+          const bool do_pv = n > 0 && was_mine, do_qk = more && mine;
+          if (do_pv) {
+            ok = wait(smem_u32(&b_p[h][0]), pp);
+            pa_fence_after();
+            if (pa_elect()) pv(0, h, vslot, !was_first);
+            __syncwarp();
+            ok = wait(smem_u32(&b_p[h][1]), pp) && ok;
+            pp ^= 1;
+          }
+          pa_fence_after();
+          if (pa_elect()) {
+            if (do_pv) {
+              pv(1, h, vslot, true);
+              if (was_last) pa_commit(smem_u32(&b_o[h]));
+              pa_commit(smem_u32(&b_kempty[vslot]));
+            } else if (n > 0) {
+              pa_arrive(smem_u32(&b_kempty[vslot]));
             }
-            if (n > 0) {
-              const int sb = (n - 1) & 1;
-              ok = wait(smem_u32(&b_kfull[slot_of(vplace)]), parity_of(vplace)) && wait(smem_u32(&b_p[sb]), pp[sb]);
-              pp[sb] ^= 1;
-              if (!ok) break;
-              pa_fence_after();
-              pv(sb, 0, vplace, !was_first);
-              pa_commit(smem_u32(&b_kempty[slot_of(vplace)]));
+            if (do_qk) qk(h, h, slot, last);
+            else if (more) pa_arrive(smem_u32(&b_kempty[slot]));
+          }
+          __syncwarp();
+          if (more) step();
+        } else {
+          // S runs a block ahead: K n before V n - 1 and P n - 1
+          if (more) {
+            const int kslot = n == 0 ? slot : (slot + 1 == NS ? 0 : slot + 1), kph = n > 0 && slot + 1 == NS ? ph ^ 1 : ph;
+            const int qb = tile & 1;
+            if (first) {
+              ok = ok && wait(smem_u32(&b_qfull[qb]), qp >> qb & 1);
+              qp ^= 1 << qb;
+            }
+            ok = ok && wait(smem_u32(&b_kfull[kslot]), kph);
+            if (!__all_sync(~0u, ok)) break;
+            pa_fence_after();
+            if (pa_elect()) qk(qb, n & 1, kslot, last);
+            __syncwarp();
+            if (last) ++tile;
+          }
+          if (n > 0) {
+            const int sb = (n - 1) & 1;
+            ok = ok && wait(smem_u32(&b_kfull[vslot]), ph);
+            ok = ok && wait(smem_u32(&b_p[sb][0]), pp >> sb & 1);
+            if (!__all_sync(~0u, ok)) break;
+            pa_fence_after();
+            if (pa_elect()) pv(0, sb, vslot, !was_first);
+            __syncwarp();
+            ok = wait(smem_u32(&b_p[sb][1]), pp >> sb & 1);
+            pp ^= 1 << sb;
+            pa_fence_after();
+            if (pa_elect()) {
+              pv(1, sb, vslot, true);
+              pa_commit(smem_u32(&b_kempty[vslot]));
               pa_commit(smem_u32(&b_o[0]));
             }
+            __syncwarp();
+            step();
           }
-          was_first = first;
-          was_last = last;
-          was_two = two;
-          if (more) cur.next(p);
+          if (more) step();
         }
-        pa_commit(smem_u32(&b_end));   // everything issued is complete before tensor memory goes
-        wait.drain(smem_u32(&b_end), 0);
+        was_first = first;
+        was_last = last;
+        was_mine = mine;
+        --left;
       }
-    } else if (N > 0 && warp == 10) {
+      if (pa_elect()) pa_commit(smem_u32(&b_end));   // everything issued is complete before tensor memory goes
+      __syncwarp();
+      wait.drain(smem_u32(&b_end), 0);
+    } else if (N > 0 && warp == 11) {
       // ============================== queries
       if (lane == 0) {
         PaCursor<NH> cur;
         cur.set(p, s_start.i, s_start.h, s_start.j, s_start.b);
         int ph[2] = {1, 1}, tile = 0;
         bool sent[2] = {false, false}, ok = true;
+#pragma unroll 1
         for (int n = 0; n < N && ok;) {
           const int halves = cur.second_half(p) ? 2 : 1;
+#pragma unroll 1
           for (int h = 0; h < halves; ++h) {
             const int qb = NH == 2 ? h : tile & 1;
             ok = wait(smem_u32(&b_qempty[qb]), ph[qb]);
@@ -605,48 +646,71 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       PaCursor<NH> cur;
       cur.set(p, s_start.i, s_start.h, s_start.j, s_start.b);
       const int rt = r / p.G, rg = r - rt * p.G;
-      int sp[2] = {0, 0}, tiles = 0;
-      float ref = -INFINITY, sum = 0.f;
-      int vis = 0, tok = 0, b0 = 0;
-      bool live = false, ok = true;
-      for (int n = 0; n < N; ++n, cur.next(p)) {
-        const bool first = n == 0 || cur.b == 0, last = n == N - 1 || cur.b == cur.nb - 1;
-        if (NH == 2 && half == 1 && !cur.second_half(p)) continue;
-        if (first) {
-          const int t = (cur.j * NH + half) * p.T + rt;
-          live = rt < p.T && t < cur.q.s.m;
-          vis = !live ? 0 : (p.causal ? cur.q.s.len - cur.q.s.m + t + 1 : cur.q.s.len);
-          tok = cur.q.s.q0 + t;
-          b0 = cur.b;
-          ref = -INFINITY;
-          sum = 0.f;
-        }
+      int sp = 0, tiles = 0, n = 0;   // (bit i of sp: the parity of s[i])
+      bool ok = true;
+#pragma unroll 1
+      for (; n < N && ok; cur.next_tile(p)) {
+       const int cnt = min(cur.nb - cur.b, N - n);
+       if (NH == 2 && half == 1 && !cur.second_half(p)) {
+         n += cnt;
+         continue;
+       }
+       const int t = (cur.j * NH + half) * p.T + rt;
+       const bool live = rt < p.T && t < cur.q.s.m;
+       const bool any_live = __any_sync(~0u, live);
+       const int len = cur.q.s.len - cur.b * PA_BN;                                                       // keys of the piece on
+       const int vis = (!live ? 0 : (p.causal ? cur.q.s.len - cur.q.s.m + t + 1 : cur.q.s.len)) - cur.b * PA_BN;   // and visible ones
+       const int all_vis = __reduce_min_sync(~0u, vis);   // keys that every row of the warp sees
+       float ref = -INFINITY, sum = 0.f;
+#pragma unroll 1
+       for (int k = 0; k < cnt; ++k, ++n) {
+        const bool first = k == 0;
         const int sb = NH == 2 ? half : n & 1;
-        ok = wait(smem_u32(&b_s[sb]), sp[sb]);
-        sp[sb] ^= 1;
-        if (!__all_sync(~0u, ok)) break;
+        ok = __all_sync(~0u, wait(smem_u32(&b_s[sb]), sp >> sb & 1));
+        sp ^= 1 << sb;
+        if (!ok) break;
         pa_fence_after();
         const unsigned t_s = tm + sb * 128 + lane_off;
-        const int left = vis - cur.b * PA_BN;           // visible keys of this block
-        if (__any_sync(~0u, live)) {
-          unsigned s[128];
+        if ((k + 1) * PA_BN > len) {
+          // the values behind the sequence's end may be anything: zeros, so that 0 x NaN does not reach the sum
+          const int place = 2 * n + 1, slot = place % NS;
+          ok = __all_sync(~0u, wait(smem_u32(&b_kfull[slot]), (place / NS) & 1));
+          if (!ok) break;
+          if (k * PA_BN + r >= len) {
+            const unsigned row = sm_kv + slot * Sh::TILE + r * 128;
+#pragma unroll 1
+            for (int cb = 0; cb < Sh::CB; ++cb)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) pa_ld32(t_s + c * 32, s + c * 32);
-          pa_wait_ld<128>(s);
-          if (__any_sync(~0u, left < PA_BN)) {
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c >= left) s[c] = 0xFF800000u;        // -inf, whatever lies there
+              for (int e = 0; e < 8; ++e)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row + cb * 16384 + e * 16), "r"(0) : "memory");
           }
-          float mx[4];
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        if (any_live) {
+          unsigned s[128];
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto take_max = [&](int from) {
+            if ((k + 1) * PA_BN > all_vis) {
+              const int left = vis - k * PA_BN;         // visible keys of this block
 #pragma unroll
-          for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(s[c]);
+              for (int c = 0; c < 64; ++c)
+                if (from + c >= left) s[from + c] = 0xFF800000u;   // -inf, whatever lies there
+            }
 #pragma unroll
-          for (int c = 4; c < 128; c += 8)
+            for (int c = from; c < from + 64; c += 8)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mx[k] = c + 4 + k < 128 ? fmaxf(fmaxf(mx[k], __uint_as_float(s[c + k])), __uint_as_float(s[c + 4 + k]))
-                                      : fmaxf(mx[k], __uint_as_float(s[c + k]));
+              for (int e = 0; e < 4; ++e)
+                mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(s[c + e])), __uint_as_float(s[c + 4 + e]));
+          };
+          // the second half of the columns loads while the first's maximum is taken
+          pa_ld32(t_s, s);
+          pa_ld32(t_s + 32, s + 32);
+          pa_wait_ld<64>(s);
+          pa_ld32(t_s + 64, s + 64);
+          pa_ld32(t_s + 96, s + 96);
+          take_max(0);
+          pa_wait_ld<64>(s + 64);
+          take_max(64);
           const float m = fmaxf(ref, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
           if (first) {
             ref = m;
@@ -655,17 +719,17 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             ref = m;
             sum *= f;
             if constexpr (NH == 1) {   // the P V before this block's may still be running
-              ok = wait(smem_u32(&b_o[0]), (n - 1) & 1);
-              if (!__all_sync(~0u, ok)) break;
+              ok = __all_sync(~0u, wait(smem_u32(&b_o[0]), (n - 1) & 1));
+              if (!ok) break;
               pa_fence_after();
             }
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               unsigned o[32];
               pa_ld32(t_o + c * 32, o);
               pa_wait_ld<32>(o);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
               pa_st32(t_o + c * 32, o);
             }
           }
@@ -676,53 +740,47 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
           for (int c = 0; c < 4; ++c) {
             unsigned pk[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
+            for (int e = 0; e < 16; ++e) {
               const unsigned long long x =
-                  f2_fma((unsigned long long)s[c * 32 + 2 * k] | ((unsigned long long)s[c * 32 + 2 * k + 1] << 32), sc2, ba2);
+                  f2_fma((unsigned long long)s[c * 32 + 2 * e] | ((unsigned long long)s[c * 32 + 2 * e + 1] << 32), sc2, ba2);
               const float e0 = ex2(f2_lo(x)), e1 = ex2(f2_hi(x));
-              acc[k & 1] = f2_add(acc[k & 1], f2_pack(e0, e1));
-              pk[k] = pa_pack<FP16>(e0, e1);
+              acc[e & 1] = f2_add(acc[e & 1], f2_pack(e0, e1));
+              pk[e] = pa_pack<FP16>(e0, e1);
             }
             pa_st16(t_s + c * 16, pk);
+            if (c == 1) {   // the first half of the keys can go
+              pa_wait_st();
+              pa_fence_before();
+              __syncwarp();
+              if (lane == 0) pa_arrive(smem_u32(&b_p[sb][0]));
+            }
           }
           const unsigned long long a = f2_add(acc[0], acc[1]);
           sum += f2_lo(a) + f2_hi(a);
           pa_wait_st();
+        } else if (lane == 0) {
+          pa_arrive(smem_u32(&b_p[sb][0]));
         }
         pa_fence_before();
-        if (cur.b * PA_BN + PA_BN > cur.q.s.len) {
-          // the values behind the sequence's end may be anything: zeros, so that 0 x NaN does not reach the sum
-          const long long place = 2ll * n + 1;
-          const int slot = (int)(place % NS);
-          ok = wait(smem_u32(&b_kfull[slot]), (unsigned)((place / NS) & 1));
-          if (!__all_sync(~0u, ok)) break;
-          if (cur.b * PA_BN + r >= cur.q.s.len) {
-            const unsigned row = sm_kv + slot * Sh::TILE + r * 128;
-#pragma unroll
-            for (int cb = 0; cb < Sh::CB; ++cb)
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row + cb * 16384 + k * 16), "r"(0) : "memory");
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
         __syncwarp();
-        if (lane == 0) pa_arrive(smem_u32(&b_p[sb]));
-        if (!last) continue;
+        if (lane == 0) pa_arrive(smem_u32(&b_p[sb][1]));
+       }
+       if (!ok) break;
 
         // ------------------------------ the tile's end in this piece
-        ok = wait(smem_u32(&b_o[half]), NH == 2 ? tiles & 1 : n & 1);
+        ok = __all_sync(~0u, wait(smem_u32(&b_o[half]), NH == 2 ? tiles & 1 : (n - 1) & 1));
         ++tiles;
-        if (!__all_sync(~0u, ok)) break;
+        if (!ok) break;
         pa_fence_after();
-        const bool whole = b0 == 0 && cur.b == cur.nb - 1;
-        if (__any_sync(~0u, live)) {
+        const bool whole = cnt == cur.nb;
+        if (any_live) {
+          const int tok = cur.q.s.q0 + t;
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
           const int head = cur.h * p.G + rg;
           uint16_t* dst = p.out + tok * p.ots + head * p.ohs;
-          const long long part = (((long long)blockIdx.x * 2 + (b0 == 0 ? 1 : 0)) * NH + half) * 128 + r;
+          const long long part = (((long long)blockIdx.x * 2 + (cur.b == 0 ? 1 : 0)) * NH + half) * 128 + r;
           float* po = p.part_o + part * D;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             unsigned o[32];
             pa_ld32(t_o + c * 32, o);
@@ -731,10 +789,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 uint4 x;
-                unsigned* y = &x.x;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  y[e] = pa_pack<FP16>(__uint_as_float(o[k * 8 + 2 * e]) * inv, __uint_as_float(o[k * 8 + 2 * e + 1]) * inv);
+                x.x = pa_pack<FP16>(__uint_as_float(o[k * 8]) * inv, __uint_as_float(o[k * 8 + 1]) * inv);
+                x.y = pa_pack<FP16>(__uint_as_float(o[k * 8 + 2]) * inv, __uint_as_float(o[k * 8 + 3]) * inv);
+                x.z = pa_pack<FP16>(__uint_as_float(o[k * 8 + 4]) * inv, __uint_as_float(o[k * 8 + 5]) * inv);
+                x.w = pa_pack<FP16>(__uint_as_float(o[k * 8 + 6]) * inv, __uint_as_float(o[k * 8 + 7]) * inv);
                 *reinterpret_cast<uint4*>(dst + c * 32 + k * 8) = x;
               }
             } else if (live) {
