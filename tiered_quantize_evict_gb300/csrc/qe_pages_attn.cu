@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   using Sh = PaShape<D>;
   constexpr int NS = Sh::SLOTS;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) unsigned long long b_kfull[NS], b_kempty[NS], b_qfull[2], b_qempty[2], b_s[2], b_p[2][2], b_o[2], b_end;
+  __shared__ __align__(8) unsigned long long b_kfull[NS], b_kempty[NS], b_qfull[2], b_qempty[2], b_s[2], b_p[2][2], b_o[2], b_turn[2], b_end;
   __shared__ unsigned s_tmem;
   __shared__ int s_abort;
   __shared__ PaStart s_start;
@@ -419,6 +419,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       mbar_init(smem_u32(&b_p[i][0]), 4);
       mbar_init(smem_u32(&b_p[i][1]), 4);
       mbar_init(smem_u32(&b_o[i]), 1);
+      mbar_init(smem_u32(&b_turn[i]), 1);
     }
     mbar_init(smem_u32(&b_end), NH);
     mbar_fence_init();
@@ -500,6 +501,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const unsigned o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+          if (NH == 2 && k == D / 16 - 2) pa_arrive(smem_u32(&b_turn[h ^ 1]));   // (its first product is issued by when these are done)
           pa_mma_ss(tm + sb * 128, a + o, b + o, ID_S, k > 0);
         }
         pa_commit(smem_u32(&b_s[sb]));
@@ -537,8 +539,11 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
           }
           if (!__all_sync(~0u, ok)) break;
           const bool do_pv = n > 0 && was_mine, do_qk = more && mine;
+          if (do_pv) ok = wait(smem_u32(&b_p[h][0]), pp);
+          // The halves take turns, products of a half in one go: one half's softmax runs under the other's products.  (Left
+          // to themselves they interleave, and both softmaxes and then both halves' products run at the same time.)
+          ok = wait(smem_u32(&b_turn[h]), (n & 1) ^ h ^ 1) && ok;
           if (do_pv) {
-            ok = wait(smem_u32(&b_p[h][0]), pp);
             pa_fence_after();
             if (pa_elect()) pv(0, h, vslot, !was_first);
             __syncwarp();
@@ -556,6 +561,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             }
             if (do_qk) qk(h, h, slot, last);
             else if (more) pa_arrive(smem_u32(&b_kempty[slot]));
+            if (!do_qk) pa_arrive(smem_u32(&b_turn[h ^ 1]));
           }
           __syncwarp();
           if (more) step();
