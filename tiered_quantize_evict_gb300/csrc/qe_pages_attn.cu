@@ -15,9 +15,9 @@
 // finished by its CTA; one that is cut leaves (M, sum, accumulator) parts that the join kernel merges.  The line is computed
 // from the lengths on the device by every CTA alike (a sum of floors in closed form per sequence).
 //
-// CTA: 12 warps.  Warps 0-3 and 4-7: softmax of half 0 and 1, a thread per row (with NH = 1 the second four idle).
-// Warp 8: TMA of keys and values, page by page, into a ring of slots.  Warps 9, 10: tensor-core issue of half 0 and 1.
-// Warp 11: tensor memory, TMA of the queries.
+// CTA: 8 softmax warps per half, two threads per row (one for each 64 keys of a block: the softmax of a half has to fit under
+// the products of the other), then a warp each for TMA of keys and values (page by page, into a ring of slots), tensor-core
+// issue of half 0 and of half 1, and TMA of the queries.
 //  * S = Q K^T (M 128, N 128): both operands in shared memory, 128-byte swizzle, K-major.
 //  * P overwrites its S in tensor memory in the pool's type; O += P V (N = head_dim) takes P from there and V as the
 //    MN-major operand (its rows are tokens).
@@ -26,7 +26,8 @@
 //  * P is rounded to the pool's type (the tensor cores' operand): a relative 2^-9 (bf16), 2^-12 (fp16) per probability at
 //    most half a step, as the result itself is; the sum is of the unrounded ones.
 // mbarriers: kfull / kempty per slot, qfull / qempty per query buffer, s[i] (S i complete; tensor-core commit),
-// p[i][0], p[i][1] (P i's first and second half of the keys written; one arrival per softmax warp), o[h] (the P V before it complete).  Every wait is bounded (0.2 s); one that expires sets
+// p[i][0], p[i][1] (P i's first and second half of the keys written; one arrival per softmax warp), o[h] (the
+// P V before it complete), turn[h] (half h may issue).  Every wait is bounded (0.2 s); one that expires sets
 // QE_PAGES_ERR_TIMEOUT and an abort flag that ends all loops, and the CTA leaves after what it issued has landed.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -39,10 +40,13 @@
 
 namespace qe {
 
-constexpr int PA_THREADS = 384;
 constexpr int PA_BN = 128;                       // keys of a block
 constexpr unsigned long long PA_WAIT_NS = 200000000ull;
 constexpr float PA_LAZY = 8.f;                   // log2 of how far a row's maximum may pass its reference
+
+// threads: 8 softmax warps per half, 4 others
+template <int NH>
+constexpr int PA_THREADS = 256 * NH + 128;
 
 template <int D>
 struct PaShape {
@@ -172,7 +176,7 @@ struct PaStart {
 template <int NH>
 __device__ __noinline__ void pa_find(const PaParams& p, PaStart* out, long long* s_w, long long* s_rem) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int W = PA_THREADS / 32;
+  constexpr int NT = PA_THREADS<NH>, W = NT / 32;
   const int c = blockIdx.x;
   // exclusive prefix of x over the block, and the total
   auto scan = [&](long long x, long long& total) {
@@ -197,7 +201,7 @@ __device__ __noinline__ void pa_find(const PaParams& p, PaStart* out, long long*
   };
   if (tid == 0) out->n = 0;
   long long line = 0, first_pre = 0, first_x = 0;
-  for (int base = 0; base < p.c.n; base += PA_THREADS) {
+  for (int base = 0; base < p.c.n; base += NT) {
     const int i = base + tid;
     const long long x = i < p.c.n ? pa_head_blocks<NH>(p, pa_seq<NH>(p, i, c == 0)) * p.pg.H : 0;
     long long tot;
@@ -217,7 +221,7 @@ __device__ __noinline__ void pa_find(const PaParams& p, PaStart* out, long long*
     return;
   }
   long long at = 0;
-  for (int base = 0; base < p.c.n; base += PA_THREADS) {
+  for (int base = 0; base < p.c.n; base += NT) {
     const int i = base + tid;
     long long pre = first_pre, x = first_x;
     if (base > 0) {
@@ -225,7 +229,7 @@ __device__ __noinline__ void pa_find(const PaParams& p, PaStart* out, long long*
       long long tot;
       pre = at + scan(x, tot);
       at += tot;
-    } else if (p.c.n > PA_THREADS) {
+    } else if (p.c.n > NT) {
       long long tot;
       scan(x, tot);
       at = tot;
@@ -316,14 +320,12 @@ __device__ __forceinline__ void pa_ld32(unsigned t, unsigned* r) {
       : "r"(t)
       : "memory");
 }
-__device__ __forceinline__ void pa_st32(unsigned t, const unsigned* r) {
+__device__ __forceinline__ void pa_ld16(unsigned t, unsigned* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
-      "%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
-      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
-      "r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(t)
       : "memory");
 }
 __device__ __forceinline__ void pa_st16(unsigned t, const unsigned* r) {
@@ -341,6 +343,18 @@ __device__ __forceinline__ void pa_wait_ld(unsigned* r) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 __device__ __forceinline__ void pa_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// the two warps of a row: barrier, and barrier with the OR of a truth value
+__device__ __forceinline__ void pa_pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool pa_pair_or(int id, bool v) {
+  unsigned r;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbar.red.or.pred p, %2, 64, q;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      : "r"((unsigned)v), "r"(id)
+      : "memory");
+  return r != 0;
+}
 
 struct PaWait {
   const PagesView* pg;
@@ -385,7 +399,7 @@ constexpr unsigned long long PA_DESC_V = (1024ull << 16) | (64ull << 32) | (1ull
 // ---------------------------------------------------------------------------- the kernel
 
 template <int D, int NH, bool FP16>
-__global__ void __launch_bounds__(PA_THREADS, 1)
+__global__ void __launch_bounds__(PA_THREADS<NH>, 1)
     pages_attend_kernel(const __grid_constant__ PaParams p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                         const __grid_constant__ CUtensorMap mv) {
   using Sh = PaShape<D>;
@@ -395,15 +409,17 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   __shared__ unsigned s_tmem;
   __shared__ int s_abort;
   __shared__ PaStart s_start;
-  __shared__ long long s_w[PA_THREADS / 32], s_rem;
+  __shared__ long long s_w[PA_THREADS<NH> / 32], s_rem;
+  __shared__ float s_x[NH][128];      // what the two threads of a row tell each other
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(~0u, tid >> 5, 0), aux = warp - 8 * NH;   // aux: TMA, tensor cores of half 0 and 1, queries
   const unsigned sm = (smem_u32(smem_raw) + 1023) & ~1023u;
   const unsigned sm_q = sm, sm_kv = sm + 2 * Sh::TILE;
   const PaWait wait{&p.pg, &s_abort};
 
   griddep_launch_dependents();
-  if (warp == 11) {
+  if (aux == 3) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -432,9 +448,9 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
   const unsigned tm = s_tmem;
   const int N = s_start.n;
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (N > 0 && warp == 8) {
+  if (aux >= 0) {
+    if (NH == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (N > 0 && aux == 0) {
       // ============================== keys and values
       PaCursor<NH> cur;
       cur.set(p, s_start.i, s_start.h, s_start.j, s_start.b);
@@ -477,10 +493,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       }
       if (!ok && lane == 0)   // leaving early: the copies in flight land first
         for (int i = max(0, issued - NS); i < issued; ++i) wait.drain(smem_u32(&b_kfull[i % NS]), (i / NS) & 1);
-    } else if (N > 0 && warp - 9 < NH) {
+    } else if (N > 0 && aux - 1 < NH) {
       // ============================== tensor cores: a warp per half, so that the waits and the issue of one half pass while
       // the products of the other run.  The whole warp walks the loop (addresses and descriptors stay uniform), one lane issues.
-      const int h = warp - 9;
+      const int h = aux - 1;
       constexpr unsigned FMT = FP16 ? 0u : (1u << 7) | (1u << 10);
       constexpr unsigned ID_S = (1u << 4) | FMT | ((128u >> 3) << 17) | ((128u >> 4) << 24);
       constexpr unsigned ID_O = (1u << 4) | FMT | (1u << 16) | (((unsigned)D >> 3) << 17) | ((128u >> 4) << 24);
@@ -610,7 +626,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       if (pa_elect()) pa_commit(smem_u32(&b_end));   // everything issued is complete before tensor memory goes
       __syncwarp();
       wait.drain(smem_u32(&b_end), 0);
-    } else if (N > 0 && warp == 11) {
+    } else if (N > 0 && aux == 3) {
       // ============================== queries
       if (lane == 0) {
         PaCursor<NH> cur;
@@ -642,180 +658,177 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int half = warp >> 2;
-    if (N > 0 && half < NH) {
-      // ============================== softmax: this thread's row
-      const int r = tid & 127, w4 = warp & 3;
+    if (NH == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    const int half = warp >> 3;
+    if (N > 0) {
+      // ============================== softmax: a row of the half and one half of a block's keys
+      const int w4 = warp & 3, ch = (warp >> 2) & 1, r = w4 * 32 + lane;
       const unsigned lane_off = (unsigned)(w4 * 32) << 16;
-      const unsigned t_o = tm + Sh::TM_O + half * D + lane_off;
+      const unsigned t_o = tm + Sh::TM_O + half * D + ch * (D / 2) + lane_off;   // this thread's half of O's columns
+      const int pair = 1 + half * 4 + w4;                 // named barrier of the two warps of these rows
       PaCursor<NH> cur;
       cur.set(p, s_start.i, s_start.h, s_start.j, s_start.b);
       const int rt = r / p.G, rg = r - rt * p.G;
       int sp = 0, tiles = 0, n = 0;   // (bit i of sp: the parity of s[i])
-      bool ok = true;
+      auto together = [&](float x, auto op) {   // op of the row's two values, the same for both threads
+        if (ch) s_x[half][r] = x;
+        pa_pair_sync(pair);
+        if (!ch) s_x[half][r] = x = op(x, s_x[half][r]);
+        pa_pair_sync(pair);
+        return ch ? s_x[half][r] : x;
+      };
+      // A wait that fails (the CTA is leaving) lets the loops run out without waiting, so that the pairs' barriers stay in step.
 #pragma unroll 1
-      for (; n < N && ok; cur.next_tile(p)) {
-       const int cnt = min(cur.nb - cur.b, N - n);
-       if (NH == 2 && half == 1 && !cur.second_half(p)) {
-         n += cnt;
-         continue;
-       }
-       const int t = (cur.j * NH + half) * p.T + rt;
-       const bool live = rt < p.T && t < cur.q.s.m;
-       const bool any_live = __any_sync(~0u, live);
-       const int len = cur.q.s.len - cur.b * PA_BN;                                                       // keys of the piece on
-       const int vis = (!live ? 0 : (p.causal ? cur.q.s.len - cur.q.s.m + t + 1 : cur.q.s.len)) - cur.b * PA_BN;   // and visible ones
-       const int all_vis = __reduce_min_sync(~0u, vis);   // keys that every row of the warp sees
-       float ref = -INFINITY, sum = 0.f;
-#pragma unroll 1
-       for (int k = 0; k < cnt; ++k, ++n) {
-        const bool first = k == 0;
-        const int sb = NH == 2 ? half : n & 1;
-        ok = __all_sync(~0u, wait(smem_u32(&b_s[sb]), sp >> sb & 1));
-        sp ^= 1 << sb;
-        if (!ok) break;
-        pa_fence_after();
-        const unsigned t_s = tm + sb * 128 + lane_off;
-        if ((k + 1) * PA_BN > len) {
-          // the values behind the sequence's end may be anything: zeros, so that 0 x NaN does not reach the sum
-          const int place = 2 * n + 1, slot = place % NS;
-          ok = __all_sync(~0u, wait(smem_u32(&b_kfull[slot]), (place / NS) & 1));
-          if (!ok) break;
-          if (k * PA_BN + r >= len) {
-            const unsigned row = sm_kv + slot * Sh::TILE + r * 128;
-#pragma unroll 1
-            for (int cb = 0; cb < Sh::CB; ++cb)
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row + cb * 16384 + e * 16), "r"(0) : "memory");
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      for (; n < N; cur.next_tile(p)) {
+        const int cnt = min(cur.nb - cur.b, N - n);
+        if (NH == 2 && half == 1 && !cur.second_half(p)) {
+          n += cnt;
+          continue;
         }
-        if (any_live) {
-          unsigned s[128];
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          auto take_max = [&](int from) {
-            if ((k + 1) * PA_BN > all_vis) {
-              const int left = vis - k * PA_BN;         // visible keys of this block
+        const int t = (cur.j * NH + half) * p.T + rt;
+        const bool live = rt < p.T && t < cur.q.s.m;
+        const bool any_live = __any_sync(~0u, live);
+        const int len = cur.q.s.len - cur.b * PA_BN;      // keys from the first block on; and visible ones, from this thread's half on
+        const int vis = (!live ? 0 : (p.causal ? cur.q.s.len - cur.q.s.m + t + 1 : cur.q.s.len)) - cur.b * PA_BN - ch * 64;
+        const int all_vis = __reduce_min_sync(~0u, vis);
+        float ref = -INFINITY, sum = 0.f;
+#pragma unroll 1
+        for (int k = 0; k < cnt; ++k, ++n) {
+          const int sb = NH == 2 ? half : n & 1;
+          wait(smem_u32(&b_s[sb]), sp >> sb & 1);
+          sp ^= 1 << sb;
+          __syncwarp();
+          pa_fence_after();
+          const unsigned t_s = tm + sb * 128 + lane_off;
+          if (__builtin_expect((k + 1) * PA_BN > len && ch == 0, 0)) {
+            // the values behind the sequence's end may be anything: zeros, so that 0 x NaN does not reach the sum
+            const int place = 2 * n + 1, slot = place % NS;
+            wait(smem_u32(&b_kfull[slot]), (place / NS) & 1);
+            if (k * PA_BN + r >= len) {
+              const unsigned row = sm_kv + slot * Sh::TILE + r * 128;
+#pragma unroll 1
+              for (int cb = 0; cb < Sh::CB; ++cb)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row + cb * 16384 + e * 16), "r"(0) : "memory");
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+          }
+          if (any_live) {
+            unsigned s[64];
+            pa_ld32(t_s + ch * 64, s);
+            pa_ld32(t_s + ch * 64 + 32, s + 32);
+            pa_wait_ld<64>(s);
+            if (__builtin_expect(k * PA_BN + 64 > all_vis, 0)) {
+              const int left = vis - k * PA_BN;           // visible keys of these
 #pragma unroll
               for (int c = 0; c < 64; ++c)
-                if (from + c >= left) s[from + c] = 0xFF800000u;   // -inf, whatever lies there
+                if (c >= left) s[c] = 0xFF800000u;        // -inf, whatever lies there
             }
+            float mx[4];
 #pragma unroll
-            for (int c = from; c < from + 64; c += 8)
+            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 4]));
+#pragma unroll
+            for (int c = 8; c < 64; c += 8)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(s[c + e])), __uint_as_float(s[c + 4 + e]));
-          };
-          // the second half of the columns loads while the first's maximum is taken
-          pa_ld32(t_s, s);
-          pa_ld32(t_s + 32, s + 32);
-          pa_wait_ld<64>(s);
-          pa_ld32(t_s + 64, s + 64);
-          pa_ld32(t_s + 96, s + 96);
-          take_max(0);
-          pa_wait_ld<64>(s + 64);
-          take_max(64);
-          const float m = fmaxf(ref, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-          if (first) {
-            ref = m;
-          } else if (__any_sync(~0u, (m - ref) * p.scale2 > PA_LAZY)) {   // false for -inf - -inf
-            const float f = m == -INFINITY ? 1.f : ex2((ref - m) * p.scale2);
-            ref = m;
-            sum *= f;
-            if constexpr (NH == 1) {   // the P V before this block's may still be running
-              ok = __all_sync(~0u, wait(smem_u32(&b_o[0]), (n - 1) & 1));
-              if (!ok) break;
-              pa_fence_after();
-            }
+            float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            if (__builtin_expect(pa_pair_or(pair, k == 0 || (m - ref) * p.scale2 > PA_LAZY), 0)) {
+              m = together(fmaxf(m, ref), [](float a, float b) { return fmaxf(a, b); });
+              const float f = m == -INFINITY ? 1.f : ex2((ref - m) * p.scale2);
+              ref = m;
+              if (k > 0) {
+                sum *= f;
+                if constexpr (NH == 1) {   // the P V before this block's may still be running
+                  wait(smem_u32(&b_o[0]), (n - 1) & 1);
+                  __syncwarp();
+                  pa_fence_after();
+                }
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              unsigned o[32];
-              pa_ld32(t_o + c * 32, o);
-              pa_wait_ld<32>(o);
+                for (int c = 0; c < D / 2; c += 16) {
+                  unsigned o[16];
+                  pa_ld16(t_o + c, o);
+                  pa_wait_ld<16>(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              pa_st32(t_o + c * 32, o);
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  pa_st16(t_o + c, o);
+                }
+                pa_wait_st();
+                pa_fence_before();
+                pa_pair_sync(pair);   // O is scaled whole before either half of the keys is handed over
+              }
             }
+            const float base = ref == -INFINITY ? 0.f : -ref * p.scale2;
+            const unsigned long long sc2 = f2_pack(p.scale2, p.scale2), ba2 = f2_pack(base, base);
+            unsigned long long acc[2] = {0ull, 0ull};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              unsigned pk[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const unsigned long long x =
+                    f2_fma((unsigned long long)s[c * 32 + 2 * e] | ((unsigned long long)s[c * 32 + 2 * e + 1] << 32), sc2, ba2);
+                const float e0 = ex2(f2_lo(x)), e1 = ex2(f2_hi(x));
+                acc[e & 1] = f2_add(acc[e & 1], f2_pack(e0, e1));
+                pk[e] = pa_pack<FP16>(e0, e1);
+              }
+              pa_st16(t_s + ch * 32 + c * 16, pk);
+            }
+            const unsigned long long a = f2_add(acc[0], acc[1]);
+            sum += f2_lo(a) + f2_hi(a);
+            pa_wait_st();
           }
-          const float base = ref == -INFINITY ? 0.f : -ref * p.scale2;
-          const unsigned long long sc2 = f2_pack(p.scale2, p.scale2), ba2 = f2_pack(base, base);
-          unsigned long long acc[2] = {0ull, 0ull};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            unsigned pk[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const unsigned long long x =
-                  f2_fma((unsigned long long)s[c * 32 + 2 * e] | ((unsigned long long)s[c * 32 + 2 * e + 1] << 32), sc2, ba2);
-              const float e0 = ex2(f2_lo(x)), e1 = ex2(f2_hi(x));
-              acc[e & 1] = f2_add(acc[e & 1], f2_pack(e0, e1));
-              pk[e] = pa_pack<FP16>(e0, e1);
-            }
-            pa_st16(t_s + c * 16, pk);
-            if (c == 1) {   // the first half of the keys can go
-              pa_wait_st();
-              pa_fence_before();
-              __syncwarp();
-              if (lane == 0) pa_arrive(smem_u32(&b_p[sb][0]));
-            }
-          }
-          const unsigned long long a = f2_add(acc[0], acc[1]);
-          sum += f2_lo(a) + f2_hi(a);
-          pa_wait_st();
-        } else if (lane == 0) {
-          pa_arrive(smem_u32(&b_p[sb][0]));
+          pa_fence_before();
+          __syncwarp();
+          if (lane == 0) pa_arrive(smem_u32(&b_p[sb][ch]));
         }
-        pa_fence_before();
-        __syncwarp();
-        if (lane == 0) pa_arrive(smem_u32(&b_p[sb][1]));
-       }
-       if (!ok) break;
 
         // ------------------------------ the tile's end in this piece
-        ok = __all_sync(~0u, wait(smem_u32(&b_o[half]), NH == 2 ? tiles & 1 : (n - 1) & 1));
+        wait(smem_u32(&b_o[half]), NH == 2 ? tiles & 1 : (n - 1) & 1);
         ++tiles;
-        if (!ok) break;
+        __syncwarp();
         pa_fence_after();
-        const bool whole = cnt == cur.nb;
         if (any_live) {
+          sum = together(sum, [](float a, float b) { return a + b; });
+          const bool whole = cnt == cur.nb;
           const int tok = cur.q.s.q0 + t;
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
           const int head = cur.h * p.G + rg;
-          uint16_t* dst = p.out + tok * p.ots + head * p.ohs;
+          uint16_t* dst = p.out + tok * p.ots + head * p.ohs + ch * (D / 2);
           const long long part = (((long long)blockIdx.x * 2 + (cur.b == 0 ? 1 : 0)) * NH + half) * 128 + r;
-          float* po = p.part_o + part * D;
+          float* po = p.part_o + part * D + ch * (D / 2);
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            unsigned o[32];
-            pa_ld32(t_o + c * 32, o);
-            pa_wait_ld<32>(o);
+          for (int c = 0; c < D / 2; c += 16) {
+            unsigned o[16];
+            pa_ld16(t_o + c, o);
+            pa_wait_ld<16>(o);
             if (live && whole) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
+              for (int e = 0; e < 16; e += 8) {
                 uint4 x;
-                x.x = pa_pack<FP16>(__uint_as_float(o[k * 8]) * inv, __uint_as_float(o[k * 8 + 1]) * inv);
-                x.y = pa_pack<FP16>(__uint_as_float(o[k * 8 + 2]) * inv, __uint_as_float(o[k * 8 + 3]) * inv);
-                x.z = pa_pack<FP16>(__uint_as_float(o[k * 8 + 4]) * inv, __uint_as_float(o[k * 8 + 5]) * inv);
-                x.w = pa_pack<FP16>(__uint_as_float(o[k * 8 + 6]) * inv, __uint_as_float(o[k * 8 + 7]) * inv);
-                *reinterpret_cast<uint4*>(dst + c * 32 + k * 8) = x;
+                x.x = pa_pack<FP16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                x.y = pa_pack<FP16>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                x.z = pa_pack<FP16>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                x.w = pa_pack<FP16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                *reinterpret_cast<uint4*>(dst + c + e) = x;
               }
             } else if (live) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<uint4*>(po + c * 32 + k * 4) = make_uint4(o[k * 4], o[k * 4 + 1], o[k * 4 + 2], o[k * 4 + 3]);
+              for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(po + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
-          if (live && whole && p.lse) p.lse[(long long)tok * p.Hq + head] = sum == 0.f ? -INFINITY : ref * p.scale + logf(sum);
-          if (live && !whole) p.part_ml[part] = make_float2(sum == 0.f ? -INFINITY : ref * p.scale2, sum);
+          if (live && whole && p.lse && ch == 0) p.lse[(long long)tok * p.Hq + head] = sum == 0.f ? -INFINITY : ref * p.scale + logf(sum);
+          if (live && !whole && ch == 0) p.part_ml[part] = make_float2(sum == 0.f ? -INFINITY : ref * p.scale2, sum);
+          pa_fence_before();
+          pa_pair_sync(pair);   // O is read whole before the next tile's first P is handed over
         }
-        pa_fence_before();
       }
     }
   }
   __syncthreads();
-  if (warp == 11) {
+  if (aux == 3) {
     pa_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
   }
@@ -901,7 +914,7 @@ static cudaError_t launch_t(const PaParams& p, const CUtensorMap* maps, int devi
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(n_sm);
-  cfg.blockDim = dim3(PA_THREADS);
+  cfg.blockDim = dim3(PA_THREADS<NH>);
   cfg.dynamicSmemBytes = PaShape<D>::SMEM;
   cfg.stream = st;
   cfg.attrs = at;
