@@ -60,6 +60,7 @@ struct PaShape {
 // what a CTA's piece of the line starts with (read by the join kernel)
 struct PaRec {
   long long begin;     // place of the tile's first block on the line
+  long long before;    // where the piece before this one starts
   long long total;     // length of the line
   int pieces;          // CTAs that have a piece
   int nb, b;           // blocks of the tile, and the one the piece starts with
@@ -78,7 +79,7 @@ struct PaParams {
   float scale, scale2;     // of the logits; and times log2(e)
   PaRec* rec;              // [CTAs]
   float2* part_ml;         // [CTAs][2][NH][128]: reference, sum
-  float* part_o;           // [CTAs][2][NH][128][D]
+  float* part_o;           // [CTAs][2][NH][D / 4][128][4]
 };
 
 // ---------------------------------------------------------------------------- the line of blocks
@@ -216,7 +217,7 @@ __device__ __noinline__ void pa_find(const PaParams& p, PaStart* out, long long*
   pieces = pieces < 1 ? 1 : (pieces > gridDim.x ? gridDim.x : pieces);
   const long long p0 = line * c / pieces, p1 = line * (c + 1) / pieces;
   if (c >= pieces || line == 0) {
-    if (tid == 0) p.rec[c] = PaRec{0, 0, 0, 0, 0, 0, 0, 0};
+    if (tid == 0) p.rec[c] = PaRec{0, 0, 0, 0, 0, 0, 0, 0, 0};
     __syncthreads();
     return;
   }
@@ -262,7 +263,7 @@ __device__ __noinline__ void pa_find(const PaParams& p, PaStart* out, long long*
       out->j = lo;
       out->b = b;
       const int tt = NH * p.T;
-      p.rec[c] = PaRec{p0 - b, line, (int)pieces, pa_blocks<NH>(p, q.s, lo), b, q.s.q0 + lo * tt, min(tt, q.s.m - lo * tt), h};
+      p.rec[c] = PaRec{p0 - b, c > 0 ? line * (c - 1) / pieces : 0, line, (int)pieces, pa_blocks<NH>(p, q.s, lo), b, q.s.q0 + lo * tt, min(tt, q.s.m - lo * tt), h};
     }
   }
   __syncthreads();
@@ -319,6 +320,17 @@ __device__ __forceinline__ void pa_ld32(unsigned t, unsigned* r) {
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(t)
       : "memory");
+}
+// 32 bytes to global memory: one store where the address allows it, else two
+__device__ __forceinline__ void pa_store32(uint16_t* dst, const unsigned* r) {
+  if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(r[0], r[1], r[2], r[3]);
+    *reinterpret_cast<uint4*>(dst + 8) = make_uint4(r[4], r[5], r[6], r[7]);
+  }
 }
 __device__ __forceinline__ void pa_ld16(unsigned t, unsigned* r) {
   asm volatile(
@@ -735,7 +747,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
               for (int e = 0; e < 4; ++e)
                 mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(s[c + e])), __uint_as_float(s[c + 4 + e]));
             float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            if (__builtin_expect(pa_pair_or(pair, k == 0 || (m - ref) * p.scale2 > PA_LAZY), 0)) {
+            if (__builtin_expect(k == 0 || pa_pair_or(pair, (m - ref) * p.scale2 > PA_LAZY), 0)) {
               m = together(fmaxf(m, ref), [](float a, float b) { return fmaxf(a, b); });
               const float f = m == -INFINITY ? 1.f : ex2((ref - m) * p.scale2);
               ref = m;
@@ -797,30 +809,26 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
           const int head = cur.h * p.G + rg;
           uint16_t* dst = p.out + tok * p.ots + head * p.ohs + ch * (D / 2);
-          const long long part = (((long long)blockIdx.x * 2 + (cur.b == 0 ? 1 : 0)) * NH + half) * 128 + r;
-          float* po = p.part_o + part * D + ch * (D / 2);
+          const long long part = ((long long)blockIdx.x * 2 + (cur.b == 0 ? 1 : 0)) * NH + half;
+          float* po = p.part_o + (part * (D / 4) + ch * (D / 8)) * 512 + r * 4;
 #pragma unroll 1
-          for (int c = 0; c < D / 2; c += 16) {
-            unsigned o[16];
-            pa_ld16(t_o + c, o);
-            pa_wait_ld<16>(o);
+          for (int c = 0; c < D / 2; c += 32) {
+            unsigned o[32];
+            pa_ld32(t_o + c, o);
+            pa_wait_ld<32>(o);
             if (live && whole) {
 #pragma unroll
-              for (int e = 0; e < 16; e += 8) {
-                uint4 x;
-                x.x = pa_pack<FP16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                x.y = pa_pack<FP16>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                x.z = pa_pack<FP16>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                x.w = pa_pack<FP16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                *reinterpret_cast<uint4*>(dst + c + e) = x;
-              }
+              for (int e = 0; e < 16; ++e) o[e] = pa_pack<FP16>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+              pa_store32(dst + c, o);           // a row's channels: whole 32-byte sectors
+              pa_store32(dst + c + 16, o + 8);
             } else if (live) {
 #pragma unroll
-              for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(po + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              for (int e = 0; e < 8; ++e)       // four channels of 32 rows side by side
+                *reinterpret_cast<uint4*>(po + (c / 4 + e) * 512) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             }
           }
           if (live && whole && p.lse && ch == 0) p.lse[(long long)tok * p.Hq + head] = sum == 0.f ? -INFINITY : ref * p.scale + logf(sum);
-          if (live && !whole && ch == 0) p.part_ml[part] = make_float2(sum == 0.f ? -INFINITY : ref * p.scale2, sum);
+          if (live && !whole && ch == 0) p.part_ml[part * 128 + r] = make_float2(sum == 0.f ? -INFINITY : ref * p.scale2, sum);
           pa_fence_before();
           pa_pair_sync(pair);   // O is read whole before the next tile's first P is handed over
         }
@@ -834,49 +842,72 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
   }
 }
 
-// Joins the parts of the tiles that were cut: block c takes the tile its piece starts inside of, if no earlier piece
-// starts inside of it too.  A warp per row, lanes over the channels.
+// Joins the parts of the tiles that were cut: block (c, y) takes the tile that piece c starts inside of, if no earlier
+// piece starts inside of it too, and of it half y / (D / 16) and 16 channels.  A thread per row; where there are fewer rows than
+// threads, several threads share a row's parts (a decode step cuts a few rows into many).
+constexpr int PJ_THREADS = 128, PJ_CH = 16;
 template <int D, int NH, bool FP16>
-__global__ void __launch_bounds__(512) pages_join_kernel(const __grid_constant__ PaParams p) {
+__global__ void __launch_bounds__(PJ_THREADS) pages_join_kernel(const __grid_constant__ PaParams p) {
+  __shared__ float s_m[PJ_THREADS], s_sum[PJ_THREADS], s_o[PJ_CH][PJ_THREADS];
   griddep_launch_dependents();
   griddep_wait();
-  const int c = blockIdx.x;
+  const int c = blockIdx.x, h = blockIdx.y / (D / PJ_CH), ch = blockIdx.y % (D / PJ_CH) * PJ_CH;
   const PaRec r = p.rec[c];
-  if (r.pieces == 0 || r.b == 0) return;
-  const long long before = r.total * (c - 1) / r.pieces;   // where the piece before starts
-  if (before > r.begin) return;
-  int end = c + 1;   // the pieces [c, end) hold the rest of the tile
-  while (end < r.pieces && r.total * end / r.pieces < r.begin + r.nb) ++end;
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  for (int x = threadIdx.x >> 5; x < r.ntok * p.G; x += blockDim.x >> 5) {
-    const int t = x / p.G, g = x - t * p.G, h = t / p.T, row = (t - h * p.T) * p.G + g;
-    auto part = [&](int q) { return (((long long)q * 2 + (q < c ? 1 : 0)) * NH + h) * 128 + row; };
-    float m = -INFINITY;
-    for (int q = c - 1 + lane; q < end; q += 32) m = fmaxf(m, p.part_ml[part(q)].x);
+  if (r.pieces == 0 || r.b == 0 || r.before > r.begin) return;
+  const int rows = (min(r.ntok, (h + 1) * p.T) - h * p.T) * p.G;
+  if (rows <= 0) return;
+  // the pieces [c, end) hold the rest of the tile
+  const int end = (int)min((long long)r.pieces, ((r.begin + r.nb) * r.pieces + r.total - 1) / r.total);
+  int lg = 0;
+  while ((1 << lg) < rows) ++lg;
+  const int row = threadIdx.x & ((1 << lg) - 1), grp = threadIdx.x >> lg, grps = PJ_THREADS >> lg;
+  auto part = [&](int q) { return ((long long)q * 2 + (q < c ? 1 : 0)) * NH + h; };
+  float m = -INFINITY;
+  for (int q = c - 1 + grp; q < end; q += grps) m = fmaxf(m, p.part_ml[part(q) * 128 + row].x);
+  if (grps > 1) {
+    s_m[threadIdx.x] = m;
+    __syncthreads();
+    for (int g = 0; g < grps; ++g) m = fmaxf(m, s_m[(g << lg) + row]);
+  }
+  float sum = 0.f, o[PJ_CH] = {};
+#pragma unroll 2
+  for (int q = c - 1 + grp; q < end; q += grps) {
+    const float2 ml = p.part_ml[part(q) * 128 + row];
+    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+    sum += ml.y * f;
+    const float4* po = reinterpret_cast<const float4*>(p.part_o + (part(q) * (D / 4) + ch / 4) * 512) + row;
 #pragma unroll
-    for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, k));
-    float sum = 0.f, o[E] = {};
-    if (m != -INFINITY) {
-#pragma unroll 4
-      for (int q = c - 1; q < end; ++q) {
-        const float2 ml = p.part_ml[part(q)];
-        if (ml.x == -INFINITY) continue;
-        const float f = ex2(ml.x - m);
-        sum += ml.y * f;
-        const float* po = p.part_o + part(q) * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += po[e] * f;
+    for (int e = 0; e < PJ_CH / 4; ++e) {
+      const float4 x = po[e * 128];
+      if (f != 0.f) {   // (a part without keys may hold anything)
+        o[4 * e] += x.x * f;
+        o[4 * e + 1] += x.y * f;
+        o[4 * e + 2] += x.z * f;
+        o[4 * e + 3] += x.w * f;
       }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const long long tok = r.tok + t;
-    const int head = r.kvh * p.G + g;
-    unsigned* dst = reinterpret_cast<unsigned*>(p.out + tok * p.ots + head * p.ohs + lane * E);
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) dst[e] = pa_pack<FP16>(o[2 * e] * inv, o[2 * e + 1] * inv);
-    if (p.lse && lane == 0) p.lse[tok * p.Hq + head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
   }
+  if (grps > 1) {
+    s_sum[threadIdx.x] = sum;
+#pragma unroll
+    for (int e = 0; e < PJ_CH; ++e) s_o[e][threadIdx.x] = o[e];
+    __syncthreads();
+    if (grp == 0)
+      for (int g = 1; g < grps; ++g) {
+        sum += s_sum[(g << lg) + row];
+#pragma unroll
+        for (int e = 0; e < PJ_CH; ++e) o[e] += s_o[e][(g << lg) + row];
+      }
+  }
+  if (grp != 0 || row >= rows) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int t = row / p.G, head = r.kvh * p.G + (row - t * p.G);
+  const long long tok = r.tok + h * p.T + t;
+  unsigned x[PJ_CH / 2];
+#pragma unroll
+  for (int e = 0; e < PJ_CH / 2; ++e) x[e] = pa_pack<FP16>(o[2 * e] * inv, o[2 * e + 1] * inv);
+  pa_store32(p.out + tok * p.ots + head * p.ohs + ch, x);
+  if (p.lse && ch == 0) p.lse[tok * p.Hq + head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
 }
 
 // ---------------------------------------------------------------------------- launch
@@ -921,7 +952,8 @@ static cudaError_t launch_t(const PaParams& p, const CUtensorMap* maps, int devi
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, pages_attend_kernel<D, NH, FP16>, p, maps[0], maps[1], maps[2]);
   if (e != cudaSuccess) return e;
-  cfg.blockDim = dim3(512);
+  cfg.gridDim = dim3(n_sm, NH * (D / PJ_CH));
+  cfg.blockDim = dim3(PJ_THREADS);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, pages_join_kernel<D, NH, FP16>, p);
 }
