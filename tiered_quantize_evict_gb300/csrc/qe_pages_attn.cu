@@ -59,13 +59,11 @@ struct PaShape {
 
 // what a CTA's piece of the line starts with (read by the join kernel)
 struct PaRec {
-  long long begin;     // place of the tile's first block on the line
-  long long before;    // where the piece before this one starts
-  long long total;     // length of the line
-  int pieces;          // CTAs that have a piece
-  int nb, b;           // blocks of the tile, and the one the piece starts with
+  long long begin;     // place of the tile on the line; -1: no piece
+  int b;               // block of the tile that the piece starts with
   int tok, ntok;       // the tile's first packed token, and how many
   int kvh;
+  int pieces;          // CTAs that have a piece
 };
 
 struct PaParams {
@@ -75,7 +73,7 @@ struct PaParams {
   uint16_t* out;
   float* lse;
   long long ots, ohs;
-  int Hq, G, T, causal, min_blocks;
+  int Hq, G, T, causal, min_piece;
   float scale, scale2;     // of the logits; and times log2(e)
   PaRec* rec;              // [CTAs]
   float2* part_ml;         // [CTAs][2][NH][128]: reference, sum
@@ -84,28 +82,49 @@ struct PaParams {
 
 // ---------------------------------------------------------------------------- the line of blocks
 
-// sum over i < n of floor((a i + b) / 128): Euclid's recursion on (128, a)
-__device__ __noinline__ unsigned long long floor_sum128(unsigned long long n, unsigned long long a, unsigned long long b) {
-  unsigned long long m = 128, ans = 0;
-  if (n == 0) return 0;
-  while (true) {
-    if (a >= m) {
-      ans += n * (n - 1) / 2 * (a / m);
-      a %= m;
-    }
-    if (b >= m) {
-      ans += n * (b / m);
-      b %= m;
-    }
-    const unsigned long long y = a * n + b;
-    if (y < m) return ans;
-    n = y / m;
-    b = y % m;
-    const unsigned long long z = m;
-    m = a;
-    a = z;
+// sum over i < n of floor((a i + b) / 128), a >= 0, b >= 0.  With i = 128 k + j the term is a k + floor((a j + b) / 128), so it
+// comes down to n <= 128: over a whole period the residues of a j + b are b mod g, + g, + 2 g, ... g times over (g = gcd(a, 128)),
+// which gives the sum in closed form; the rest by Euclid's recursion on (128, a) in 32 bits.
+__device__ __forceinline__ long long floor_sum128(int n, int a, long long b) {
+  long long ans = n * (b >> 7) + (long long)n * (n - 1) / 2 * (a >> 7);
+  a &= 127;
+  const int c = (int)(b & 127);
+  const int q = n >> 7;
+  unsigned r = n & 127;
+  if (q) {
+    const int g = a ? a & -a : 128;
+    ans += 64ll * a * q * (q - 1) + (long long)q * ((127 * a + g) / 2 - 64 + c - (c & (g - 1))) + (long long)r * a * q;
   }
+  unsigned m = 128, x = a, y = c, sum = 0;
+  while (r) {
+    if (x >= m) {
+      sum += r * (r - 1) / 2 * (x / m);
+      x %= m;
+    }
+    if (y >= m) {
+      sum += r * (y / m);
+      y %= m;
+    }
+    const unsigned top = x * r + y;
+    if (top < m) break;
+    r = top / m;
+    y = top % m;
+    const unsigned z = m;
+    m = x;
+    x = z;
+  }
+  return ans + sum;
 }
+
+// quotient of numbers that are mostly small
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
+  return a / b;
+}
+
+// What a tile costs besides its blocks (its queries, its first maximum, its output), in blocks: measured about 3800 cycles, against
+// 2800 of a block.
+constexpr int PA_TILE_COST = 1;
 
 struct PaSeq {
   SeqInfo s;
@@ -125,40 +144,63 @@ __device__ __forceinline__ int pa_blocks(const PaParams& p, const SeqInfo& s, in
   const int end = p.causal ? s.len - s.m + min(s.m, (j + 1) * NH * p.T) : s.len;
   return max(1, (end + PA_BN - 1) >> 7);
 }
-// blocks of the tiles before tile j (j < tiles: those are all whole)
+// length on the line of the tiles before tile j (j < tiles: those are all whole)
 template <int NH>
 __device__ __forceinline__ long long pa_before(const PaParams& p, const SeqInfo& s, int j) {
-  if (!p.causal || j == 0) return (long long)j * max(1, (s.len + PA_BN - 1) >> 7);
+  if (!p.causal || j == 0) return (long long)j * (PA_TILE_COST + max(1, (s.len + PA_BN - 1) >> 7));
   const int tt = NH * p.T, off = s.len - s.m;
   const int none = off < 0 ? min(j, -off / tt) : 0;   // tiles that see no key
-  return none + (long long)floor_sum128(j - none, tt, (long long)off + (long long)(none + 1) * tt + PA_BN - 1);
+  return (long long)j * PA_TILE_COST + none + floor_sum128(j - none, tt, (long long)off + (long long)(none + 1) * tt + PA_BN - 1);
 }
 template <int NH>
-__device__ __forceinline__ long long pa_head_blocks(const PaParams& p, const PaSeq& q) {
-  return q.tiles == 0 ? 0 : pa_before<NH>(p, q.s, q.tiles - 1) + pa_blocks<NH>(p, q.s, q.tiles - 1);
+__device__ __forceinline__ long long pa_head_length(const PaParams& p, const PaSeq& q) {
+  return q.tiles == 0 ? 0 : pa_before<NH>(p, q.s, q.tiles - 1) + PA_TILE_COST + pa_blocks<NH>(p, q.s, q.tiles - 1);
 }
 
-// A place on the line.
+// A place on the line: sequence, KV head, tile, block.  The end of the line is (n, 0, 0, 0).
+struct PaPlace {
+  int i, h, j, b;
+  SeqInfo s;
+  long long rem;      // (while it is being found) how far behind the sequence's start
+};
+
+// A walk from one place to another, tile by tile.
 template <int NH>
 struct PaCursor {
-  int i, h, j, b, nb;   // sequence, KV head, tile, block; blocks of the tile
+  int i, h, j, b, nb;   // the place; blocks of the tile
   PaSeq q;
-  __device__ __forceinline__ void set(const PaParams& p, int i_, int h_, int j_, int b_) {
-    i = i_;
-    h = h_;
-    j = j_;
-    b = b_;
-    q = pa_seq<NH>(p, i, false);
+  int ei, eh, ej, eb;   // where the walk ends
+  __device__ __forceinline__ void set(const PaParams& p, const PaPlace* pl) {
+    i = pl[0].i;
+    h = pl[0].h;
+    j = pl[0].j;
+    b = pl[0].b;
+    ei = pl[1].i;
+    eh = pl[1].h;
+    ej = pl[1].j;
+    eb = pl[1].b;
+    q.s = pl[0].s;
+    q.tiles = (q.s.m + NH * p.T - 1) / (NH * p.T);
     nb = pa_blocks<NH>(p, q.s, j);
   }
+  // blocks left of the tile on this walk; 0: the walk is over
+  __device__ __forceinline__ bool last_tile() const { return i == ei && h == eh && j == ej; }
+  __device__ __forceinline__ int count() const { return last_tile() ? eb - b : nb - b; }
   __device__ __forceinline__ void next_tile(const PaParams& p) {
+    if (last_tile()) {   // the walk is over
+      b = eb;
+      return;
+    }
     b = 0;
     if (++j >= q.tiles) {
       j = 0;
       if (++h >= p.pg.H) {
         h = 0;
         do {
-          if (++i >= p.c.n) return;   // the end of the line
+          if (++i >= p.c.n) {   // the end of the line
+            nb = 0;
+            return;
+          }
           q = pa_seq<NH>(p, i, false);
         } while (q.tiles == 0);
       }
@@ -168,14 +210,9 @@ struct PaCursor {
   __device__ __forceinline__ bool second_half(const PaParams& p) const { return NH == 2 && j * 2 * p.T + p.T < q.s.m; }
 };
 
-struct PaStart {
-  int i, h, j, b;
-  int n;              // blocks of the piece
-};
-
-// Every CTA finds its piece: sums the sequences' blocks, cuts the line, finds the tile its cut falls in.
+// Every CTA finds its piece: sums the sequences' lengths on the line, cuts it, finds the places of its two cuts.
 template <int NH>
-__device__ __noinline__ void pa_find(const PaParams& p, PaStart* out, long long* s_w, long long* s_rem) {
+__device__ __noinline__ void pa_find(const PaParams& p, PaPlace* pl, long long* s_w) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int NT = PA_THREADS<NH>, W = NT / 32;
   const int c = blockIdx.x;
@@ -200,54 +237,57 @@ __device__ __noinline__ void pa_find(const PaParams& p, PaStart* out, long long*
     __syncthreads();
     return before + y - x;
   };
-  if (tid == 0) out->n = 0;
-  long long line = 0, first_pre = 0, first_x = 0;
-  for (int base = 0; base < p.c.n; base += NT) {
-    const int i = base + tid;
-    const long long x = i < p.c.n ? pa_head_blocks<NH>(p, pa_seq<NH>(p, i, c == 0)) * p.pg.H : 0;
+  auto length = [&](int i, bool report, SeqInfo& s) {
+    if (i >= p.c.n) return 0ll;
+    const PaSeq q = pa_seq<NH>(p, i, report);
+    s = q.s;
+    return pa_head_length<NH>(p, q) * p.pg.H;
+  };
+  if (tid < 2) pl[tid].i = p.c.n, pl[tid].h = pl[tid].j = pl[tid].b = 0;
+  SeqInfo s;
+  long long line, x = length(tid, c == 0, s), pre = scan(x, line);
+#pragma unroll 1
+  for (int base = NT; base < p.c.n; base += NT) {   // (more sequences than threads)
     long long tot;
-    const long long pre = scan(x, tot);
-    if (base == 0) {
-      first_pre = pre;
-      first_x = x;
-    }
+    SeqInfo z;
+    scan(length(base + tid, c == 0, z), tot);
     line += tot;
   }
-  long long pieces = line / p.min_blocks;
-  pieces = pieces < 1 ? 1 : (pieces > gridDim.x ? gridDim.x : pieces);
-  const long long p0 = line * c / pieces, p1 = line * (c + 1) / pieces;
+  const long long most = div_ll(line, p.min_piece);
+  const int pieces = most < 1 ? 1 : (most > gridDim.x ? (int)gridDim.x : (int)most);
+  const long long each = div_ll(line, pieces);
+  const int over = (int)(line - each * pieces);
+  const long long cut[2] = {each * c + over * c / pieces, each * (c + 1) + over * (c + 1) / pieces};
   if (c >= pieces || line == 0) {
-    if (tid == 0) p.rec[c] = PaRec{0, 0, 0, 0, 0, 0, 0, 0, 0};
+    if (tid == 0) p.rec[c] = PaRec{-1, 0, 0, 0, 0, 0};
     __syncthreads();
     return;
   }
   long long at = 0;
+#pragma unroll 1
   for (int base = 0; base < p.c.n; base += NT) {
-    const int i = base + tid;
-    long long pre = first_pre, x = first_x;
-    if (base > 0) {
-      x = i < p.c.n ? pa_head_blocks<NH>(p, pa_seq<NH>(p, i, false)) * p.pg.H : 0;
+    if (base > 0) x = length(base + tid, false, s);
+    if (p.c.n > NT) {
       long long tot;
       pre = at + scan(x, tot);
       at += tot;
-    } else if (p.c.n > NT) {
-      long long tot;
-      scan(x, tot);
-      at = tot;
     }
-    if (p0 >= pre && p0 < pre + x) {
-      out->i = i;
-      out->n = (int)(p1 - p0);
-      *s_rem = p0 - pre;
-    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (cut[k] >= pre && cut[k] < pre + x) {
+        pl[k].i = base + tid;
+        pl[k].s = s;
+        pl[k].rem = cut[k] - pre;
+      }
   }
   __syncthreads();
-  if (warp == 0) {
-    const int i = out->i;
-    const PaSeq q = pa_seq<NH>(p, i, false);
-    const long long head = pa_head_blocks<NH>(p, q);
-    long long rem = *s_rem;
-    const int h = (int)(rem / head);
+  if (warp < 2 && pl[warp].i < p.c.n) {
+    PaSeq q;
+    q.s = pl[warp].s;
+    q.tiles = (q.s.m + NH * p.T - 1) / (NH * p.T);
+    const long long head = pa_head_length<NH>(p, q);
+    long long rem = pl[warp].rem;
+    const int h = (int)div_ll(rem, head);
     rem -= h * head;
     int lo = 0, hi = q.tiles;   // the last tile that begins at or before rem: 32 places a round
     while (hi - lo > 1) {
@@ -257,13 +297,14 @@ __device__ __noinline__ void pa_find(const PaParams& p, PaStart* out, long long*
       lo += top * step;
       hi = min(hi, lo + step);
     }
-    const int b = (int)(rem - pa_before<NH>(p, q.s, lo));
+    rem -= pa_before<NH>(p, q.s, lo);
+    const int b = max(0, (int)rem - PA_TILE_COST);   // a cut in what the tile costs besides is one before the tile
     if (lane == 0) {
-      out->h = h;
-      out->j = lo;
-      out->b = b;
+      pl[warp].h = h;
+      pl[warp].j = lo;
+      pl[warp].b = b;
       const int tt = NH * p.T;
-      p.rec[c] = PaRec{p0 - b, c > 0 ? line * (c - 1) / pieces : 0, line, (int)pieces, pa_blocks<NH>(p, q.s, lo), b, q.s.q0 + lo * tt, min(tt, q.s.m - lo * tt), h};
+      if (warp == 0) p.rec[c] = PaRec{cut[0] - rem, b, q.s.q0 + lo * tt, min(tt, q.s.m - lo * tt), h, pieces};
     }
   }
   __syncthreads();
@@ -420,8 +461,8 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
   __shared__ __align__(8) unsigned long long b_kfull[NS], b_kempty[NS], b_qfull[2], b_qempty[2], b_s[2], b_p[2][2], b_o[2], b_turn[2], b_end;
   __shared__ unsigned s_tmem;
   __shared__ int s_abort;
-  __shared__ PaStart s_start;
-  __shared__ long long s_w[PA_THREADS<NH> / 32], s_rem;
+  __shared__ PaPlace s_place[2];
+  __shared__ long long s_w[PA_THREADS<NH> / 32];
   __shared__ float s_x[NH][128];      // what the two threads of a row tell each other
 
   const int tid = threadIdx.x, lane = tid & 31;
@@ -455,17 +496,19 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
   }
   pa_fence_before();
   griddep_wait();
-  pa_find<NH>(p, &s_start, s_w, &s_rem);   // ends with a barrier
+  pa_find<NH>(p, s_place, s_w);   // ends with a barrier
   pa_fence_after();
   const unsigned tm = s_tmem;
-  const int N = s_start.n;
+  // (two cuts that fall into the same place leave an empty piece)
+  const bool work = s_place[0].i < p.c.n && (s_place[0].i != s_place[1].i || s_place[0].h != s_place[1].h || s_place[0].j != s_place[1].j ||
+                                             s_place[0].b != s_place[1].b);
 
   if (aux >= 0) {
     if (NH == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (N > 0 && aux == 0) {
+    if (work && aux == 0) {
       // ============================== keys and values
       PaCursor<NH> cur;
-      cur.set(p, s_start.i, s_start.h, s_start.j, s_start.b);
+      cur.set(p, s_place);
       const int rows = min(p.pg.S, PA_BN);               // tokens of a piece: a page, or a block's part of one
       const int np = PA_BN / rows;
       const int piece = lane % np, cb = lane / np;       // lane -> (page of the block, column block)
@@ -477,14 +520,18 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
         const int g = page_at(p.pg, p.t, cur.q.s.row, key);
         return g < 0 ? p.pg.P : g;
       };
-      int slot = 0, ph = 1, issued = 0;
+      int slot = 0, ph = 1, issued = 0, left = cur.count();
       int page = page_of();
       bool ok = true;
 #pragma unroll 1
-      for (int n = 0; n < N && ok; ++n) {
+      while (left > 0 && ok) {
         const int tk = (cur.b * PA_BN) & (p.pg.S - 1), h = cur.h, now = page;
-        if (++cur.b >= cur.nb) cur.next_tile(p);
-        if (n + 1 < N) page = page_of();                 // the next block's, read ahead
+        ++cur.b;
+        if (--left == 0) {
+          cur.next_tile(p);
+          left = cur.count();
+        }
+        if (left > 0) page = page_of();                  // the next block's, read ahead
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           ok = ok && wait(smem_u32(&b_kempty[slot]), ph);
@@ -505,7 +552,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
       }
       if (!ok && lane == 0)   // leaving early: the copies in flight land first
         for (int i = max(0, issued - NS); i < issued; ++i) wait.drain(smem_u32(&b_kfull[i % NS]), (i / NS) & 1);
-    } else if (N > 0 && aux - 1 < NH) {
+    } else if (work && aux - 1 < NH) {
       // ============================== tensor cores: a warp per half, so that the waits and the issue of one half pass while
       // the products of the other run.  The whole warp walks the loop (addresses and descriptors stay uniform), one lane issues.
       const int h = aux - 1;
@@ -513,10 +560,10 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
       constexpr unsigned ID_S = (1u << 4) | FMT | ((128u >> 3) << 17) | ((128u >> 4) << 24);
       constexpr unsigned ID_O = (1u << 4) | FMT | (1u << 16) | (((unsigned)D >> 3) << 17) | ((128u >> 4) << 24);
       PaCursor<NH> cur;
-      cur.set(p, s_start.i, s_start.h, s_start.j, s_start.b);
+      cur.set(p, s_place);
       // The ring is consumed in its order: K 0, then V n - 1 and K n in turn.
       int slot = 0, ph = 0, pp = 0, qp = 0, tile = 0, left = 0;   // (bit i of pp, qp: the parity of p[i], qfull[i])
-      bool was_first = false, was_last = false, was_mine = false, mine = false, ok = true;
+      bool was_first = false, was_last = false, was_mine = false, mine = false, ok = true, more = true;
       auto step = [&]() {
         if (++slot == NS) {
           slot = 0;
@@ -543,11 +590,12 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
           pa_mma_ts(t_o, tm + sb * 128 + part * 32 + k * 8, b + k * 128, ID_O, acc || k > 0);
       };
 #pragma unroll 1
-      for (int n = 0; n <= N; ++n) {
-        const bool more = n < N, first = left == 0;
-        if (first && more) {
+      for (int n = 0; more; ++n) {
+        const bool first = left == 0;
+        if (first) {
           if (n > 0) cur.next_tile(p);
-          left = min(cur.nb - cur.b, N - n);
+          left = cur.count();
+          more = left > 0;      // one more round for the last P V
           mine = h == 0 || cur.second_half(p);
         }
         const bool last = left == 1;
@@ -567,11 +615,11 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
           }
           if (!__all_sync(~0u, ok)) break;
           const bool do_pv = n > 0 && was_mine, do_qk = more && mine;
-          if (do_pv) ok = wait(smem_u32(&b_p[h][0]), pp);
           // The halves take turns, products of a half in one go: one half's softmax runs under the other's products.  (Left
           // to themselves they interleave, and both softmaxes and then both halves' products run at the same time.)
-          ok = wait(smem_u32(&b_turn[h]), (n & 1) ^ h ^ 1) && ok;
+          ok = wait(smem_u32(&b_turn[h]), (n & 1) ^ h ^ 1);
           if (do_pv) {
+            ok = wait(smem_u32(&b_p[h][0]), pp) && ok;
             pa_fence_after();
             if (pa_elect()) pv(0, h, vslot, !was_first);
             __syncwarp();
@@ -638,15 +686,15 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
       if (pa_elect()) pa_commit(smem_u32(&b_end));   // everything issued is complete before tensor memory goes
       __syncwarp();
       wait.drain(smem_u32(&b_end), 0);
-    } else if (N > 0 && aux == 3) {
+    } else if (work && aux == 3) {
       // ============================== queries
       if (lane == 0) {
         PaCursor<NH> cur;
-        cur.set(p, s_start.i, s_start.h, s_start.j, s_start.b);
+        cur.set(p, s_place);
         int ph[2] = {1, 1}, tile = 0;
         bool sent[2] = {false, false}, ok = true;
 #pragma unroll 1
-        for (int n = 0; n < N && ok;) {
+        for (; ok && cur.count() > 0; cur.next_tile(p)) {
           const int halves = cur.second_half(p) ? 2 : 1;
 #pragma unroll 1
           for (int h = 0; h < halves; ++h) {
@@ -660,9 +708,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
               pa_tma3(sm_q + qb * Sh::TILE + cb * 16384, &mq, cb * 64, cur.h * p.G, cur.q.s.q0 + (cur.j * NH + h) * p.T, full);
             sent[qb] = true;
           }
-          n += cur.nb - cur.b;
           ++tile;
-          cur.next_tile(p);
         }
         if (!ok)
           for (int qb = 0; qb < 2; ++qb)
@@ -672,14 +718,14 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
   } else {
     if (NH == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     const int half = warp >> 3;
-    if (N > 0) {
+    if (work) {
       // ============================== softmax: a row of the half and one half of a block's keys
       const int w4 = warp & 3, ch = (warp >> 2) & 1, r = w4 * 32 + lane;
       const unsigned lane_off = (unsigned)(w4 * 32) << 16;
       const unsigned t_o = tm + Sh::TM_O + half * D + ch * (D / 2) + lane_off;   // this thread's half of O's columns
       const int pair = 1 + half * 4 + w4;                 // named barrier of the two warps of these rows
       PaCursor<NH> cur;
-      cur.set(p, s_start.i, s_start.h, s_start.j, s_start.b);
+      cur.set(p, s_place);
       const int rt = r / p.G, rg = r - rt * p.G;
       int sp = 0, tiles = 0, n = 0;   // (bit i of sp: the parity of s[i])
       auto together = [&](float x, auto op) {   // op of the row's two values, the same for both threads
@@ -691,8 +737,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
       };
       // A wait that fails (the CTA is leaving) lets the loops run out without waiting, so that the pairs' barriers stay in step.
 #pragma unroll 1
-      for (; n < N; cur.next_tile(p)) {
-        const int cnt = min(cur.nb - cur.b, N - n);
+      for (int cnt; (cnt = cur.count()) > 0; cur.next_tile(p)) {
         if (NH == 2 && half == 1 && !cur.second_half(p)) {
           n += cnt;
           continue;
@@ -853,11 +898,15 @@ __global__ void __launch_bounds__(PJ_THREADS) pages_join_kernel(const __grid_con
   griddep_wait();
   const int c = blockIdx.x, h = blockIdx.y / (D / PJ_CH), ch = blockIdx.y % (D / PJ_CH) * PJ_CH;
   const PaRec r = p.rec[c];
-  if (r.pieces == 0 || r.b == 0 || r.before > r.begin) return;
+  if (r.begin < 0 || r.b == 0) return;
+  if (p.rec[c - 1].begin == r.begin && p.rec[c - 1].b > 0) return;
   const int rows = (min(r.ntok, (h + 1) * p.T) - h * p.T) * p.G;
   if (rows <= 0) return;
-  // the pieces [c, end) hold the rest of the tile
-  const int end = (int)min((long long)r.pieces, ((r.begin + r.nb) * r.pieces + r.total - 1) / r.total);
+  int end = c + 1;   // the pieces [c, end) hold the rest of the tile
+  for (int in = PJ_THREADS; in == PJ_THREADS && end < r.pieces; end += in) {
+    const int q = end + threadIdx.x;
+    in = __syncthreads_count(q < r.pieces && p.rec[q].begin == r.begin);
+  }
   int lg = 0;
   while ((1 << lg) < rows) ++lg;
   const int row = threadIdx.x & ((1 << lg) - 1), grp = threadIdx.x >> lg, grps = PJ_THREADS >> lg;
@@ -980,7 +1029,7 @@ cudaError_t launch_pages_attend(const PagesAttendParams& a, int fp16, int device
   const int fit = 128 / p.G;
   const bool one = a.max_q_len > 0 && a.max_q_len <= fit;
   p.T = one ? a.max_q_len : fit;
-  p.min_blocks = 2;
+  p.min_piece = 2;
   const int nh = one ? 1 : 2;
   char* at = static_cast<char*>(ws);
   p.part_o = reinterpret_cast<float*>(at);
