@@ -581,10 +581,11 @@ typedef struct {
  * Deterministic for the same lengths.  n_seqs up to 65536. */
 qe_status qe_pages_attend(const qe_pages* pages, int layer, const qe_page_table* seqs, const qe_chunks* chunks,
                           const qe_pages_attend_args* args, void* workspace, size_t bytes, void* stream);
-qe_status qe_pages_attend_workspace(const qe_pages* pages, size_t* bytes);
+/* Bytes of workspace that qe_pages_attend needs with tables of this size (0 where a row is too short to be split). */
+qe_status qe_pages_attend_workspace(const qe_pages* pages, const qe_page_table* seqs, size_t* bytes);
 
 /* Set the length of n rows (rows[i] to new_len[i], device int32): pages are taken (the lowest free
- * ones, in the order of the call) or given back; a length of 0 frees the row.  Where the page that ends up partly
+ * ones, in the order of the call) or given back; a length of 0 frees the row (new_len NULL: all of them).  Where the page that ends up partly
  * filled is shared, the row gets a copy of its own.  Pages given back are free from the next call on. */
 qe_status qe_pages_resize(const qe_pages* pages, const qe_page_table* seqs, const int* rows, const int* new_len, int n,
                           void* workspace, size_t bytes, void* stream);

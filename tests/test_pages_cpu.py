@@ -11,6 +11,25 @@ from conftest import ROOT
 from oracle import pages as op
 
 
+_P, _I, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
+
+
+class Chunks(ctypes.Structure):
+    _fields_ = [("q_start", _P), ("rows", _P), ("n_seqs", _I), ("total_q", _I)]
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("k_token_stride", _L), ("k_head_stride", _L), ("v_token_stride", _L),
+                ("v_head_stride", _L), ("q", _P), ("q_out", _P), ("q_token_stride", _L), ("q_head_stride", _L),
+                ("q_out_token_stride", _L), ("q_out_head_stride", _L), ("n_q_heads", _I), ("rope", _P), ("positions", _P),
+                ("pos_stride", _L)]
+
+
+class AttendArgs(ctypes.Structure):
+    _fields_ = [("q", _P), ("out", _P), ("lse", _P), ("q_token_stride", _L), ("q_head_stride", _L), ("out_token_stride", _L),
+                ("out_head_stride", _L), ("n_q_heads", _I), ("causal", _I), ("max_q_len", _I), ("scale", ctypes.c_float)]
+
+
 @pytest.fixture(scope="module")
 def paged():
     import tiered_quantize_evict_gb300 as qe
@@ -30,9 +49,9 @@ def env(paged):
         lib = qe.load_library()
         pages = paged._Pages(4096, 8192, 0, 0, 2, 10, 2, 16, 64, 20480, 2048, 1024, 64, 16)
         table = paged._Table(4096, 4096, 4096, 8, 4, 8)
-        chunks = paged._Chunks(4096, None, 2, 5)
-        append = paged._AppendArgs(4096, 4096, 128, 64, 128, 64, 4096, 4096, 256, 64, 256, 64, 4, None, None, 0)
-        attend = paged._AttendArgs(4096, 4096, None, 256, 64, 256, 64, 4, 1, 0, 0.125)
+        chunks = Chunks(4096, None, 2, 5)
+        append = AppendArgs(4096, 4096, 128, 64, 128, 64, 4096, 4096, 256, 64, 256, 64, 4, None, None, 0)
+        attend = AttendArgs(4096, 4096, None, 256, 64, 256, 64, 4, 1, 0, 0.125)
         rope = paged._Rope(64, 0, 1)
 
         def run(self, what, layer=0, ws=4096, nb=1 << 40, n=3, null=()):
@@ -110,10 +129,12 @@ def test_attend_arguments(env, field, value, text):
 
 def test_attend_workspace(env):
     import tiered_quantize_evict_gb300 as qe
-    n = ctypes.c_size_t()
-    st = env.lib.qe_pages_attend_workspace(ctypes.byref(env.pages), ctypes.byref(n))
-    assert st in (qe.QE_OK, qe.QE_ERR_CUDA)     # its size goes by the device
-    assert env.lib.qe_pages_attend_workspace(ctypes.byref(env.pages), None) == qe.QE_ERR_INVALID_ARG
+    n = ctypes.c_size_t(7)
+    ask = lambda: env.lib.qe_pages_attend_workspace(ctypes.byref(env.pages), ctypes.byref(env.table), ctypes.byref(n))  # noqa: E731
+    assert ask() == qe.QE_OK and n.value == 0       # 8 pages of 16 tokens: never split
+    env.table.max_pages, env.table.row_stride = 1000, 1000
+    assert ask() in (qe.QE_OK, qe.QE_ERR_CUDA)      # else its size goes by the device
+    assert env.lib.qe_pages_attend_workspace(ctypes.byref(env.pages), ctypes.byref(env.table), None) == qe.QE_ERR_INVALID_ARG
     refused(env, "resize", "workspace", nb=64)
     refused(env, "fork", "workspace", ws=None)
     refused(env, "compact", "aligned", ws=4100)
@@ -178,8 +199,8 @@ def test_nothing_to_do(env):
 
 def test_structs_match_the_header(paged, tmp_path):
     """Sizes and offsets of the ctypes structs are the C ones."""
-    names = {"qe_pages": paged._Pages, "qe_page_table": paged._Table, "qe_rope": paged._Rope, "qe_chunks": paged._Chunks,
-             "qe_pages_append_args": paged._AppendArgs, "qe_pages_attend_args": paged._AttendArgs}
+    names = {"qe_pages": paged._Pages, "qe_page_table": paged._Table, "qe_rope": paged._Rope, "qe_chunks": Chunks,
+             "qe_pages_append_args": AppendArgs, "qe_pages_attend_args": AttendArgs}
     body = "".join(f'printf("{n} %zu", sizeof({n}));' + "".join(f'printf(" %zu", offsetof({n}, {f[0]}));' for f in c._fields_) + 'printf("\\n");'
                    for n, c in names.items())
     (tmp_path / "s.c").write_text('#include <stdio.h>\n#include "qe.h"\nint main(void) {' + body + "return 0;}")
@@ -187,6 +208,12 @@ def test_structs_match_the_header(paged, tmp_path):
     for line in subprocess.run([str(tmp_path / "s")], capture_output=True, text=True, check=True).stdout.splitlines():
         n, *nums = line.split()
         c = names[n]
+        if n in ("qe_chunks", "qe_pages_append_args", "qe_pages_attend_args"):   # what the binding packs has the same layout
+            packed = {"qe_chunks": paged._CHUNKS, "qe_pages_append_args": paged._APPEND, "qe_pages_attend_args": paged._ATTEND}[n]
+            vals = [0.5 * i if f[1] is ctypes.c_float else i + 1 for i, f in enumerate(c._fields_)]
+            assert packed.size == ctypes.sizeof(c)
+            got = c.from_buffer_copy(packed.pack(*vals))
+            assert [getattr(got, f[0]) for f in c._fields_] == vals
         assert [int(x) for x in nums] == [ctypes.sizeof(c)] + [getattr(c, f[0]).offset for f in c._fields_], n
 
 

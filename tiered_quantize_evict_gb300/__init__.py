@@ -135,7 +135,7 @@ def load_library() -> ctypes.CDLL:
     "qe_restore": ([P, P, ctypes.c_size_t], I),
         "qe_pages_append": ([P, I, P, P, P, P], I),
         "qe_pages_attend": ([P, I, P, P, P, P, S, P], I),
-        "qe_pages_attend_workspace": ([P, P], I),
+        "qe_pages_attend_workspace": ([P, P, P], I),
         "qe_pages_resize": ([P, P, P, P, I, P, S, P], I),
         "qe_pages_fork": ([P, P, P, P, I, P, S, P], I),
         "qe_pages_compact": ([P, P, P, P, P, P, S, P], I),

@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) pages_plan_kernel(const PagesVie
       const int row = FORK ? b[i] : a[i], src = FORK ? a[i] : row;
       bool ok = row >= 0 && row < t.rows && src >= 0 && src < t.rows && ws.owner[row] == i;
       if (ok) {
-        const int old_len = t.kv_len[row], len = FORK ? t.kv_len[src] : b[i];
+        const int old_len = t.kv_len[row], len = FORK ? t.kv_len[src] : (b ? b[i] : 0);
         ok = old_len >= 0 && old_len <= most && len >= 0 && len <= most && !(FORK && old_len != 0);
         if (ok) {
           m.row = row;

@@ -72,6 +72,7 @@ struct PagesPair {
 cudaError_t launch_pages_append(const PagesAppendParams& p, int fp16, int n_sm, cudaStream_t st);
 cudaError_t launch_pages_attend(const PagesAttendParams& p, int fp16, int device, int n_sm, void* ws, cudaStream_t st);
 size_t pages_attend_bytes(int n_sm, int D);
+bool pages_attend_cuts(const PagesView& pg, const TableView& t);   // whether any row of the table may be cut (and needs workspace)
 cudaError_t launch_pages_resize(const PagesView& pg, const TableView& t, const int* rows, const int* new_len, int n, void* ws,
                                 int n_sm, cudaStream_t st);
 cudaError_t launch_pages_fork(const PagesView& pg, const TableView& t, const int* src, const int* dst, int n, void* ws,

@@ -75,7 +75,7 @@ struct PaParams {
   long long ots, ohs;
   int Hq, G, T, causal, min_piece;
   float scale, scale2;     // of the logits; and times log2(e)
-  PaRec* rec;              // [CTAs]
+  PaRec* rec;              // [CTAs]; NULL: no tile is cut
   float2* part_ml;         // [CTAs][2][NH][128]: reference, sum
   float* part_o;           // [CTAs][2][NH][D / 4][128][4]
 };
@@ -125,6 +125,8 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
 // What a tile costs besides its blocks (its queries, its first maximum, its output), in blocks: measured about 3800 cycles, against
 // 2800 of a block.
 constexpr int PA_TILE_COST = 1;
+// A tile of so few blocks is never cut: a block takes a CTA 1.4 us, a join 3 us.
+constexpr int PA_WHOLE = 4;
 
 struct PaSeq {
   SeqInfo s;
@@ -259,7 +261,7 @@ __device__ __noinline__ void pa_find(const PaParams& p, PaPlace* pl, long long* 
   const int over = (int)(line - each * pieces);
   const long long cut[2] = {each * c + over * c / pieces, each * (c + 1) + over * (c + 1) / pieces};
   if (c >= pieces || line == 0) {
-    if (tid == 0) p.rec[c] = PaRec{-1, 0, 0, 0, 0, 0};
+    if (tid == 0 && p.rec) p.rec[c] = PaRec{-1, 0, 0, 0, 0, 0};
     __syncthreads();
     return;
   }
@@ -298,13 +300,14 @@ __device__ __noinline__ void pa_find(const PaParams& p, PaPlace* pl, long long* 
       hi = min(hi, lo + step);
     }
     rem -= pa_before<NH>(p, q.s, lo);
-    const int b = max(0, (int)rem - PA_TILE_COST);   // a cut in what the tile costs besides is one before the tile
+    // a cut in what the tile costs besides, or in a short tile, is one before the tile
+    const int b = pa_blocks<NH>(p, q.s, lo) <= PA_WHOLE ? 0 : max(0, (int)rem - PA_TILE_COST);
     if (lane == 0) {
       pl[warp].h = h;
       pl[warp].j = lo;
       pl[warp].b = b;
       const int tt = NH * p.T;
-      if (warp == 0) p.rec[c] = PaRec{cut[0] - rem, b, q.s.q0 + lo * tt, min(tt, q.s.m - lo * tt), h, pieces};
+      if (warp == 0 && p.rec) p.rec[c] = PaRec{cut[0] - rem, b, q.s.q0 + lo * tt, min(tt, q.s.m - lo * tt), h, pieces};
     }
   }
   __syncthreads();
@@ -961,6 +964,8 @@ __global__ void __launch_bounds__(PJ_THREADS) pages_join_kernel(const __grid_con
 
 // ---------------------------------------------------------------------------- launch
 
+bool pages_attend_cuts(const PagesView& pg, const TableView& t) { return ((long long)t.cols << pg.lgS) > PA_WHOLE * PA_BN; }
+
 // parts of NH halves of 128 rows, two per CTA; records
 size_t pages_attend_bytes(int n_sm, int D) {
   return (size_t)n_sm * (sizeof(PaRec) + 2 * 2 * 128 * (sizeof(float2) + sizeof(float) * D)) + 64;
@@ -1000,7 +1005,7 @@ static cudaError_t launch_t(const PaParams& p, const CUtensorMap* maps, int devi
   cfg.attrs = at;
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, pages_attend_kernel<D, NH, FP16>, p, maps[0], maps[1], maps[2]);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || !p.rec) return e;   // no tile is cut
   cfg.gridDim = dim3(n_sm, NH * (D / PJ_CH));
   cfg.blockDim = dim3(PJ_THREADS);
   cfg.dynamicSmemBytes = 0;
@@ -1031,12 +1036,14 @@ cudaError_t launch_pages_attend(const PagesAttendParams& a, int fp16, int device
   p.T = one ? a.max_q_len : fit;
   p.min_piece = 2;
   const int nh = one ? 1 : 2;
-  char* at = static_cast<char*>(ws);
-  p.part_o = reinterpret_cast<float*>(at);
-  at += (size_t)n_sm * 2 * nh * 128 * g.D * sizeof(float);
-  p.part_ml = reinterpret_cast<float2*>(at);
-  at += (size_t)n_sm * 2 * nh * 128 * sizeof(float2);
-  p.rec = reinterpret_cast<PaRec*>(at);
+  if (pages_attend_cuts(g, a.t)) {
+    char* at = static_cast<char*>(ws);
+    p.part_o = reinterpret_cast<float*>(at);
+    at += (size_t)n_sm * 2 * nh * 128 * g.D * sizeof(float);
+    p.part_ml = reinterpret_cast<float2*>(at);
+    at += (size_t)n_sm * 2 * nh * 128 * sizeof(float2);
+    p.rec = reinterpret_cast<PaRec*>(at);
+  }
 
   CUtensorMap maps[3];
   const CUtensorMapDataType ty = fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;

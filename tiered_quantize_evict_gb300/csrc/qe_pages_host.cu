@@ -207,10 +207,14 @@ qe_status qe_pages_append(const qe_pages* pages, int layer, const qe_page_table*
   return launched(qe::launch_pages_append(p, pages->dtype == QE_DTYPE_FP16, n_sm, static_cast<cudaStream_t>(stream)), "qe_pages_append");
 }
 
-qe_status qe_pages_attend_workspace(const qe_pages* pages, size_t* bytes) {
+qe_status qe_pages_attend_workspace(const qe_pages* pages, const qe_page_table* seqs, size_t* bytes) {
   qe::PagesView pg{};
+  qe::TableView t{};
   QE_TRY(check_pages(pages, &pg));
+  QE_TRY(check_table(seqs, false, &t));
   if (!bytes) return fail(QE_ERR_INVALID_ARG, "bytes is null");
+  *bytes = 0;
+  if (!qe::pages_attend_cuts(pg, t)) return QE_OK;
   int n_sm = 0;
   QE_TRY(sm_count(pages->device, &n_sm));
   *bytes = qe::pages_attend_bytes(n_sm, pg.D);
@@ -236,7 +240,7 @@ qe_status qe_pages_attend(const qe_pages* pages, int layer, const qe_page_table*
   if (misaligned(a->lse, 4)) return fail(QE_ERR_INVALID_ARG, "lse must be 4-byte aligned");
   int n_sm = 0;
   QE_TRY(sm_count(pages->device, &n_sm));
-  QE_TRY(check_workspace(workspace, bytes, qe::pages_attend_bytes(n_sm, p.pg.D)));
+  if (qe::pages_attend_cuts(p.pg, p.t)) QE_TRY(check_workspace(workspace, bytes, qe::pages_attend_bytes(n_sm, p.pg.D)));
   p.q = static_cast<const uint16_t*>(a->q);
   p.out = static_cast<uint16_t*>(a->out);
   p.lse = a->lse;
@@ -273,7 +277,7 @@ static qe_status manage(const char* name, const qe_pages* pages, const qe_page_t
   QE_TRY(check_table(seqs, true, &t));
   if (n < 0 || n > (1 << 24)) return fail(QE_ERR_INVALID_ARG, "n must be 0 .. 2^24");
   if (n == 0) return QE_OK;
-  if (!a || !b || misaligned(a, 4) || misaligned(b, 4)) return fail(QE_ERR_INVALID_ARG, "index arrays must be non-null and 4-byte aligned");
+  if (!a || (fork && !b) || misaligned(a, 4) || misaligned(b, 4)) return fail(QE_ERR_INVALID_ARG, "index arrays must be non-null and 4-byte aligned");
   QE_TRY(check_workspace(workspace, bytes, qe::pages_manage_bytes(pg.P, t.rows, n)));
   DeviceGuard guard(pages->device);
   if (guard.err != cudaSuccess) return cuda_fail(guard.err, "cudaSetDevice");

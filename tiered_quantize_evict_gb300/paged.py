@@ -11,13 +11,15 @@ and reference counts, ``Rope`` the rotary positions of several axes.  A serving 
 and ``pool.gather(layer, seqs, 0, n)`` gives keys and values as ``QECache.qe_append`` takes them.
 
 Work runs on the current stream of the pool's device; nothing waits for the GPU except ``check``.
-Scratch comes from torch's allocator, call by call, so calls on several streams and captured
-graphs never share it.
+A pool keeps a scratch buffer for each stream it is used on; a call that is captured into a graph
+takes its own from the graph's memory, so neither streams nor graphs share any.
 """
 from __future__ import annotations
 
 import ctypes
 import math
+import struct
+import threading
 from typing import Optional, Sequence
 
 import torch
@@ -27,7 +29,7 @@ from . import QE_ERR_DEVICE, QE_ERR_INVALID_ARG, QEError, load_library
 QE_PAGES_ERR_PAGE, QE_PAGES_ERR_ROW, QE_PAGES_ERR_NO_PAGES, QE_PAGES_ERR_TIMEOUT = 1, 2, 4, 8
 
 _P, _I, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
-_I32 = torch.int32
+_I32, _DENSE = torch.int32, torch.contiguous_format
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 
@@ -45,30 +47,29 @@ class _Rope(ctypes.Structure):
     _fields_ = [("rot_dim", _I), ("halves", _I), ("n_axes", _I), ("axis", ctypes.c_byte * 64), ("inv_freq", ctypes.c_double * 64)]
 
 
-class _Chunks(ctypes.Structure):
-    _fields_ = [("q_start", _P), ("rows", _P), ("n_seqs", _I), ("total_q", _I)]
+# qe_chunks, qe_pages_append_args and qe_pages_attend_args, packed call by call (native sizes and alignment; a ctypes
+# structure costs three times as much to fill)
+_CHUNKS = struct.Struct("@PPii0P")
+_APPEND = struct.Struct("@PPqqqqPPqqqqiPPq0P")
+_ATTEND = struct.Struct("@PPPqqqqiiif0P")
 
-
-class _AppendArgs(ctypes.Structure):
-    _fields_ = [("k", _P), ("v", _P), ("k_token_stride", _L), ("k_head_stride", _L), ("v_token_stride", _L),
-                ("v_head_stride", _L), ("q", _P), ("q_out", _P), ("q_token_stride", _L), ("q_head_stride", _L),
-                ("q_out_token_stride", _L), ("q_out_head_stride", _L), ("n_q_heads", _I), ("rope", _P), ("positions", _P),
-                ("pos_stride", _L)]
-
-
-class _AttendArgs(ctypes.Structure):
-    _fields_ = [("q", _P), ("out", _P), ("lse", _P), ("q_token_stride", _L), ("q_head_stride", _L), ("out_token_stride", _L),
-                ("out_head_stride", _L), ("n_q_heads", _I), ("causal", _I), ("max_q_len", _I), ("scale", ctypes.c_float)]
+try:   # the raw handle without a Stream object around it
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
+_get_device, _capturing = torch.cuda.current_device, torch.cuda.is_current_stream_capturing
 
 
 def _bad(msg: str) -> QEError:
     return QEError(QE_ERR_INVALID_ARG, msg)
 
 
-def _ints(name: str, t: torch.Tensor, device, dims: int = 1):
-    """Checks an int32 index tensor: device, type, contiguous."""
-    if t.dtype is not _I32 or t.device != device or t.dim() != dims or not t.is_contiguous():
-        raise _bad(f"{name} must be a contiguous {dims}-d int32 tensor on {device}")
+def _ints(name: str, t: torch.Tensor, index: int) -> int:
+    """Checks an int32 index tensor (1-d, contiguous, on the device of that index); its length."""
+    if t.dtype is not _I32 or t.get_device() != index or t.dim() != 1 or not t.is_contiguous():
+        raise _bad(f"{name} must be a contiguous 1-d int32 tensor on cuda:{index}")
+    return t.shape[0]
 
 
 class Rope:
@@ -109,16 +110,15 @@ class PageTable:
     """Sequences: table [n_rows][max_pages], kv_len [n_rows], refs [n_pages] (int32; refs where pages are managed)."""
 
     def __init__(self, table: torch.Tensor, kv_len: torch.Tensor, refs: Optional[torch.Tensor] = None):
-        dev = table.device
+        dev = table.get_device()
         if table.dtype is not _I32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
             raise _bad("table must be a 2-d int32 tensor with contiguous rows")
-        _ints("kv_len", kv_len, dev)
-        if kv_len.shape[0] != table.shape[0]:
+        if _ints("kv_len", kv_len, dev) != table.shape[0]:
             raise _bad("kv_len must have one entry per row of table")
         if refs is not None:
             _ints("refs", refs, dev)
         self.table, self.kv_len, self.refs = table, kv_len, refs
-        self.device = dev
+        self._index, self._n_refs = dev, refs.shape[0] if refs is not None else -1
         self._s = _Table(table.data_ptr(), kv_len.data_ptr(), refs.data_ptr() if refs is not None else None, table.stride(0),
                          table.shape[0], table.shape[1])
         self._ref = ctypes.byref(self._s)
@@ -147,16 +147,36 @@ class PagePool:
         self._s = _Pages(k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], k.device.index, *k.shape, st[0], st[1], st[2], st[3],
                          self.err.data_ptr())
         self._ref = ctypes.byref(self._s)
-        n = ctypes.c_size_t()
-        self._check(self._lib.qe_pages_attend_workspace(self._ref, ctypes.byref(n)))
-        self._attend_bytes = n.value
+        self._index, self._scale = k.device.index, 1.0 / math.sqrt(k.shape[4])
+        self._bytes = {}       # workspace sizes by table shape and entries
+        self._kept = {}        # scratch by stream
+        self._lock = threading.Lock()
 
     def _check(self, st: int):
         if st:
             raise QEError(st, self._lib.qe_last_error(None).decode())
 
-    def _stream(self) -> int:
-        return torch.cuda.current_stream(self.device).cuda_stream
+    def _need(self, seqs: PageTable, n: int) -> int:
+        """Bytes of workspace of attend (n < 0) or of managing n entries, with tables of this shape."""
+        key = (seqs._s.n_rows, seqs._s.max_pages, n)
+        need = self._bytes.get(key)
+        if need is None:
+            b = ctypes.c_size_t()
+            if n < 0:
+                self._check(self._lib.qe_pages_attend_workspace(self._ref, seqs._ref, ctypes.byref(b)))
+            else:
+                self._check(self._lib.qe_pages_manage_workspace(self._ref, seqs._ref, n, ctypes.byref(b)))
+            need = self._bytes[key] = b.value
+        return need
+
+    def _scratch(self, need: int, stream: int) -> torch.Tensor:
+        """need bytes for work on this stream (held under the lock until the call is enqueued)."""
+        if _get_device() != self._index or _capturing():
+            return torch.empty(need, dtype=torch.uint8, device=self.device)
+        buf = self._kept.get(stream)
+        if buf is None or buf.shape[0] < need:
+            buf = self._kept[stream] = torch.empty(need, dtype=torch.uint8, device=self.device)
+        return buf
 
     def check(self):
         """Waits for the current stream and raises if a call met a bad page, row or length, or ran out of pages;
@@ -170,27 +190,27 @@ class PagePool:
                                     (QE_PAGES_ERR_TIMEOUT, "a bounded device wait expired")) if bits & b]
             raise QEError(QE_ERR_DEVICE, "; ".join(names))
 
-    def _seqs(self, seqs: PageTable, refs: bool = False):
-        if seqs.device != self.device:
-            raise _bad(f"the page table is on {seqs.device}, the pool on {self.device}")
-        if refs and (seqs.refs is None or seqs.refs.shape[0] != self.n_pages):
-            raise _bad("the page table needs refs with one entry per page of the pool")
+    def _seqs(self, seqs: PageTable):
+        if seqs._index != self._index:
+            raise _bad(f"the page table is on {seqs.table.device}, the pool on {self.device}")
         return seqs._ref
 
     def _chunks(self, q_start, rows, total):
-        _ints("q_start", q_start, self.device)
-        n = q_start.shape[0] - 1
-        if rows is not None:
-            _ints("rows", rows, self.device)
-            if rows.shape[0] != n:
-                raise _bad("q_start must have one entry more than rows")
-        return _Chunks(q_start.data_ptr(), rows.data_ptr() if rows is not None else None, n, total)
+        n = _ints("q_start", q_start, self._index) - 1
+        if rows is None:
+            return _CHUNKS.pack(q_start.data_ptr(), 0, n, total)
+        if _ints("rows", rows, self._index) != n:
+            raise _bad("q_start must have one entry more than rows")
+        return _CHUNKS.pack(q_start.data_ptr(), rows.data_ptr(), n, total)
 
     def _tokens(self, name, t, total, heads):
-        """Checks a [total][heads][head_dim] tensor of the pool's type."""
-        if t.dtype is not self.dtype or t.device != self.device or t.dim() != 3 or t.shape[0] != total or t.shape[2] != self.head_dim \
-                or (heads and t.shape[1] != heads) or t.stride(2) != 1:
-            raise _bad(f"{name} must be a {self.dtype} tensor [{total}, {heads or 'heads'}, {self.head_dim}] on {self.device}, channels contiguous")
+        """Checks a [total][heads][head_dim] tensor of the pool's type; its strides."""
+        if t.dtype is not self.dtype or t.get_device() != self._index or t.shape != (total, heads, self.head_dim):
+            raise _bad(f"{name} must be a {self.dtype} tensor [{total}, {heads}, {self.head_dim}] on {self.device}")
+        st = t.stride()
+        if st[2] != 1:
+            raise _bad(f"{name} must have contiguous channels")
+        return st
 
     # ---------------------------------------------------------------- the path
     def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor, seqs: PageTable, *,
@@ -200,34 +220,34 @@ class PagePool:
 
         k, v [total][n_kv_heads][head_dim], q [total][n_q_heads][head_dim]; q_start int32 [n + 1]; positions int32
         [n_axes][total] (or [total] for one axis), default the cache positions."""
-        total = k.shape[0]
-        self._tokens("k", k, total, self.n_kv_heads)
-        self._tokens("v", v, total, self.n_kv_heads)
-        hq, qp, op, qs, os = 0, None, None, (0, 0), (0, 0)
+        total = k.shape[0] if k.dim() else 0
+        ks = self._tokens("k", k, total, self.n_kv_heads)
+        vs = self._tokens("v", v, total, self.n_kv_heads)
+        hq = qp = op = pp = pst = 0
+        qs = os = (0, 0)
         if q is not None:
-            self._tokens("q", q, total, 0)
-            hq = q.shape[1]
+            hq = q.shape[1] if q.dim() == 3 else 0
+            qs = self._tokens("q", q, total, hq)
             if q_out is None:
-                q_out = torch.empty(total, hq, self.head_dim, dtype=self.dtype, device=self.device)
-            else:
-                self._tokens("q_out", q_out, total, hq)
-            qp, op, qs, os = q.data_ptr(), q_out.data_ptr(), q.stride(), q_out.stride()
+                q_out = torch.empty_like(q, memory_format=_DENSE)
+            os = self._tokens("q_out", q_out, total, hq)
+            qp, op = q.data_ptr(), q_out.data_ptr()
         elif q_out is not None:
             raise _bad("q_out without q")
-        pp, pst = None, 0
         if positions is not None:
             if rope is None:
                 raise _bad("positions without rope")
-            if positions.dtype is not _I32 or positions.device != self.device or positions.shape[-1] != total or \
-                    positions.stride(-1) != 1 and total > 1 or positions.dim() > 2 or \
-                    (positions.shape[0] if positions.dim() == 2 else 1) != rope.n_axes:
+            want = (rope.n_axes, total) if positions.dim() == 2 or rope.n_axes > 1 else (total,)
+            if positions.dtype is not _I32 or positions.get_device() != self._index or positions.shape != want or \
+                    positions.stride(-1) != 1 and total > 1:
                 raise _bad(f"positions must be int32 [{rope.n_axes}, {total}] on {self.device}, tokens contiguous")
-            pp, pst = positions.data_ptr(), positions.stride(0) if positions.dim() == 2 else 0
-        c = self._chunks(q_start, rows, total)
-        ks, vs = k.stride(), v.stride()
-        a = _AppendArgs(k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1], qp, op, qs[0], qs[1], os[0], os[1], hq,
-                        rope._addr if rope is not None else None, pp, pst)
-        self._check(self._lib.qe_pages_append(self._ref, layer, self._seqs(seqs), ctypes.byref(c), ctypes.byref(a), self._stream()))
+            pp, pst = positions.data_ptr(), positions.stride(0)
+        st = self._lib.qe_pages_append(
+            self._ref, layer, self._seqs(seqs), self._chunks(q_start, rows, total),
+            _APPEND.pack(k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1], qp, op, qs[0], qs[1], os[0], os[1], hq,
+                         rope._addr if rope is not None else 0, pp, pst), _raw_stream(self._index))
+        if st:
+            self._check(st)
         return q_out
 
     def attend(self, layer: int, q: torch.Tensor, q_start: torch.Tensor, seqs: PageTable, *, rows: Optional[torch.Tensor] = None,
@@ -235,36 +255,43 @@ class PagePool:
                return_lse: bool = False):
         """qe_pages_attend: q [total][n_q_heads][head_dim] over the rows' cached tokens; returns out, or (out, lse
         [total][n_q_heads] float32) with return_lse.  scale defaults to head_dim ** -0.5."""
-        total, hq = q.shape[0], q.shape[1]
-        self._tokens("q", q, total, 0)
+        total, hq = q.shape[:2] if q.dim() == 3 else (0, 0)
+        qs = self._tokens("q", q, total, hq)
         if out is None:
-            out = torch.empty(total, hq, self.head_dim, dtype=self.dtype, device=self.device)
-        else:
-            self._tokens("out", out, total, hq)
+            out = torch.empty_like(q, memory_format=_DENSE)
+        os = self._tokens("out", out, total, hq)
         lse = torch.empty(total, hq, dtype=torch.float32, device=self.device) if return_lse else None
-        ws = torch.empty(self._attend_bytes, dtype=torch.uint8, device=self.device)
-        c = self._chunks(q_start, rows, total)
-        qs, os = q.stride(), out.stride()
-        a = _AttendArgs(q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else None, qs[0], qs[1], os[0], os[1], hq,
-                        1 if causal else 0, max_q_len, 1.0 / math.sqrt(self.head_dim) if scale is None else scale)
-        self._check(self._lib.qe_pages_attend(self._ref, layer, self._seqs(seqs), ctypes.byref(c), ctypes.byref(a), ws.data_ptr(),
-                                              self._attend_bytes, self._stream()))
+        ref, c = self._seqs(seqs), self._chunks(q_start, rows, total)
+        a = _ATTEND.pack(q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else 0, qs[0], qs[1], os[0], os[1], hq,
+                         1 if causal else 0, max_q_len, self._scale if scale is None else scale)
+        need, stream = self._need(seqs, -1), _raw_stream(self._index)
+        if need:
+            with self._lock:
+                ws = self._scratch(need, stream)
+                st = self._lib.qe_pages_attend(self._ref, layer, ref, c, a, ws.data_ptr(), need, stream)
+        else:
+            st = self._lib.qe_pages_attend(self._ref, layer, ref, c, a, None, 0, stream)
+        if st:
+            self._check(st)
         return (out, lse) if return_lse else out
 
     # ---------------------------------------------------------------- managing pages
-    def _workspace(self, ref, n):
-        b = ctypes.c_size_t()
-        self._check(self._lib.qe_pages_manage_workspace(self._ref, ref, n, ctypes.byref(b)))
-        return torch.empty(b.value, dtype=torch.uint8, device=self.device), b.value
+    def _refs(self, seqs):
+        if seqs._n_refs != self.n_pages:
+            raise _bad("the page table needs refs with one entry per page of the pool")
+        return self._seqs(seqs)
 
     def _manage(self, fn, seqs, a, b, names):
-        ref = self._seqs(seqs, refs=True)
-        _ints(names[0], a, self.device)
-        _ints(names[1], b, self.device)
-        if a.shape[0] != b.shape[0]:
+        ref = self._refs(seqs)
+        n = _ints(names[0], a, self._index)
+        if b is not None and _ints(names[1], b, self._index) != n:
             raise _bad(f"{names[0]} and {names[1]} must have one entry each")
-        ws, nb = self._workspace(ref, a.shape[0])
-        self._check(fn(self._ref, ref, a.data_ptr(), b.data_ptr(), a.shape[0], ws.data_ptr(), nb, self._stream()))
+        need, stream = self._need(seqs, n), _raw_stream(self._index)
+        with self._lock:
+            ws = self._scratch(need, stream)
+            st = fn(self._ref, ref, a.data_ptr(), b.data_ptr() if b is not None else None, n, ws.data_ptr(), need, stream)
+        if st:
+            self._check(st)
 
     def resize(self, seqs: PageTable, rows: torch.Tensor, new_len: torch.Tensor):
         """qe_pages_resize: row rows[i] gets length new_len[i]; pages are taken or given back."""
@@ -272,7 +299,7 @@ class PagePool:
 
     def free(self, seqs: PageTable, rows: torch.Tensor):
         """Free whole rows: qe_pages_resize to length 0."""
-        self.resize(seqs, rows, torch.zeros_like(rows))
+        self._manage(self._lib.qe_pages_resize, seqs, rows, None, ("rows", "new_len"))
 
     def fork(self, seqs: PageTable, src: torch.Tensor, dst: torch.Tensor):
         """qe_pages_fork: empty row dst[i] becomes a copy of row src[i], sharing its full pages."""
@@ -281,43 +308,42 @@ class PagePool:
     def compact(self, seqs: PageTable, *, table_out: Optional[torch.Tensor] = None, refs_out: Optional[torch.Tensor] = None,
                 n_live: Optional[torch.Tensor] = None):
         """qe_pages_compact: live pages move to the front of the pool; in place unless table_out / refs_out are given."""
-        ref = self._seqs(seqs, refs=True)
-        if table_out is not None and (table_out.dtype is not _I32 or table_out.device != self.device or
+        ref = self._refs(seqs)
+        if table_out is not None and (table_out.dtype is not _I32 or table_out.get_device() != self._index or
                                       table_out.shape != seqs.table.shape or table_out.stride() != seqs.table.stride()):
             raise _bad("table_out must be like the page table")
-        if refs_out is not None:
-            _ints("refs_out", refs_out, self.device)
-            if refs_out.shape[0] != self.n_pages:
-                raise _bad("refs_out must have one entry per page")
-        if n_live is not None:
-            _ints("n_live", n_live, self.device)
-            if n_live.shape[0] != 1:
-                raise _bad("n_live must have one entry")
-        ws, nb = self._workspace(ref, 0)
-        self._check(self._lib.qe_pages_compact(self._ref, ref, *(t.data_ptr() if t is not None else None
-                                                                for t in (table_out, refs_out, n_live)), ws.data_ptr(), nb, self._stream()))
+        if refs_out is not None and _ints("refs_out", refs_out, self._index) != self.n_pages:
+            raise _bad("refs_out must have one entry per page")
+        if n_live is not None and _ints("n_live", n_live, self._index) != 1:
+            raise _bad("n_live must have one entry")
+        need, stream = self._need(seqs, 0), _raw_stream(self._index)
+        with self._lock:
+            ws = self._scratch(need, stream)
+            st = self._lib.qe_pages_compact(self._ref, ref, *(t.data_ptr() if t is not None else None for t in (table_out, refs_out, n_live)),
+                                            ws.data_ptr(), need, stream)
+        if st:
+            self._check(st)
 
     def copy(self, src: torch.Tensor, dst: torch.Tensor):
         """qe_pages_copy: page src[i] to page dst[i], all layers."""
-        _ints("src", src, self.device)
-        _ints("dst", dst, self.device)
-        if src.shape[0] != dst.shape[0]:
+        n = _ints("src", src, self._index)
+        if _ints("dst", dst, self._index) != n:
             raise _bad("src and dst must have one entry each")
-        self._check(self._lib.qe_pages_copy(self._ref, src.data_ptr(), dst.data_ptr(), src.shape[0], self._stream()))
+        self._check(self._lib.qe_pages_copy(self._ref, src.data_ptr(), dst.data_ptr(), n, _raw_stream(self._index)))
 
     def gather(self, layer: int, seqs: PageTable, start: int, n_tokens: int, *, rows: Optional[torch.Tensor] = None,
                out: Optional[Sequence[torch.Tensor]] = None):
         """qe_pages_gather: (k, v), each [n_rows][n_kv_heads][n_tokens][head_dim], the layout ``QECache.qe_append`` takes."""
-        n = seqs.table.shape[0]
-        if rows is not None:
-            _ints("rows", rows, self.device)
-            n = rows.shape[0]
+        n = seqs._s.n_rows if rows is None else _ints("rows", rows, self._index)
         shape = (n, self.n_kv_heads, max(0, n_tokens), self.head_dim)
         if out is None:
             out = [torch.empty(shape, dtype=self.dtype, device=self.device) for _ in range(2)]
-        for t in out:
-            if t.dtype is not self.dtype or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
+        k, v = out
+        for t in (k, v):
+            if t.dtype is not self.dtype or t.get_device() != self._index or t.shape != shape or not t.is_contiguous():
                 raise _bad(f"out must be two contiguous {self.dtype} tensors {list(shape)} on {self.device}")
-        self._check(self._lib.qe_pages_gather(self._ref, layer, self._seqs(seqs), rows.data_ptr() if rows is not None else None, n, start,
-                                              n_tokens, out[0].data_ptr(), out[1].data_ptr(), self._stream()))
-        return out[0], out[1]
+        st = self._lib.qe_pages_gather(self._ref, layer, self._seqs(seqs), rows.data_ptr() if rows is not None else None, n, start,
+                                       n_tokens, k.data_ptr(), v.data_ptr(), _raw_stream(self._index))
+        if st:
+            self._check(st)
+        return k, v
