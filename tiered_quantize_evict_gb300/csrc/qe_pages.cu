@@ -76,59 +76,60 @@ __global__ void __launch_bounds__(256) pages_append_kernel(const __grid_constant
     s_cs[t][c] = make_float2(cs, sn);
   }
   __syncthreads();
-  // one item: 8 adjacent channels, or with halves 8 channels of the first half and their partners
+  // A thread keeps one token and one vector (8 adjacent channels; with halves 8 of the first half and their partners) and
+  // walks the heads, so the sines and cosines stay in registers and several heads' loads are in flight.
   const int nv = p.halves ? p.R / 16 + (p.pg.D - p.R) / 8 : p.pg.D / 8;
-  const int Hq = p.q ? p.Hq : 0, heads = Hq + 2 * p.pg.H;
-  for (int i = threadIdx.x; i < nt * heads * nv; i += blockDim.x) {
-    const int th = i / nv, t = th / heads, h = th - t * heads;
-    int v = i - th * nv;
-    if (s_pos[t] == INT_MIN) continue;
-    const uint16_t* src;
-    uint16_t* dst;
-    const long long tok = t0 + t;
-    if (h < Hq) {
-      src = p.q + tok * p.qts + h * p.qhs;
-      dst = p.q_out + tok * p.ots + h * p.ohs;
-    } else {
-      if (s_at[t] < 0) continue;
-      const bool key = h < Hq + p.pg.H;
-      const int kh = h - Hq - (key ? 0 : p.pg.H);
-      src = key ? p.k + tok * p.kts + kh * p.khs : p.v + tok * p.vts + kh * p.vhs;
-      dst = (key ? p.pg.k : p.pg.v) + s_at[t] + kh * p.pg.hs;
-    }
-    const bool rot = h < Hq + p.pg.H;
-    const float2* cs = s_cs[t];
-    if (!p.halves) {
-      uint4 x = *reinterpret_cast<const uint4*>(src + v * 8);
-      if (rot) {
-        unsigned* w = &x.x;
+  const int grp = threadIdx.x / nv, v = threadIdx.x - grp * nv;
+  const int slots = (int)blockDim.x / nv / nt;                 // threads that share a token's heads
+  const int t = grp / slots, h0 = grp - t * slots;
+  if (t >= nt || s_pos[t] == INT_MIN) return;
+  const long long tok = t0 + t;
+  const bool paired = p.halves && v < p.R / 16;
+  const int c0 = paired ? v * 8 : (p.halves ? p.R + (v - p.R / 16) * 8 : v * 8);   // first channel, and its partner's
+  const int c1 = c0 + half;
+  const int angles = paired ? 8 : (p.halves ? 0 : min(4, max(0, half - v * 4)));
+  float2 cs[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (v * 4 + k < half) {
-            const float2 a = pages_unpack<FP16>(w[k]), c = cs[v * 4 + k];
-            w[k] = pages_pack<FP16>(a.x * c.x - a.y * c.y, a.x * c.y + a.y * c.x);
-          }
-      }
-      *reinterpret_cast<uint4*>(dst + v * 8) = x;
-    } else if (v < p.R / 16) {
-      uint4 x = *reinterpret_cast<const uint4*>(src + v * 8);
-      uint4 y = *reinterpret_cast<const uint4*>(src + half + v * 8);
-      if (rot) {
-        unsigned *a = &x.x, *b = &y.x;
+  for (int k = 0; k < 8; ++k) cs[k] = k < angles ? s_cs[t][paired ? c0 + k : v * 4 + k] : make_float2(1.f, 0.f);
+  auto walk = [&](const uint16_t* src, long long shs, uint16_t* dst, long long dhs, int heads, bool rot) {
+    constexpr int DEEP = 4;
+#pragma unroll 1
+    for (int h = h0; h < heads; h += DEEP * slots) {
+      uint4 x[DEEP], y[DEEP];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 xa = pages_unpack<FP16>(a[k]), ya = pages_unpack<FP16>(b[k]);
-          const float2 c0 = cs[v * 8 + 2 * k], c1 = cs[v * 8 + 2 * k + 1];
-          a[k] = pages_pack<FP16>(xa.x * c0.x - ya.x * c0.y, xa.y * c1.x - ya.y * c1.y);
-          b[k] = pages_pack<FP16>(xa.x * c0.y + ya.x * c0.x, xa.y * c1.y + ya.y * c1.x);
+      for (int k = 0; k < DEEP; ++k)
+        if (h + k * slots < heads) {
+          x[k] = *reinterpret_cast<const uint4*>(src + (h + k * slots) * shs + c0);
+          if (paired) y[k] = *reinterpret_cast<const uint4*>(src + (h + k * slots) * shs + c1);
         }
-      }
-      *reinterpret_cast<uint4*>(dst + v * 8) = x;
-      *reinterpret_cast<uint4*>(dst + half + v * 8) = y;
-    } else {   // channels behind the rotated ones
-      v = p.R / 8 + (v - p.R / 16);
-      *reinterpret_cast<uint4*>(dst + v * 8) = *reinterpret_cast<const uint4*>(src + v * 8);
+#pragma unroll
+      for (int k = 0; k < DEEP; ++k)
+        if (h + k * slots < heads) {
+          unsigned *a = &x[k].x, *b = &y[k].x;
+          if (rot && paired) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 xa = pages_unpack<FP16>(a[e]), ya = pages_unpack<FP16>(b[e]), q0 = cs[2 * e], q1 = cs[2 * e + 1];
+              a[e] = pages_pack<FP16>(xa.x * q0.x - ya.x * q0.y, xa.y * q1.x - ya.y * q1.y);
+              b[e] = pages_pack<FP16>(xa.x * q0.y + ya.x * q0.x, xa.y * q1.y + ya.y * q1.x);
+            }
+          } else if (rot) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (e < angles) {
+                const float2 xa = pages_unpack<FP16>(a[e]);
+                a[e] = pages_pack<FP16>(xa.x * cs[e].x - xa.y * cs[e].y, xa.x * cs[e].y + xa.y * cs[e].x);
+              }
+          }
+          *reinterpret_cast<uint4*>(dst + (h + k * slots) * dhs + c0) = x[k];
+          if (paired) *reinterpret_cast<uint4*>(dst + (h + k * slots) * dhs + c1) = y[k];
+        }
     }
+  };
+  if (p.q) walk(p.q + tok * p.qts, p.qhs, p.q_out + tok * p.ots, p.ohs, p.Hq, true);
+  if (s_at[t] >= 0) {
+    walk(p.k + tok * p.kts, p.khs, p.pg.k + s_at[t], p.pg.hs, p.pg.H, true);
+    walk(p.v + tok * p.vts, p.vhs, p.pg.v + s_at[t], p.pg.hs, p.pg.H, false);
   }
 }
 
@@ -306,30 +307,68 @@ __device__ __forceinline__ void ref_down(const PagesView& pg, int* refs, int pag
   }
 }
 
-// Copies of whole or partly used pages: a unit is one head of one page of one layer, of the keys or the values.
+// Rows of head_dim channels, one warp: vector v of 16 bytes is channels 8 (v mod vpr) of row v / vpr.  COPY_DEEP loads per lane
+// are in flight before the first store: memory is what bounds it (measured 6.2 TB/s read and written for 2 GB of pages against
+// 4.9 TB/s with one).
+constexpr int COPY_DEEP = 8;
+__device__ __forceinline__ void copy_rows(const PagesView& pg, const uint16_t* from, uint16_t* to, int vectors) {
+  const int lgv = pg.D == 128 ? 4 : 3, lane = threadIdx.x & 31;
+  for (int v0 = lane; v0 < vectors; v0 += 32 * COPY_DEEP) {
+    uint4 x[COPY_DEEP];
+#pragma unroll
+    for (int k = 0; k < COPY_DEEP; ++k) {
+      const int v = v0 + 32 * k;
+      if (v < vectors) x[k] = *reinterpret_cast<const uint4*>(from + (long long)(v >> lgv) * pg.ts + ((v & ((1 << lgv) - 1)) << 3));
+    }
+#pragma unroll
+    for (int k = 0; k < COPY_DEEP; ++k) {
+      const int v = v0 + 32 * k;
+      if (v < vectors) *reinterpret_cast<uint4*>(to + (long long)(v >> lgv) * pg.ts + ((v & ((1 << lgv) - 1)) << 3)) = x[k];
+    }
+  }
+}
+
+struct CopyUnit {
+  long long item;
+  int l, kv, h;
+};
+// unit u of (item, layer, keys or values, head), heads innermost
+__device__ __forceinline__ CopyUnit copy_unit(long long u, int L, int H) {
+  CopyUnit c;
+  if (u >> 32) {
+    c.h = (int)(u % H);
+    u /= H;
+    c.kv = (int)(u & 1);
+    u >>= 1;
+    c.l = (int)(u % L);
+    c.item = u / L;
+  } else {
+    unsigned x = (unsigned)u;
+    c.h = x % (unsigned)H;
+    x /= (unsigned)H;
+    c.kv = x & 1;
+    x >>= 1;
+    c.l = x % (unsigned)L;
+    c.item = x / (unsigned)L;
+  }
+  return c;
+}
+
+// Copies of whole or partly used pages, a warp per head of a page of a layer, of the keys or the values.
 __device__ void copy_pairs(const PagesView& pg, const PagesPair* pair, const int* src, const int* dst, int n, unsigned bid,
                            unsigned blocks) {
-  const int vpr = pg.D / 8;
+  const unsigned per = blockDim.x >> 5;
   const long long units = (long long)n * pg.L * 2 * pg.H;
-  for (long long u = bid; u < units; u += blocks) {
-    const int h = (int)(u % pg.H);
-    long long r = u / pg.H;
-    const int kv = (int)(r & 1);
-    r >>= 1;
-    const int l = (int)(r % pg.L), i = (int)(r / pg.L);
-    const int s = pair ? pair[i].src : src[i], d = pair ? pair[i].dst : dst[i], rows = pair ? pair[i].rows : pg.S;
+  for (long long u = (long long)bid * per + (threadIdx.x >> 5); u < units; u += (long long)blocks * per) {
+    const CopyUnit c = copy_unit(u, pg.L, pg.H);
+    const int s = pair ? pair[c.item].src : src[c.item], d = pair ? pair[c.item].dst : dst[c.item], rows = pair ? pair[c.item].rows : pg.S;
     if (s < 0 || s >= pg.P || d < 0 || d >= pg.P) {
-      if (threadIdx.x == 0) pages_report(pg, QE_PAGES_ERR_PAGE);
+      if ((threadIdx.x & 31) == 0) pages_report(pg, QE_PAGES_ERR_PAGE);
       continue;
     }
     if (s == d) continue;
-    uint16_t* base = (kv ? pg.v : pg.k) + l * pg.ls + h * pg.hs;
-    const uint16_t* from = base + s * pg.ps;
-    uint16_t* to = base + d * pg.ps;
-    for (int v = threadIdx.x; v < rows * vpr; v += blockDim.x) {
-      const int tk = v / vpr, c = (v - tk * vpr) * 8;
-      *reinterpret_cast<uint4*>(to + tk * pg.ts + c) = *reinterpret_cast<const uint4*>(from + tk * pg.ts + c);
-    }
+    uint16_t* base = (c.kv ? pg.v : pg.k) + c.l * pg.ls + c.h * pg.hs;
+    copy_rows(pg, base + s * pg.ps, base + d * pg.ps, rows * (pg.D / 8));
   }
 }
 
@@ -480,41 +519,47 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const PagesView pg, con
   copy_pairs(pg, nullptr, src, dst, n, blockIdx.x, gridDim.x);
 }
 cudaError_t launch_pages_copy(const PagesView& pg, const int* src, const int* dst, int n, int n_sm, cudaStream_t st) {
-  const long long units = (long long)n * pg.L * 2 * pg.H;
-  const int blocks = (int)(units < n_sm * 8 ? units : n_sm * 8);
-  pages_copy_kernel<<<blocks, 256, 0, st>>>(pg, src, dst, n);
+  const long long blocks = ((long long)n * pg.L * 2 * pg.H + 7) / 8;   // a warp per unit
+  pages_copy_kernel<<<(unsigned)(blocks < n_sm * 8 ? blocks : n_sm * 8), 256, 0, st>>>(pg, src, dst, n);
   return cudaGetLastError();
 }
 
-// a unit is one head of one page's worth of tokens of one row, of the keys or the values
+// a warp per head of one page's worth of tokens of one row, of the keys or the values
 __global__ void __launch_bounds__(256) pages_gather_kernel(const PagesView pg, const TableView t, int layer, const int* rows, int n,
                                                            int start, int n_tok, uint16_t* k, uint16_t* v) {
-  const int first = start >> pg.lgS, last = (start + n_tok - 1) >> pg.lgS, np = last - first + 1, vpr = pg.D / 8;
+  const int first = start >> pg.lgS, np = ((start + n_tok - 1) >> pg.lgS) - first + 1, vpr = pg.D / 8, lane = threadIdx.x & 31;
   const long long units = (long long)n * np * 2 * pg.H;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const int h = (int)(u % pg.H);
-    long long r = u / pg.H;
-    const int kv = (int)(r & 1);
-    r >>= 1;
-    const int j = first + (int)(r % np), s = (int)(r / np);
-    const int row = rows ? rows[s] : s;
-    const int len = row_len(pg, t, row, threadIdx.x == 0);
-    const int p0 = j << pg.lgS;
+  for (long long u = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += (long long)gridDim.x * 8) {
+    const CopyUnit c = copy_unit(u, np, pg.H);
+    const int p0 = (first + c.l) << pg.lgS, s = (int)c.item, row = rows ? rows[s] : s;
+    const int len = row_len(pg, t, row, lane == 0);
     const int page = p0 < len ? page_at(pg, t, row, p0) : -1;
-    const uint16_t* from = (kv ? pg.v : pg.k) + layer * pg.ls + (long long)max(page, 0) * pg.ps + h * pg.hs;
-    uint16_t* to = (kv ? v : k) + ((long long)s * pg.H + h) * n_tok * pg.D;
-    for (int i = threadIdx.x; i < pg.S * vpr; i += blockDim.x) {
-      const int tk = i / vpr, c = (i - tk * vpr) * 8, pos = p0 + tk;
-      if (pos < start || pos >= start + n_tok) continue;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (page >= 0 && pos < len) x = *reinterpret_cast<const uint4*>(from + tk * pg.ts + c);
-      *reinterpret_cast<uint4*>(to + (long long)(pos - start) * pg.D + c) = x;
+    const int a = max(start - p0, 0), b = min(start + n_tok - p0, pg.S);         // the page's tokens that are asked for
+    const int have = page >= 0 ? min(max(len - p0, a), b) : a;                    // and are there
+    const uint16_t* from = (c.kv ? pg.v : pg.k) + layer * pg.ls + (long long)max(page, 0) * pg.ps + c.h * pg.hs + a * pg.ts;
+    uint16_t* to = (c.kv ? v : k) + (((long long)s * pg.H + c.h) * n_tok + (p0 + a - start)) * pg.D;
+    const int lgv = pg.D == 128 ? 4 : 3, all = (b - a) * vpr, some = (have - a) * vpr;
+    for (int v0 = lane; v0 < all; v0 += 32 * COPY_DEEP) {
+      uint4 x[COPY_DEEP];
+#pragma unroll
+      for (int e = 0; e < COPY_DEEP; ++e) {
+        const int i = v0 + 32 * e;
+        x[e] = make_uint4(0, 0, 0, 0);
+        if (i < some) x[e] = *reinterpret_cast<const uint4*>(from + (long long)(i >> lgv) * pg.ts + ((i & (vpr - 1)) << 3));
+      }
+#pragma unroll
+      for (int e = 0; e < COPY_DEEP; ++e) {
+        const int i = v0 + 32 * e;
+        if (i < all) *reinterpret_cast<uint4*>(to + (long long)i * 8) = x[e];
+      }
     }
   }
 }
 cudaError_t launch_pages_gather(const PagesView& pg, const TableView& t, int layer, const int* rows, int n, int start, int n_tok,
                                 uint16_t* k, uint16_t* v, int n_sm, cudaStream_t st) {
-  pages_gather_kernel<<<n_sm * 8, 256, 0, st>>>(pg, t, layer, rows, n, start, n_tok, k, v);
+  const int np = ((start + n_tok - 1) >> pg.lgS) - (start >> pg.lgS) + 1;
+  const long long blocks = ((long long)n * np * 2 * pg.H + 7) / 8;
+  pages_gather_kernel<<<(unsigned)(blocks < n_sm * 8 ? blocks : n_sm * 8), 256, 0, st>>>(pg, t, layer, rows, n, start, n_tok, k, v);
   return cudaGetLastError();
 }
 
