@@ -226,10 +226,9 @@ __device__ int plan_take(const PagesView& pg, const int* refs, int need, int* ta
   return got;
 }
 
-// FORK: row a[i] -> row b[i]; else: row a[i] gets length b[i]
+// FORK: row a[i] -> row b[i]; else: row a[i] gets length b[i] (0 where b is NULL)
 template <bool FORK>
-__global__ void __launch_bounds__(PLAN_THREADS) pages_plan_kernel(const PagesView pg, const TableView t, const int* a, const int* b,
-                                                                  int n, const PlanSpace ws) {
+__device__ void plan_moves(const PagesView& pg, const TableView& t, const int* a, const int* b, int n, const PlanSpace& ws) {
   const long long most = (long long)t.cols << pg.lgS;
   const int tid = threadIdx.x;
   for (int i = tid; i < n; i += PLAN_THREADS) {
@@ -372,12 +371,14 @@ __device__ void copy_pairs(const PagesView& pg, const PagesPair* pair, const int
   }
 }
 
-// The work of a planned resize or fork: table entries, reference counts, lengths, page copies.
-template <bool FORK>
-__global__ void __launch_bounds__(256) pages_apply_kernel(const PagesView pg, const TableView t, int n, const PlanSpace ws) {
+// The work of a planned resize or fork, by block bid of several: table entries, reference counts, lengths, page copies.
+// TEAM threads take a row.
+template <bool FORK, int TEAM>
+__device__ void apply_moves(const PagesView& pg, const TableView& t, int n, const PlanSpace& ws, int bid, int blocks) {
   const PlanHeader head = *ws.head;
   if (!head.go) return;
-  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+  const int tid = threadIdx.x % TEAM, teams = blockDim.x / TEAM;
+  for (int i = bid * teams + threadIdx.x / TEAM; i < n; i += blocks * teams) {
     const PagesRowMove m = ws.mv[i];
     if (m.row < 0) continue;
     int* row = t.table + (long long)m.row * t.stride;
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(256) pages_apply_kernel(const PagesView pg, co
     if (FORK) {
       const int* from = t.table + (long long)m.src * t.stride;
       const int full = m.new_len >> pg.lgS;
-      for (int j = threadIdx.x; j < t.cols; j += blockDim.x) {
+      for (int j = tid; j < t.cols; j += TEAM) {
         int e = -1;
         if (j < full) {
           e = from[j];
@@ -402,12 +403,12 @@ __global__ void __launch_bounds__(256) pages_apply_kernel(const PagesView pg, co
       }
     } else {
       const int edge = min(m.old_len, m.new_len) >> pg.lgS;
-      if (threadIdx.x == 0 && m.copy_page >= 0) {
+      if (tid == 0 && m.copy_page >= 0) {
         ref_down(pg, t.refs, row[edge]);
         row[edge] = m.copy_page;
         t.refs[m.copy_page] = 1;
       }
-      for (int j = min(oldp, newp) + threadIdx.x; j < max(oldp, newp); j += blockDim.x) {
+      for (int j = min(oldp, newp) + tid; j < max(oldp, newp); j += TEAM) {
         if (j >= oldp) {
           const int e = ws.taken[m.first_new + j - oldp];
           row[j] = e;
@@ -418,9 +419,43 @@ __global__ void __launch_bounds__(256) pages_apply_kernel(const PagesView pg, co
         }
       }
     }
-    if (threadIdx.x == 0) t.kv_len[m.row] = m.new_len;
+    if (tid == 0) t.kv_len[m.row] = m.new_len;
   }
-  copy_pairs(pg, ws.pair, nullptr, nullptr, head.n_pairs, blockIdx.x, gridDim.x);
+  copy_pairs(pg, ws.pair, nullptr, nullptr, head.n_pairs, bid, blocks);
+}
+
+// ALL: the planning block does the work too (a call so small that a second launch would cost more: 10 -> 6 us)
+template <bool FORK, bool ALL>
+__global__ void __launch_bounds__(PLAN_THREADS) pages_plan_kernel(const __grid_constant__ PagesView pg, const __grid_constant__ TableView t,
+                                                                  const int* a, const int* b, int n,
+                                                                  const __grid_constant__ PlanSpace ws) {
+  griddep_launch_dependents();
+  plan_moves<FORK>(pg, t, a, b, n, ws);
+  if constexpr (ALL) {
+    __syncthreads();
+    apply_moves<FORK, 32>(pg, t, n, ws, 0, 1);
+  }
+}
+template <bool FORK>
+__global__ void __launch_bounds__(256) pages_apply_kernel(const __grid_constant__ PagesView pg, const __grid_constant__ TableView t, int n,
+                                                          const __grid_constant__ PlanSpace ws) {
+  griddep_wait();
+  apply_moves<FORK, 256>(pg, t, n, ws, blockIdx.x, gridDim.x);
+}
+
+// a launch that may start while the one before it still runs (it waits inside)
+template <class K, class... A>
+static cudaError_t launch_after(K kernel, unsigned blocks, unsigned threads, cudaStream_t st, A... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <bool FORK>
@@ -428,9 +463,15 @@ static cudaError_t launch_planned(const PagesView& pg, const TableView& t, const
                                   cudaStream_t st) {
   PlanSpace s;
   plan_layout(ws, pg.P, t.rows, n, &s);
-  pages_plan_kernel<FORK><<<1, PLAN_THREADS, 0, st>>>(pg, t, a, b, n, s);
-  pages_apply_kernel<FORK><<<n_sm * 8, 256, 0, st>>>(pg, t, n, s);
-  return cudaGetLastError();
+  // at most a page per entry is copied (none where rows are only freed)
+  const long long copied = !FORK && !b ? 0 : (long long)n * pg.L * 2 * pg.H * pg.S * pg.D * 2;
+  if (copied <= 128 * 1024 && (long long)n * t.cols <= 8192) {
+    pages_plan_kernel<FORK, true><<<1, PLAN_THREADS, 0, st>>>(pg, t, a, b, n, s);
+    return cudaGetLastError();
+  }
+  pages_plan_kernel<FORK, false><<<1, PLAN_THREADS, 0, st>>>(pg, t, a, b, n, s);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_after(pages_apply_kernel<FORK>, n_sm * 8, 256, st, pg, t, n, s);
 }
 cudaError_t launch_pages_resize(const PagesView& pg, const TableView& t, const int* rows, const int* new_len, int n, void* ws,
                                 int n_sm, cudaStream_t st) {
@@ -444,6 +485,7 @@ cudaError_t launch_pages_fork(const PagesView& pg, const TableView& t, const int
 // ---------------------------------------------------------------------------- compact
 __global__ void __launch_bounds__(PLAN_THREADS) pages_plan_compact_kernel(const PagesView pg, const TableView t, const PlanSpace ws,
                                                                           int* n_live_out) {
+  griddep_launch_dependents();
   const int tid = threadIdx.x;
   int live = 0;
   for (int i = tid; i < pg.P; i += PLAN_THREADS) live += t.refs[i] > 0;
@@ -482,6 +524,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) pages_plan_compact_kernel(const 
 
 __global__ void __launch_bounds__(256) pages_compact_kernel(const PagesView pg, const TableView t, const PlanSpace ws, int* table_out,
                                                             int* refs_out) {
+  griddep_wait();
   const PlanHeader head = *ws.head;
   const long long nt = (long long)gridDim.x * blockDim.x, id = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   for (long long i = id; i < (long long)t.rows * t.cols; i += nt) {
@@ -510,8 +553,8 @@ cudaError_t launch_pages_compact(const PagesView& pg, const TableView& t, int* t
   PlanSpace s;
   plan_layout(ws, pg.P, t.rows, 0, &s);
   pages_plan_compact_kernel<<<1, PLAN_THREADS, 0, st>>>(pg, t, s, n_live);
-  pages_compact_kernel<<<n_sm * 8, 256, 0, st>>>(pg, t, s, table_out, refs_out);
-  return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_after(pages_compact_kernel, n_sm * 8, 256, st, pg, t, s, table_out, refs_out);
 }
 
 // ---------------------------------------------------------------------------- copy, gather
