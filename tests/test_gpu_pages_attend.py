@@ -114,6 +114,15 @@ def test_few_rows_over_a_long_cache(torch, m, n, hint):
     run(torch, [(m, n)], hq=4, hkv=1, d=128, ps=64, hint=hint)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m,hint", [(1, 1), (3, 3), (16, 16), (16, 0)])
+def test_long_caches_of_several_sequences(torch, d, m, hint):
+    """Every SM walks many blocks, finishes rows and starts others in the middle of them."""
+    rng = np.random.default_rng(d + m)
+    n = 24 if m < 16 else 10
+    run(torch, [(m, int(x)) for x in rng.integers(4000, 9000, n)], hq=4 if m < 16 else 2, hkv=2 if m < 16 else 1, d=d, ps=64, hint=hint, seed=m)
+
+
 @pytest.mark.parametrize("hint", [0, 1])
 def test_many_short_sequences(torch, hint):
     rng = np.random.default_rng(7)

@@ -846,6 +846,9 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
         }
 
         // ------------------------------ the tile's end in this piece
+        // (NH = 1: o has a phase per block, and the last S says that all P V but the last two are complete: the waits are for
+        // each of those in turn, as a parity only tells one phase from the next)
+        if (NH == 1 && n > 1) wait(smem_u32(&b_o[0]), n & 1);
         wait(smem_u32(&b_o[half]), NH == 2 ? tiles & 1 : (n - 1) & 1);
         ++tiles;
         __syncwarp();
