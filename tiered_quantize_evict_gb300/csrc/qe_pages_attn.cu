@@ -23,8 +23,9 @@
 //    MN-major operand (its rows are tokens).
 //  * The reference M is raised only when a row's maximum passes it by 2^8 (then the softmax warps rescale O in tensor
 //    memory); up to that P and the sums are larger than 1, exactly as precise.
-//  * P is rounded to the pool's type (the tensor cores' operand): a relative 2^-9 (bf16), 2^-12 (fp16) per probability at
-//    most half a step, as the result itself is; the sum is of the unrounded ones.
+//  * P is rounded to the pool's type (the tensor cores' operand): off by half a step at most, as the result itself is; the sum
+//    is of the unrounded ones.  With NH = 1, where the tensor cores wait for memory anyway, what the rounding leaves is kept as
+//    a second operand and multiplied too: error against 64 bits 1.45 -> 1.0 times that of the result's own rounding.
 // mbarriers: kfull / kempty per slot, qfull / qempty per query buffer, s[i] (S i complete; tensor-core commit),
 // p[i][0], p[i][1] (P i's first and second half of the keys written; one arrival per softmax warp), o[h] (the
 // P V before it complete), turn[h] (half h may issue).  Every wait is bounded (0.2 s); one that expires sets
@@ -52,8 +53,12 @@ template <int D>
 struct PaShape {
   static constexpr int CB = D / 64;              // column blocks of 128 bytes
   static constexpr int TILE = 128 * D * 2;       // a query buffer, or a slot: 128 rows
-  static constexpr int SLOTS = (7 * 32768 - 2 * TILE) / TILE;
-  static constexpr int SMEM = (2 + SLOTS) * TILE + 1024;
+  static constexpr int ALL = 7 * 32768;          // query buffers and slots together
+  static constexpr int MOST = (ALL - TILE) / TILE;
+  static constexpr int SMEM = ALL + 1024;
+  // Slots beside two query buffers of `rows` rows (64 where a tile has no more, else 128; the products of rows behind read what
+  // lies there and are not used): bound by memory, the ring's depth is what counts (32K decode 347 us with 4 slots, 311 with 5).
+  static constexpr int slots(int rows) { return (ALL - 2 * CB * rows * 128) / TILE; }
   static constexpr int TM_O = 256;               // tensor memory: S0 at column 0, S1 at 128, O0 here, O1 at + D
 };
 
@@ -74,6 +79,7 @@ struct PaParams {
   float* lse;
   long long ots, ohs;
   int Hq, G, T, causal, min_piece;
+  int q_rows;              // rows of a query buffer
   float scale, scale2;     // of the logits; and times log2(e)
   PaRec* rec;              // [CTAs]; NULL: no tile is cut
   float2* part_ml;         // [CTAs][2][NH][128]: reference, sum
@@ -447,6 +453,16 @@ __device__ __forceinline__ unsigned pa_pack(float lo, float hi) {
   return d;
 }
 
+template <bool FP16>
+__device__ __forceinline__ float2 pa_unpack(unsigned x) {
+  if constexpr (FP16) {
+    __half2 h;
+    memcpy(&h, &x, 4);
+    return __half22float2(h);
+  }
+  return make_float2(bf16lo_to_f32(x), bf16hi_to_f32(x));
+}
+
 // shared-memory descriptors: 128-byte swizzle, 8-row groups 1024 bytes apart.  K-major operands (Q, K); and V with
 // channels as the rows of the operand (MN-major: 64 channels to a column block, blocks 128 tokens x 128 bytes apart).
 constexpr unsigned long long PA_DESC_K = (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
@@ -459,9 +475,10 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
     pages_attend_kernel(const __grid_constant__ PaParams p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                         const __grid_constant__ CUtensorMap mv) {
   using Sh = PaShape<D>;
-  constexpr int NS = Sh::SLOTS;
+  const int NS = NH == 1 && p.q_rows == 64 ? Sh::slots(64) : Sh::slots(128);
+  const int q_cb = (NH == 1 ? p.q_rows : 128) * 128, q_buf = Sh::CB * q_cb;   // bytes of a query buffer's column block, and of the buffer
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) unsigned long long b_kfull[NS], b_kempty[NS], b_qfull[2], b_qempty[2], b_s[2], b_p[2][2], b_o[2], b_turn[2], b_end;
+  __shared__ __align__(8) unsigned long long b_kfull[Sh::MOST], b_kempty[Sh::MOST], b_qfull[2], b_qempty[2], b_s[2], b_p[2][2], b_o[2], b_turn[2], b_end;
   __shared__ unsigned s_tmem;
   __shared__ int s_abort;
   __shared__ PaPlace s_place[2];
@@ -471,7 +488,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0), aux = warp - 8 * NH;   // aux: TMA, tensor cores of half 0 and 1, queries
   const unsigned sm = (smem_u32(smem_raw) + 1023) & ~1023u;
-  const unsigned sm_q = sm, sm_kv = sm + 2 * Sh::TILE;
+  const unsigned sm_q = sm, sm_kv = sm + 2 * q_buf;
   const PaWait wait{&p.pg, &s_abort};
 
   griddep_launch_dependents();
@@ -575,12 +592,12 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
       };
       const unsigned t_o = tm + Sh::TM_O + h * D;
       auto qk = [&](int qb, int sb, int kslot, bool q_done) {   // S sb = Q qb K^T (by one lane)
-        const unsigned long long a = PA_DESC_K | ((sm_q + qb * Sh::TILE) >> 4), b = PA_DESC_K | ((sm_kv + kslot * Sh::TILE) >> 4);
+        const unsigned long long a = PA_DESC_K | ((sm_q + qb * q_buf) >> 4), b = PA_DESC_K | ((sm_kv + kslot * Sh::TILE) >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const unsigned o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+          const unsigned o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4, oq = ((k >> 2) * q_cb + (k & 3) * 32) >> 4;
           if (NH == 2 && k == D / 16 - 2) pa_arrive(smem_u32(&b_turn[h ^ 1]));   // (its first product is issued by when these are done)
-          pa_mma_ss(tm + sb * 128, a + o, b + o, ID_S, k > 0);
+          pa_mma_ss(tm + sb * 128, a + oq, b + o, ID_S, k > 0);
         }
         pa_commit(smem_u32(&b_s[sb]));
         pa_commit(smem_u32(&b_kempty[kslot]));
@@ -591,6 +608,9 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
 #pragma unroll
         for (int k = 0; k < PA_BN / 32; ++k)
           pa_mma_ts(t_o, tm + sb * 128 + part * 32 + k * 8, b + k * 128, ID_O, acc || k > 0);
+        if (NH == 1)   // the remainders of P
+#pragma unroll
+          for (int k = 0; k < PA_BN / 32; ++k) pa_mma_ts(t_o, tm + sb * 128 + 64 + part * 32 + k * 8, b + k * 128, ID_O, true);
       };
 #pragma unroll 1
       for (int n = 0; more; ++n) {
@@ -708,7 +728,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
             const unsigned full = smem_u32(&b_qfull[qb]);
             mbar_expect_tx(full, p.T * p.G * 128 * Sh::CB);
             for (int cb = 0; cb < Sh::CB; ++cb)
-              pa_tma3(sm_q + qb * Sh::TILE + cb * 16384, &mq, cb * 64, cur.h * p.G, cur.q.s.q0 + (cur.j * NH + h) * p.T, full);
+              pa_tma3(sm_q + qb * q_buf + cb * q_cb, &mq, cb * 64, cur.h * p.G, cur.q.s.q0 + (cur.j * NH + h) * p.T, full);
             sent[qb] = true;
           }
           ++tile;
@@ -825,7 +845,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
             unsigned long long acc[2] = {0ull, 0ull};
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              unsigned pk[16];
+              unsigned pk[16], rest[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const unsigned long long x =
@@ -833,8 +853,14 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
                 const float e0 = ex2(f2_lo(x)), e1 = ex2(f2_hi(x));
                 acc[e & 1] = f2_add(acc[e & 1], f2_pack(e0, e1));
                 pk[e] = pa_pack<FP16>(e0, e1);
+                if (NH == 1) {
+                  const float2 r = pa_unpack<FP16>(pk[e]);
+                  const unsigned long long d = f2_sub(f2_pack(e0, e1), f2_pack(r.x, r.y));
+                  rest[e] = pa_pack<FP16>(f2_lo(d), f2_hi(d));
+                }
               }
               pa_st16(t_s + ch * 32 + c * 16, pk);
+              if (NH == 1) pa_st16(t_s + 64 + ch * 32 + c * 16, rest);
             }
             const unsigned long long a = f2_add(acc[0], acc[1]);
             sum += f2_lo(a) + f2_hi(a);
@@ -1037,6 +1063,7 @@ cudaError_t launch_pages_attend(const PagesAttendParams& a, int fp16, int device
   const int fit = 128 / p.G;
   const bool one = a.max_q_len > 0 && a.max_q_len <= fit;
   p.T = one ? a.max_q_len : fit;
+  p.q_rows = one && p.T * p.G <= 64 ? 64 : 128;
   p.min_piece = 2;
   const int nh = one ? 1 : 2;
   if (pages_attend_cuts(g, a.t)) {
