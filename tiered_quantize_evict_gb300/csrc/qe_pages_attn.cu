@@ -768,8 +768,9 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
         const int t = (cur.j * NH + half) * p.T + rt;
         const bool live = rt < p.T && t < cur.q.s.m;
         const bool any_live = __any_sync(~0u, live);
-        const int len = cur.q.s.len - cur.b * PA_BN;      // keys from the first block on; and visible ones, from this thread's half on
-        const int vis = (!live ? 0 : (p.causal ? cur.q.s.len - cur.q.s.m + t + 1 : cur.q.s.len)) - cur.b * PA_BN - ch * 64;
+        const int len = cur.q.s.len - cur.b * PA_BN;      // keys from the first block on
+        // and visible ones, from this thread's half on (a lane without a row computes whatever it finds, and nobody reads it)
+        const int vis = !live ? 1 << 30 : (p.causal ? cur.q.s.len - cur.q.s.m + t + 1 : cur.q.s.len) - cur.b * PA_BN - ch * 64;
         const int all_vis = __reduce_min_sync(~0u, vis);
         float ref = -INFINITY, sum = 0.f;
 #pragma unroll 1
@@ -815,7 +816,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
               for (int e = 0; e < 4; ++e)
                 mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(s[c + e])), __uint_as_float(s[c + 4 + e]));
             float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            if (__builtin_expect(k == 0 || pa_pair_or(pair, (m - ref) * p.scale2 > PA_LAZY), 0)) {
+            if (__builtin_expect(k == 0 || pa_pair_or(pair, live && (m - ref) * p.scale2 > PA_LAZY), 0)) {
               m = together(fmaxf(m, ref), [](float a, float b) { return fmaxf(a, b); });
               const float f = m == -INFINITY ? 1.f : ex2((ref - m) * p.scale2);
               ref = m;
