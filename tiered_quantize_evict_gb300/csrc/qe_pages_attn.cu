@@ -371,6 +371,51 @@ __device__ __forceinline__ void pa_ld32(unsigned t, unsigned* r) {
       : "r"(t)
       : "memory");
 }
+// D / 2 columns of 16 lanes: register 4 j + e is (lane T / 4, column 8 j + 2 (T mod 4) + e), 4 j + 2 + e the same of lane 8 + T / 4
+template <int D>
+__device__ __forceinline__ void pa_ld_rows(unsigned t, unsigned* r) {
+  if constexpr (D == 128)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+        "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(t)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(t)
+        : "memory");
+}
+// Among four lanes: u[K q + k] of lane t (q, t < 4, k < K) becomes u[4 k + t] of lane q.
+template <int K>
+__device__ __forceinline__ void pa_quad_transpose(unsigned* u) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 1; s < 4; s <<= 1) {
+    const bool odd = lane & s;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (!(q & s))
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          unsigned &a = u[K * q + k], &b = u[K * (q + s) + k];
+          const unsigned got = __shfl_xor_sync(~0u, odd ? a : b, s);
+          if (odd) a = got;
+          else b = got;
+        }
+  }
+  if constexpr (K == 2) {   // (lane, k) -> (k, lane)
+    const unsigned x[8] = {u[0], u[2], u[4], u[6], u[1], u[3], u[5], u[7]};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = x[i];
+  }
+}
 // 32 bytes to global memory: one store where the address allows it, else two
 __device__ __forceinline__ void pa_store32(uint16_t* dst, const unsigned* r) {
   if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
@@ -886,23 +931,44 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
           const int tok = cur.q.s.q0 + t;
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
           const int head = cur.h * p.G + rg;
-          uint16_t* dst = p.out + tok * p.ots + head * p.ohs + ch * (D / 2);
           const long long part = ((long long)blockIdx.x * 2 + (cur.b == 0 ? 1 : 0)) * NH + half;
-          float* po = p.part_o + (part * (D / 4) + ch * (D / 8)) * 512 + r * 4;
+          if (whole) {
+            // four lanes write a row's 128 (64) bytes side by side, eight rows a store: with a row per lane a store touches 32
+            // lines, and what follows queues behind it (prompts 132 -> 129 us)
+            const unsigned long long at = live ? reinterpret_cast<unsigned long long>(p.out + tok * p.ots + head * p.ohs + ch * (D / 2)) : 0ull;
 #pragma unroll 1
-          for (int c = 0; c < D / 2; c += 32) {
-            unsigned o[32];
-            pa_ld32(t_o + c, o);
-            pa_wait_ld<32>(o);
-            if (live && whole) {
+            for (int g = 0; g < 2; ++g) {
+              unsigned o[D / 4];
+              pa_ld_rows<D>(t_o + ((unsigned)(16 * g) << 16), o);
+              pa_wait_ld<D / 4>(o);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = pa_pack<FP16>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-              pa_store32(dst + c, o);           // a row's channels: whole 32-byte sectors
-              pa_store32(dst + c + 16, o + 8);
-            } else if (live) {
+              for (int up = 0; up < 2; ++up) {
+                const int from = 16 * g + 8 * up + (lane >> 2);
+                const float f = __shfl_sync(~0u, inv, from);
+                const unsigned long long to = __shfl_sync(~0u, at, from);
+                unsigned u[D / 16];                       // unit j: channels 8 j + 2 (lane mod 4), + 1
 #pragma unroll
-              for (int e = 0; e < 8; ++e)       // four channels of 32 rows side by side
-                *reinterpret_cast<uint4*>(po + (c / 4 + e) * 512) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                for (int j = 0; j < D / 16; ++j)
+                  u[j] = pa_pack<FP16>(__uint_as_float(o[4 * j + 2 * up]) * f, __uint_as_float(o[4 * j + 2 * up + 1]) * f);
+                pa_quad_transpose<D / 64>(u);
+                if (to) {
+                  uint16_t* dst = reinterpret_cast<uint16_t*>(to) + (lane & 3) * (D / 8);
+                  if constexpr (D == 128) pa_store32(dst, u);
+                  else *reinterpret_cast<uint4*>(dst) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+              }
+            }
+          } else {
+            float* po = p.part_o + (part * (D / 4) + ch * (D / 8)) * 512 + r * 4;
+#pragma unroll 1
+            for (int c = 0; c < D / 2; c += 32) {
+              unsigned o[32];
+              pa_ld32(t_o + c, o);
+              pa_wait_ld<32>(o);
+              if (live)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)       // four channels of 32 rows side by side
+                  *reinterpret_cast<uint4*>(po + (c / 4 + e) * 512) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             }
           }
           if (live && whole && p.lse && ch == 0) p.lse[(long long)tok * p.Hq + head] = sum == 0.f ? -INFINITY : ref * p.scale + logf(sum);
