@@ -476,6 +476,9 @@ qe_status qe_decode_step_noalloc(qe_handle h, int layer, const void* q, void* ou
  * read on the device when the work runs, so a replayed graph sees their new values.
  * On failure qe_last_error(NULL) has the message (of the calling thread).
  *
+ * Calls on one page table, or that write one pool's pages, are ordered by the caller (one stream,
+ * or events); attention and gathering only read and may overlap.
+ *
  * What the host cannot check is checked on the device: a page index outside [0, n_pages), a row
  * outside [0, n_rows), a length outside [0, max_pages * page_size], a q_start that decreases or
  * passes total_q, a call that needs more free pages than there are.  Such an entry is skipped
@@ -511,7 +514,7 @@ typedef struct {
 
 /* The sequences.  Row r holds the tokens [0, kv_len[r]) of one sequence, on the pages
  * table[r * row_stride + i], i < ceil(kv_len[r] / page_size); entries behind them are -1 after
- * the calls that manage pages.  refs[p] is how many table entries name page p, 0 for a free page
+ * the calls that manage pages.  A row holds at most 2^30 tokens.  refs[p] is how many table entries name page p, 0 for a free page
  * (qe_pages_append, _attend and _gather do not read it; it may be NULL for them).  A page that two rows
  * share is full: the calls below keep it so. */
 typedef struct {
@@ -557,7 +560,7 @@ typedef struct {
 } qe_pages_append_args;
 
 /* Rotate the chunk's queries and keys and write its keys and values to their pages of one
- * layer.  The pages must be there (qe_pages_resize).  Tokens before position 0 (a chunk longer than its
+ * layer.  The pages must be there (qe_pages_resize), and no row may be named twice.  Tokens before position 0 (a chunk longer than its
  * kv_len) have no place in the cache: their queries are rotated (at position NULL: as position 0) and
  * their keys dropped.  Rotation is in float32, rounded once to the pool's type. */
 qe_status qe_pages_append(const qe_pages* pages, int layer, const qe_page_table* seqs, const qe_chunks* chunks,
@@ -598,7 +601,7 @@ qe_status qe_pages_fork(const qe_pages* pages, const qe_page_table* seqs, const 
 
 /* Move the live pages (refs > 0) together: with n_live of them, each live page of index >= n_live goes
  * to the free page of index < n_live of the same rank, all layers, and the tables follow.
- * table_out (rows row_stride apart) and refs_out take the new table and counts; NULL or the old pointers: in place.
+ * table_out (rows row_stride apart) and refs_out take the new table and counts (both NULL, or the old pointers: in place).
  * n_live: device int32, or NULL.  The moved pages' old places keep their contents until they are used again. */
 qe_status qe_pages_compact(const qe_pages* pages, const qe_page_table* seqs, int* table_out, int* refs_out, int* n_live,
                            void* workspace, size_t bytes, void* stream);

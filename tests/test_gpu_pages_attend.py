@@ -188,6 +188,44 @@ def test_bad_pages_rows_and_starts_are_reported(torch):
             pool.check()
 
 
+def test_offsets_past_32_bits(torch):
+    """A pool of 2^31 elements and more: pages at its far end, through every operator."""
+    import tiered_quantize_evict_gb300 as qe
+    from oracle import pages as op
+    H, S, D = 8, 256, 128
+    P = 2 ** 31 // (H * S * D) + 40
+    k = torch.empty(1, P, H, S, D, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    rng = np.random.default_rng(5)
+    table = np.array([[P - 1, P - 3], [P - 8, -1]], np.int32)
+    ints = lambda x: torch.tensor(np.asarray(x, np.int32)).cuda()  # noqa: E731
+    pool, seqs = qe.PagePool(k, v), qe.PageTable(ints(table), ints([300, 20]))
+    kn, vn = (torch.from_numpy(rng.standard_normal((320, H, D), dtype=np.float32)).to(torch.bfloat16) for _ in range(2))
+    starts = ints([0, 300, 320])
+    pool.append(0, kn.cuda(), vn.cuda(), starts, seqs)
+    q = torch.from_numpy(rng.standard_normal((2, H, D), dtype=np.float32)).to(torch.bfloat16)
+    out = pool.attend(0, q.cuda(), ints([0, 1, 2]), seqs)
+    for r, (a, b) in enumerate(((0, 300), (300, 320))):
+        ref, _, spread, _ = op.attend(bits(q[r:r + 1]), bits(kn[a:b]), bits(vn[a:b]), H, D ** -0.5, True)
+        assert (np.abs(bits(out[r:r + 1]) - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -14) * spread).all()
+    gk, gv = pool.gather(0, seqs, 0, 300)
+    assert torch.equal(gk[0].cpu(), kn[:300].transpose(0, 1)) and torch.equal(gv[1, :, :20].cpu(), vn[300:].transpose(0, 1))
+    pool.copy(ints([P - 8]), ints([P - 20]))
+    assert torch.equal(k[0, P - 20, :, :20].cpu(), kn[300:].transpose(0, 1))
+    pool.check()
+
+
+def test_a_row_read_twice(torch):
+    """Two chunks may name one row (the same prefix, two continuations' queries)."""
+    import tiered_quantize_evict_gb300 as qe
+    c = Case(torch, [90, 40], hkv=2, d=64, ps=16)
+    pool, seqs = c.objects(qe)
+    q = c.draw(5, 4, 64).to(c.dev)
+    both = pool.attend(0, q, c.ints([0, 2, 5]), seqs, rows=c.ints([0, 0]))
+    assert torch.equal(both[:2], pool.attend(0, q[:2], c.ints([0, 2]), seqs, rows=c.ints([0])))
+    assert torch.equal(both[2:], pool.attend(0, q[2:], c.ints([0, 3]), seqs, rows=c.ints([0])))
+
+
 def test_captured_and_replayed_with_new_lengths(torch):
     import tiered_quantize_evict_gb300 as qe
     c = Case(torch, [300, 260], hkv=2, d=64, ps=16)

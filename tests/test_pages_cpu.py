@@ -110,7 +110,7 @@ def test_refs_are_needed_where_pages_are_managed(env):
 
 
 @pytest.mark.parametrize("field,value,text", [("q_start", None, "q_start"), ("n_seqs", -1, "n_seqs"), ("n_seqs", 65537, "n_seqs"),
-                                              ("total_q", -1, "total_q"), ("rows", 4098, "aligned")])
+                                              ("total_q", -1, "total_q"), ("total_q", 2 ** 30 + 1, "total_q"), ("rows", 4098, "aligned")])
 def test_chunks_are_checked(env, field, value, text):
     setattr(env.chunks, field, value)
     refused(env, "append", text)
@@ -175,6 +175,13 @@ def test_rope_pairs(env):
 @pytest.mark.parametrize("layer", [-1, 2])
 def test_layer_range(env, what, layer):
     refused(env, what, "layer", layer=layer)
+
+
+def test_compact_outputs_go_together(env):
+    import tiered_quantize_evict_gb300 as qe
+    for t, r in ((4096, None), (None, 4096)):
+        assert env.lib.qe_pages_compact(ctypes.byref(env.pages), ctypes.byref(env.table), t, r, None, 4096, 1 << 40, None) == qe.QE_ERR_INVALID_ARG
+        assert b"together" in env.lib.qe_last_error(None)
 
 
 def test_null_structs(env):

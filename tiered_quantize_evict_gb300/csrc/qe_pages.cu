@@ -229,7 +229,7 @@ __device__ int plan_take(const PagesView& pg, const int* refs, int need, int* ta
 // FORK: row a[i] -> row b[i]; else: row a[i] gets length b[i] (0 where b is NULL)
 template <bool FORK>
 __device__ void plan_moves(const PagesView& pg, const TableView& t, const int* a, const int* b, int n, const PlanSpace& ws) {
-  const long long most = (long long)t.cols << pg.lgS;
+  const long long most = pages_most(pg, t);
   const int tid = threadIdx.x;
   for (int i = tid; i < n; i += PLAN_THREADS) {
     const int row = FORK ? b[i] : a[i];

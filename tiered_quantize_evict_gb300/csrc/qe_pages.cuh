@@ -92,13 +92,19 @@ __device__ __forceinline__ void pages_report(const PagesView& pg, unsigned bit) 
   if (pg.err) atomicOr(pg.err, bit);
 }
 
+// the most tokens a row can have
+__device__ __forceinline__ long long pages_most(const PagesView& pg, const TableView& t) {
+  const long long m = (long long)t.cols << pg.lgS;
+  return m < (1ll << 30) ? m : 1ll << 30;
+}
+
 // Length of a row, within what its table can hold; 0 (reported) for a row that does not exist.
 __device__ __forceinline__ int row_len(const PagesView& pg, const TableView& t, int row, bool report) {
   bool bad = row < 0 || row >= t.rows;
   int len = 0;
   if (!bad) {
     const int x = t.kv_len[row];
-    const long long most = (long long)t.cols << pg.lgS;
+    const long long most = pages_most(pg, t);
     len = x < 0 ? 0 : (x > most ? (int)most : x);
     bad = x != len;
   }

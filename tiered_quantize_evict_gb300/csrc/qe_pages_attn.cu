@@ -536,7 +536,6 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
   const unsigned sm_q = sm, sm_kv = sm + 2 * q_buf;
   const PaWait wait{&p.pg, &s_abort};
 
-  griddep_launch_dependents();
   if (aux == 3) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -561,6 +560,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
   }
   pa_fence_before();
   griddep_wait();
+  griddep_launch_dependents();   // (what follows may then rely on all that ran before this launch)
   pa_find<NH>(p, s_place, s_w);   // ends with a barrier
   pa_fence_after();
   const unsigned tm = s_tmem;
@@ -993,8 +993,8 @@ constexpr int PJ_THREADS = 128, PJ_CH = 16;
 template <int D, int NH, bool FP16>
 __global__ void __launch_bounds__(PJ_THREADS) pages_join_kernel(const __grid_constant__ PaParams p) {
   __shared__ float s_m[PJ_THREADS], s_sum[PJ_THREADS], s_o[PJ_CH][PJ_THREADS];
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   const int c = blockIdx.x, h = blockIdx.y / (D / PJ_CH), ch = blockIdx.y % (D / PJ_CH) * PJ_CH;
   const PaRec r = p.rec[c];
   if (r.begin < 0 || r.b == 0) return;

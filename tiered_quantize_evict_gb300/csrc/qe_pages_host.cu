@@ -110,8 +110,8 @@ qe_status check_table(const qe_page_table* t, bool refs, qe::TableView* o) {
 
 qe_status check_chunks(const qe_chunks* c, qe::ChunksView* o) {
   if (!c) return fail(QE_ERR_INVALID_ARG, "chunks is null");
-  if (c->n_seqs < 0 || c->n_seqs > 65536 || c->total_q < 0)
-    return fail(QE_ERR_INVALID_ARG, "chunks: n_seqs must be 0 .. 65536 and total_q >= 0");
+  if (c->n_seqs < 0 || c->n_seqs > 65536 || c->total_q < 0 || c->total_q > (1 << 30))
+    return fail(QE_ERR_INVALID_ARG, "chunks: n_seqs must be 0 .. 65536 and total_q 0 .. 2^30");
   if (c->n_seqs > 0 && c->total_q > 0 && !c->q_start) return fail(QE_ERR_INVALID_ARG, "chunks: q_start is null");
   if (misaligned(c->q_start, 4) || misaligned(c->rows, 4)) return fail(QE_ERR_INVALID_ARG, "chunks: pointers must be 4-byte aligned");
   *o = qe::ChunksView{c->q_start, c->rows, c->n_seqs, c->total_q};
@@ -307,6 +307,7 @@ qe_status qe_pages_compact(const qe_pages* pages, const qe_page_table* seqs, int
   qe::TableView t{};
   QE_TRY(check_pages(pages, &pg));
   QE_TRY(check_table(seqs, true, &t));
+  if (!table_out != !refs_out) return fail(QE_ERR_INVALID_ARG, "table_out and refs_out go together");
   if (misaligned(table_out, 4) || misaligned(refs_out, 4) || misaligned(n_live, 4))
     return fail(QE_ERR_INVALID_ARG, "outputs must be 4-byte aligned");
   QE_TRY(check_workspace(workspace, bytes, qe::pages_manage_bytes(pg.P, t.rows, 0)));
