@@ -115,7 +115,25 @@ def test_few_rows_over_a_long_cache(torch, m, n, hint):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("m,hint", [(1, 1), (3, 3), (16, 16), (16, 0)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("m,hq,hkv", [(1, 4, 1), (4, 8, 2), (16, 1, 1), (5, 3, 1), (1, 14, 2), (3, 16, 2), (8, 8, 2), (13, 4, 1), (16, 4, 1),
+                                      (9, 14, 2), (1, 128, 1)])
+def test_chunks_of_a_few_tokens(torch, d, dtype, causal, m, hq, hkv):
+    """The longest chunk is named, so tiles have as few rows as it needs: 1 to 16, to 64, to 128; ragged, some without keys."""
+    run(torch, [(m, m), (max(1, m - 1), 300), (m, 1000 + m), (0, 40), (1, 128), (m, max(0, m - 2)), (1, 129), (2 * m + 1, 200)], hq=hq, hkv=hkv, d=d,
+        ps=32, dtype=dtype, causal=causal, hint=m, seed=m + hq)
+
+
+@pytest.mark.parametrize("layout", ["plain", "token_major", "kv_together"])
+@pytest.mark.parametrize("q_layout", ["heads_first", "slice"])
+@pytest.mark.parametrize("ps", [16, 128, 256])
+def test_layouts_of_a_few_tokens(torch, layout, q_layout, ps):
+    run(torch, [(2, 500), (1, 20), (2, 1300)], hq=6, hkv=3, d=64, ps=ps, layout=layout, q_layout=q_layout, layers=2, layer=1, hint=2)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m,hint", [(1, 1), (3, 3), (16, 16), (16, 0), (4, 4), (32, 32)])
 def test_long_caches_of_several_sequences(torch, d, m, hint):
     """Every SM walks many blocks, finishes rows and starts others in the middle of them."""
     rng = np.random.default_rng(d + m)
@@ -133,10 +151,12 @@ def test_mixed_prompts_and_decode(torch):
     run(torch, [(200, 200), (1, 700), (1, 1), (65, 300), (1, 128), (0, 0), (31, 31)], hq=8, hkv=2, d=128, ps=16)
 
 
-def test_large_logits_and_growing_maximum(torch):
-    """Logits that climb along the keys by far more than float32's exponent takes without a running maximum."""
+@pytest.mark.parametrize("hint", [0, 1, 3, 24])
+def test_large_logits_and_growing_maximum(torch, hint):
+    """Logits that climb along the keys by far more than float32's exponent takes without a running maximum (in every kernel:
+    the hint and the heads make tiles of 6, 2, 6 and 96 rows)."""
     import tiered_quantize_evict_gb300 as qe
-    n, d = 700, 64
+    n, d, heads = 700, 64, 4 if hint == 24 else 2
     c = Case(torch, [n], hkv=1, d=d, ps=16, dtype="bf16")
     k = torch.zeros(n, 1, d, dtype=c.dt)
     k[:, 0, 0] = torch.linspace(-120, 120, n).to(c.dt)
@@ -144,10 +164,10 @@ def test_large_logits_and_growing_maximum(torch):
     page = torch.from_numpy(c.table[0].astype(np.int64))[torch.arange(n) // 16].to(c.dev)
     c.k[0][page, :, (torch.arange(n) % 16).to(c.dev)] = k.to(c.dev)
     pool, seqs = c.objects(qe)
-    q = torch.zeros(3, 2, d, dtype=c.dt)
-    q[:, 0, 0], q[:, 1, 0] = 8.0, -8.0
-    out, lse = pool.attend(0, q.to(c.dev), c.ints([0, 3]), seqs, scale=1.0, return_lse=True)
-    ref, tol, lref, ltol = attend_bounds(torch, c, bits(q), 3, 0, 2, 1.0, True)
+    q = torch.zeros(3, heads, d, dtype=c.dt)
+    q[:, 0::2, 0], q[:, 1::2, 0] = 8.0, -8.0
+    out, lse = pool.attend(0, q.to(c.dev), c.ints([0, 3]), seqs, scale=1.0, max_q_len=hint, return_lse=True)
+    ref, tol, lref, ltol = attend_bounds(torch, c, bits(q), 3, 0, heads, 1.0, True)
     assert (np.abs(bits(out) - ref) <= tol).all()
     assert (np.abs(lse.cpu().numpy() - lref) <= ltol).all()
 

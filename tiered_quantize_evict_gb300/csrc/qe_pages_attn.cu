@@ -27,23 +27,15 @@
 //    is of the unrounded ones.  With NH = 1, where the tensor cores wait for memory anyway, what the rounding leaves is kept as
 //    a second operand and multiplied too: error against 64 bits 1.45 -> 1.0 times that of the result's own rounding.
 // mbarriers: kfull / kempty per slot, qfull / qempty per query buffer, s[i] (S i complete; tensor-core commit),
-// p[i][0], p[i][1] (P i's first and second half of the keys written; one arrival per softmax warp), o[h] (the
-// P V before it complete), turn[h] (half h may issue).  Every wait is bounded (0.2 s); one that expires sets
+// p[i][0], p[i][1] (P i's first and second half of the keys written; one arrival per softmax warp), o[h] (half
+// h's O of a tile complete; with NH = 1 o[i], the P V of an even or odd block complete: an S tells only that the P V two blocks before is,
+// which the parity of a single barrier could not tell from the last), turn[h] (half h may issue).  Every wait is bounded (0.2 s); one that expires sets
 // QE_PAGES_ERR_TIMEOUT and an abort flag that ends all loops, and the CTA leaves after what it issued has landed.
-#include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <atomic>
 
-#include "qe_common.cuh"
-#include "qe_pages.cuh"
+#include "qe_pages_attn.cuh"
 
 namespace qe {
-
-constexpr int PA_BN = 128;                       // keys of a block
-constexpr unsigned long long PA_WAIT_NS = 200000000ull;
-constexpr float PA_LAZY = 8.f;                   // log2 of how far a row's maximum may pass its reference
 
 // threads: 8 softmax warps per half, 4 others
 template <int NH>
@@ -57,320 +49,23 @@ struct PaShape {
   static constexpr int MOST = (ALL - TILE) / TILE;
   static constexpr int SMEM = ALL + 1024;
   // Slots beside two query buffers of `rows` rows (64 where a tile has no more, else 128; the products of rows behind read what
-  // lies there and are not used): bound by memory, the ring's depth is what counts (32K decode 347 us with 4 slots, 311 with 5).
+  // lies there and are not used): bound by memory, the ring's depth is what counts.
   static constexpr int slots(int rows) { return (ALL - 2 * CB * rows * 128) / TILE; }
   static constexpr int TM_O = 256;               // tensor memory: S0 at column 0, S1 at 128, O0 here, O1 at + D
 };
 
-// what a CTA's piece of the line starts with (read by the join kernel)
-struct PaRec {
-  long long begin;     // place of the tile on the line; -1: no piece
-  int b;               // block of the tile that the piece starts with
-  int tok, ntok;       // the tile's first packed token, and how many
-  int kvh;
-  int pieces;          // CTAs that have a piece
-};
-
-struct PaParams {
-  PagesView pg;
-  TableView t;
-  ChunksView c;
-  uint16_t* out;
-  float* lse;
-  long long ots, ohs;
-  int Hq, G, T, causal, min_piece;
-  int q_rows;              // rows of a query buffer
-  float scale, scale2;     // of the logits; and times log2(e)
-  PaRec* rec;              // [CTAs]; NULL: no tile is cut
-  float2* part_ml;         // [CTAs][2][NH][128]: reference, sum
-  float* part_o;           // [CTAs][2][NH][D / 4][128][4]
-};
-
-// ---------------------------------------------------------------------------- the line of blocks
-
-// sum over i < n of floor((a i + b) / 128), a >= 0, b >= 0.  With i = 128 k + j the term is a k + floor((a j + b) / 128), so it
-// comes down to n <= 128: over a whole period the residues of a j + b are b mod g, + g, + 2 g, ... g times over (g = gcd(a, 128)),
-// which gives the sum in closed form; the rest by Euclid's recursion on (128, a) in 32 bits.
-__device__ __forceinline__ long long floor_sum128(int n, int a, long long b) {
-  long long ans = n * (b >> 7) + (long long)n * (n - 1) / 2 * (a >> 7);
-  a &= 127;
-  const int c = (int)(b & 127);
-  const int q = n >> 7;
-  unsigned r = n & 127;
-  if (q) {
-    const int g = a ? a & -a : 128;
-    ans += 64ll * a * q * (q - 1) + (long long)q * ((127 * a + g) / 2 - 64 + c - (c & (g - 1))) + (long long)r * a * q;
-  }
-  unsigned m = 128, x = a, y = c, sum = 0;
-  while (r) {
-    if (x >= m) {
-      sum += r * (r - 1) / 2 * (x / m);
-      x %= m;
-    }
-    if (y >= m) {
-      sum += r * (y / m);
-      y %= m;
-    }
-    const unsigned top = x * r + y;
-    if (top < m) break;
-    r = top / m;
-    y = top % m;
-    const unsigned z = m;
-    m = x;
-    x = z;
-  }
-  return ans + sum;
-}
-
-// quotient of numbers that are mostly small
-__device__ __forceinline__ long long div_ll(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
-  return a / b;
-}
-
-// What a tile costs besides its blocks (its queries, its first maximum, its output), in blocks: measured about 3800 cycles, against
-// 2800 of a block.
-constexpr int PA_TILE_COST = 1;
-// A tile of so few blocks is never cut: a block takes a CTA 1.4 us, a join 3 us.
-constexpr int PA_WHOLE = 4;
-
-struct PaSeq {
-  SeqInfo s;
-  int tiles;
-};
-template <int NH>
-__device__ __forceinline__ PaSeq pa_seq(const PaParams& p, int i, bool report) {
-  PaSeq r;
-  r.s = seq_info(p.pg, p.t, p.c, i, report);
-  const int tt = NH * p.T;
-  r.tiles = (r.s.m + tt - 1) / tt;
-  return r;
-}
-// blocks of tile j (at least one, so that rows without keys are written too)
-template <int NH>
-__device__ __forceinline__ int pa_blocks(const PaParams& p, const SeqInfo& s, int j) {
-  const int end = p.causal ? s.len - s.m + min(s.m, (j + 1) * NH * p.T) : s.len;
-  return max(1, (end + PA_BN - 1) >> 7);
-}
-// length on the line of the tiles before tile j (j < tiles: those are all whole)
-template <int NH>
-__device__ __forceinline__ long long pa_before(const PaParams& p, const SeqInfo& s, int j) {
-  if (!p.causal || j == 0) return (long long)j * (PA_TILE_COST + max(1, (s.len + PA_BN - 1) >> 7));
-  const int tt = NH * p.T, off = s.len - s.m;
-  const int none = off < 0 ? min(j, -off / tt) : 0;   // tiles that see no key
-  return (long long)j * PA_TILE_COST + none + floor_sum128(j - none, tt, (long long)off + (long long)(none + 1) * tt + PA_BN - 1);
-}
-template <int NH>
-__device__ __forceinline__ long long pa_head_length(const PaParams& p, const PaSeq& q) {
-  return q.tiles == 0 ? 0 : pa_before<NH>(p, q.s, q.tiles - 1) + PA_TILE_COST + pa_blocks<NH>(p, q.s, q.tiles - 1);
-}
-
-// A place on the line: sequence, KV head, tile, block.  The end of the line is (n, 0, 0, 0).
-struct PaPlace {
-  int i, h, j, b;
-  SeqInfo s;
-  long long rem;      // (while it is being found) how far behind the sequence's start
-};
-
-// A walk from one place to another, tile by tile.
-template <int NH>
-struct PaCursor {
-  int i, h, j, b, nb;   // the place; blocks of the tile
-  PaSeq q;
-  int ei, eh, ej, eb;   // where the walk ends
-  __device__ __forceinline__ void set(const PaParams& p, const PaPlace* pl) {
-    i = pl[0].i;
-    h = pl[0].h;
-    j = pl[0].j;
-    b = pl[0].b;
-    ei = pl[1].i;
-    eh = pl[1].h;
-    ej = pl[1].j;
-    eb = pl[1].b;
-    q.s = pl[0].s;
-    q.tiles = (q.s.m + NH * p.T - 1) / (NH * p.T);
-    nb = pa_blocks<NH>(p, q.s, j);
-  }
-  // blocks left of the tile on this walk; 0: the walk is over
-  __device__ __forceinline__ bool last_tile() const { return i == ei && h == eh && j == ej; }
-  __device__ __forceinline__ int count() const { return last_tile() ? eb - b : nb - b; }
-  __device__ __forceinline__ void next_tile(const PaParams& p) {
-    if (last_tile()) {   // the walk is over
-      b = eb;
-      return;
-    }
-    b = 0;
-    if (++j >= q.tiles) {
-      j = 0;
-      if (++h >= p.pg.H) {
-        h = 0;
-        do {
-          if (++i >= p.c.n) {   // the end of the line
-            nb = 0;
-            return;
-          }
-          q = pa_seq<NH>(p, i, false);
-        } while (q.tiles == 0);
-      }
-    }
-    nb = pa_blocks<NH>(p, q.s, j);
-  }
-  __device__ __forceinline__ bool second_half(const PaParams& p) const { return NH == 2 && j * 2 * p.T + p.T < q.s.m; }
-};
-
-// Every CTA finds its piece: sums the sequences' lengths on the line, cuts it, finds the places of its two cuts.
-template <int NH>
-__device__ __noinline__ void pa_find(const PaParams& p, PaPlace* pl, long long* s_w) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int NT = PA_THREADS<NH>, W = NT / 32;
-  const int c = blockIdx.x;
-  // exclusive prefix of x over the block, and the total
-  auto scan = [&](long long x, long long& total) {
-    long long y = x;
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-      const long long z = __shfl_up_sync(~0u, y, k);
-      if (lane >= k) y += z;
-    }
-    if (lane == 31) s_w[warp] = y;
-    __syncthreads();
-    long long before = 0, all = 0;
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      const long long z = s_w[k];
-      if (k < warp) before += z;
-      all += z;
-    }
-    total = all;
-    __syncthreads();
-    return before + y - x;
-  };
-  auto length = [&](int i, bool report, SeqInfo& s) {
-    if (i >= p.c.n) return 0ll;
-    const PaSeq q = pa_seq<NH>(p, i, report);
-    s = q.s;
-    return pa_head_length<NH>(p, q) * p.pg.H;
-  };
-  if (tid < 2) pl[tid].i = p.c.n, pl[tid].h = pl[tid].j = pl[tid].b = 0;
-  SeqInfo s;
-  long long line, x = length(tid, c == 0, s), pre = scan(x, line);
-#pragma unroll 1
-  for (int base = NT; base < p.c.n; base += NT) {   // (more sequences than threads)
-    long long tot;
-    SeqInfo z;
-    scan(length(base + tid, c == 0, z), tot);
-    line += tot;
-  }
-  const long long most = div_ll(line, p.min_piece);
-  const int pieces = most < 1 ? 1 : (most > gridDim.x ? (int)gridDim.x : (int)most);
-  const long long each = div_ll(line, pieces);
-  const int over = (int)(line - each * pieces);
-  const long long cut[2] = {each * c + over * c / pieces, each * (c + 1) + over * (c + 1) / pieces};
-  if (c >= pieces || line == 0) {
-    if (tid == 0 && p.rec) p.rec[c] = PaRec{-1, 0, 0, 0, 0, 0};
-    __syncthreads();
-    return;
-  }
-  long long at = 0;
-#pragma unroll 1
-  for (int base = 0; base < p.c.n; base += NT) {
-    if (base > 0) x = length(base + tid, false, s);
-    if (p.c.n > NT) {
-      long long tot;
-      pre = at + scan(x, tot);
-      at += tot;
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (cut[k] >= pre && cut[k] < pre + x) {
-        pl[k].i = base + tid;
-        pl[k].s = s;
-        pl[k].rem = cut[k] - pre;
-      }
-  }
-  __syncthreads();
-  if (warp < 2 && pl[warp].i < p.c.n) {
-    PaSeq q;
-    q.s = pl[warp].s;
-    q.tiles = (q.s.m + NH * p.T - 1) / (NH * p.T);
-    const long long head = pa_head_length<NH>(p, q);
-    long long rem = pl[warp].rem;
-    const int h = (int)div_ll(rem, head);
-    rem -= h * head;
-    int lo = 0, hi = q.tiles;   // the last tile that begins at or before rem: 32 places a round
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32, cand = lo + lane * step;
-      const bool le = cand < hi && pa_before<NH>(p, q.s, cand) <= rem;
-      const int top = 31 - __clz(__ballot_sync(~0u, le));
-      lo += top * step;
-      hi = min(hi, lo + step);
-    }
-    rem -= pa_before<NH>(p, q.s, lo);
-    // a cut in what the tile costs besides, or in a short tile, is one before the tile
-    const int b = pa_blocks<NH>(p, q.s, lo) <= PA_WHOLE ? 0 : max(0, (int)rem - PA_TILE_COST);
-    if (lane == 0) {
-      pl[warp].h = h;
-      pl[warp].j = lo;
-      pl[warp].b = b;
-      const int tt = NH * p.T;
-      if (warp == 0 && p.rec) p.rec[c] = PaRec{cut[0] - rem, b, q.s.q0 + lo * tt, min(tt, q.s.m - lo * tt), h, pieces};
-    }
-  }
-  __syncthreads();
-}
-
-// ---------------------------------------------------------------------------- instructions
-
-__device__ __forceinline__ void pa_mma_ss(unsigned d, unsigned long long a, unsigned long long b, unsigned idesc, bool acc) {
-  asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0)
-      : "memory");
-}
-__device__ __forceinline__ void pa_mma_ts(unsigned d, unsigned a, unsigned long long b, unsigned idesc, bool acc) {
-  asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1 : 0)
-      : "memory");
-}
-// one lane of a converged warp
-__device__ __forceinline__ bool pa_elect() {
+// the two warps of a row: barrier, and barrier with the OR of a truth value
+__device__ __forceinline__ void pa_pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool pa_pair_or(int id, bool v) {
   unsigned r;
-  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r)::"memory");
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbar.red.or.pred p, %2, 64, q;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      : "r"((unsigned)v), "r"(id)
+      : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void pa_commit(unsigned bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void pa_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void pa_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void pa_arrive(unsigned bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void pa_tma4(unsigned dst, const CUtensorMap* map, int x, int y, int z, int w, unsigned bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void pa_tma3(unsigned dst, const CUtensorMap* map, int x, int y, int z, unsigned bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-// 32 float32 columns of this thread's tensor-memory lane; pa_wait_ld before their use
-__device__ __forceinline__ void pa_ld32(unsigned t, unsigned* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
-      "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(t)
-      : "memory");
-}
+
 // D / 2 columns of 16 lanes: register 4 j + e is (lane T / 4, column 8 j + 2 (T mod 4) + e), 4 j + 2 + e the same of lane 8 + T / 4
 template <int D>
 __device__ __forceinline__ void pa_ld_rows(unsigned t, unsigned* r) {
@@ -416,103 +111,6 @@ __device__ __forceinline__ void pa_quad_transpose(unsigned* u) {
     for (int i = 0; i < 8; ++i) u[i] = x[i];
   }
 }
-// 32 bytes to global memory: one store where the address allows it, else two
-__device__ __forceinline__ void pa_store32(uint16_t* dst, const unsigned* r) {
-  if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
-                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-  } else {
-    *reinterpret_cast<uint4*>(dst) = make_uint4(r[0], r[1], r[2], r[3]);
-    *reinterpret_cast<uint4*>(dst + 8) = make_uint4(r[4], r[5], r[6], r[7]);
-  }
-}
-__device__ __forceinline__ void pa_ld16(unsigned t, unsigned* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(t)
-      : "memory");
-}
-__device__ __forceinline__ void pa_st16(unsigned t, const unsigned* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t), "r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
-      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-// waits for this thread's tensor-memory loads; the registers pass through empty asm, so no use moves before it
-template <int N>
-__device__ __forceinline__ void pa_wait_ld(unsigned* r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
-}
-__device__ __forceinline__ void pa_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// the two warps of a row: barrier, and barrier with the OR of a truth value
-__device__ __forceinline__ void pa_pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ bool pa_pair_or(int id, bool v) {
-  unsigned r;
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbar.red.or.pred p, %2, 64, q;\nselp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(r)
-      : "r"((unsigned)v), "r"(id)
-      : "memory");
-  return r != 0;
-}
-
-struct PaWait {
-  const PagesView* pg;
-  volatile int* abort;
-  // Bounded wait for the phase; false when it expired or the CTA is leaving.
-  __device__ __forceinline__ bool operator()(unsigned bar, unsigned parity) const {
-    return mbar_try_wait(bar, parity) || slow(bar, parity);
-  }
-  __device__ __forceinline__ bool slow(unsigned bar, unsigned parity) const {
-    const unsigned long long t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-      if (*abort) return false;
-      if (globaltimer_ns() - t0 > PA_WAIT_NS) {
-        pages_report(*pg, QE_PAGES_ERR_TIMEOUT);
-        *abort = 1;
-        return false;
-      }
-    }
-    return true;
-  }
-  // the same on the way out, for what has been issued
-  __device__ __forceinline__ void drain(unsigned bar, unsigned parity) const {
-    const unsigned long long t0 = globaltimer_ns();
-    while (!mbar_try_wait_sleep(bar, parity, 20000u))
-      if (globaltimer_ns() - t0 > PA_WAIT_NS) return;
-  }
-};
-
-template <bool FP16>
-__device__ __forceinline__ unsigned pa_pack(float lo, float hi) {
-  unsigned d;
-  if constexpr (FP16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-
-template <bool FP16>
-__device__ __forceinline__ float2 pa_unpack(unsigned x) {
-  if constexpr (FP16) {
-    __half2 h;
-    memcpy(&h, &x, 4);
-    return __half22float2(h);
-  }
-  return make_float2(bf16lo_to_f32(x), bf16hi_to_f32(x));
-}
-
-// shared-memory descriptors: 128-byte swizzle, 8-row groups 1024 bytes apart.  K-major operands (Q, K); and V with
-// channels as the rows of the operand (MN-major: 64 channels to a column block, blocks 128 tokens x 128 bytes apart).
-constexpr unsigned long long PA_DESC_K = (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-constexpr unsigned long long PA_DESC_V = (1024ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-
 // ---------------------------------------------------------------------------- the kernel
 
 template <int D, int NH, bool FP16>
@@ -561,7 +159,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
   pa_fence_before();
   griddep_wait();
   griddep_launch_dependents();   // (what follows may then rely on all that ran before this launch)
-  pa_find<NH>(p, s_place, s_w);   // ends with a barrier
+  pa_find<NH, PA_THREADS<NH>>(p, s_place, s_w);   // ends with a barrier
   pa_fence_after();
   const unsigned tm = s_tmem;
   // (two cuts that fall into the same place leave an empty piece)
@@ -578,25 +176,26 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
       const int np = PA_BN / rows;
       const int piece = lane % np, cb = lane / np;       // lane -> (page of the block, column block)
       const bool mine = cb < Sh::CB;
-      // page of this lane's piece, or n_pages (out of the pool: the copy fills zeros) where there is none
-      auto page_of = [&]() {
+      // the table's entry for this lane's piece (INT_MIN behind the sequence's end), loaded a block before it is looked at
+      auto entry = [&]() {
         const int key = cur.b * PA_BN + piece * rows;
-        if (key >= cur.q.s.len) return p.pg.P;
-        const int g = page_at(p.pg, p.t, cur.q.s.row, key);
-        return g < 0 ? p.pg.P : g;
+        return key < cur.q.s.len ? p.t.table[(long long)cur.q.s.row * p.t.stride + (key >> p.pg.lgS)] : INT_MIN;
       };
       int slot = 0, ph = 1, issued = 0, left = cur.count();
-      int page = page_of();
+      int next = entry();
       bool ok = true;
 #pragma unroll 1
       while (left > 0 && ok) {
-        const int tk = (cur.b * PA_BN) & (p.pg.S - 1), h = cur.h, now = page;
+        const int tk = (cur.b * PA_BN) & (p.pg.S - 1), h = cur.h;
+        const bool there = next >= 0 && next < p.pg.P;
+        const int now = there ? next : p.pg.P;             // out of the pool: the copy fills zeros
+        if (!there && next != INT_MIN) pages_report(p.pg, QE_PAGES_ERR_PAGE);
         ++cur.b;
         if (--left == 0) {
           cur.next_tile(p);
           left = cur.count();
         }
-        if (left > 0) page = page_of();                  // the next block's, read ahead
+        if (left > 0) next = entry();
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           ok = ok && wait(smem_u32(&b_kempty[slot]), ph);
@@ -739,7 +338,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
             if (pa_elect()) {
               pv(1, sb, vslot, true);
               pa_commit(smem_u32(&b_kempty[vslot]));
-              pa_commit(smem_u32(&b_o[0]));
+              pa_commit(smem_u32(&b_o[sb]));
             }
             __syncwarp();
             step();
@@ -868,7 +467,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
               if (k > 0) {
                 sum *= f;
                 if constexpr (NH == 1) {   // the P V before this block's may still be running
-                  wait(smem_u32(&b_o[0]), (n - 1) & 1);
+                  wait(smem_u32(&b_o[(n - 1) & 1]), (n - 1) >> 1 & 1);
                   __syncwarp();
                   pa_fence_after();
                 }
@@ -918,10 +517,8 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
         }
 
         // ------------------------------ the tile's end in this piece
-        // (NH = 1: o has a phase per block, and the last S says that all P V but the last two are complete: the waits are for
-        // each of those in turn, as a parity only tells one phase from the next)
-        if (NH == 1 && n > 1) wait(smem_u32(&b_o[0]), n & 1);
-        wait(smem_u32(&b_o[half]), NH == 2 ? tiles & 1 : (n - 1) & 1);
+        if (NH == 2) wait(smem_u32(&b_o[half]), tiles & 1);
+        else wait(smem_u32(&b_o[(n - 1) & 1]), (n - 1) >> 1 & 1);
         ++tiles;
         __syncwarp();
         pa_fence_after();
@@ -1101,11 +698,29 @@ static cudaError_t launch_t(const PaParams& p, const CUtensorMap* maps, int devi
   cfg.attrs = at;
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, pages_attend_kernel<D, NH, FP16>, p, maps[0], maps[1], maps[2]);
-  if (e != cudaSuccess || !p.rec) return e;   // no tile is cut
+  return e != cudaSuccess || !p.rec ? e : launch_pages_join(p, NH, FP16, n_sm, st);   // (no rec: no tile is cut)
+}
+
+template <int D, int NH, bool FP16>
+static cudaError_t join_t(const PaParams& p, int n_sm, cudaStream_t st) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(n_sm, NH * (D / PJ_CH));
   cfg.blockDim = dim3(PJ_THREADS);
-  cfg.dynamicSmemBytes = 0;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, pages_join_kernel<D, NH, FP16>, p);
+}
+cudaError_t launch_pages_join(const PaParams& p, int nh, int fp16, int n_sm, cudaStream_t st) {
+  if (p.pg.D == 128) {
+    if (nh == 1) return fp16 ? join_t<128, 1, true>(p, n_sm, st) : join_t<128, 1, false>(p, n_sm, st);
+    return fp16 ? join_t<128, 2, true>(p, n_sm, st) : join_t<128, 2, false>(p, n_sm, st);
+  }
+  if (nh == 1) return fp16 ? join_t<64, 1, true>(p, n_sm, st) : join_t<64, 1, false>(p, n_sm, st);
+  return fp16 ? join_t<64, 2, true>(p, n_sm, st) : join_t<64, 2, false>(p, n_sm, st);
 }
 
 cudaError_t launch_pages_attend(const PagesAttendParams& a, int fp16, int device, int n_sm, void* ws, cudaStream_t st) {
@@ -1162,6 +777,7 @@ cudaError_t launch_pages_attend(const PagesAttendParams& a, int fp16, int device
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
+  if (one && p.T * p.G <= PAGES_FEW_ROWS) return launch_pages_few(p, maps, fp16, device, n_sm, st);
   if (g.D == 128) {
     if (one) return fp16 ? launch_t<128, 1, true>(p, maps, device, n_sm, st) : launch_t<128, 1, false>(p, maps, device, n_sm, st);
     return fp16 ? launch_t<128, 2, true>(p, maps, device, n_sm, st) : launch_t<128, 2, false>(p, maps, device, n_sm, st);
