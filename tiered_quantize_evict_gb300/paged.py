@@ -119,6 +119,7 @@ class PageTable:
             _ints("refs", refs, dev)
         self.table, self.kv_len, self.refs = table, kv_len, refs
         self._index, self._n_refs = dev, refs.shape[0] if refs is not None else -1
+        self._shape = tuple(table.shape)
         self._s = _Table(table.data_ptr(), kv_len.data_ptr(), refs.data_ptr() if refs is not None else None, table.stride(0),
                          table.shape[0], table.shape[1])
         self._ref = ctypes.byref(self._s)
@@ -158,7 +159,7 @@ class PagePool:
 
     def _need(self, seqs: PageTable, n: int) -> int:
         """Bytes of workspace of attend (n < 0) or of managing n entries, with tables of this shape."""
-        key = (seqs._s.n_rows, seqs._s.max_pages, n)
+        key = (seqs._shape, n)
         need = self._bytes.get(key)
         if need is None:
             b = ctypes.c_size_t()
@@ -230,18 +231,20 @@ class PagePool:
             qs = self._tokens("q", q, total, hq)
             if q_out is None:
                 q_out = torch.empty_like(q, memory_format=_DENSE)
-            os = self._tokens("q_out", q_out, total, hq)
+                os = (hq * self.head_dim, self.head_dim)
+            else:
+                os = self._tokens("q_out", q_out, total, hq)
             qp, op = q.data_ptr(), q_out.data_ptr()
         elif q_out is not None:
             raise _bad("q_out without q")
         if positions is not None:
             if rope is None:
                 raise _bad("positions without rope")
-            want = (rope.n_axes, total) if positions.dim() == 2 or rope.n_axes > 1 else (total,)
-            if positions.dtype is not _I32 or positions.get_device() != self._index or positions.shape != want or \
-                    positions.stride(-1) != 1 and total > 1:
+            ps = positions.stride()
+            if positions.dtype is not _I32 or positions.get_device() != self._index or \
+                    positions.shape != ((rope.n_axes, total) if len(ps) == 2 or rope.n_axes > 1 else (total,)) or ps[-1] != 1 and total > 1:
                 raise _bad(f"positions must be int32 [{rope.n_axes}, {total}] on {self.device}, tokens contiguous")
-            pp, pst = positions.data_ptr(), positions.stride(0)
+            pp, pst = positions.data_ptr(), ps[0]
         st = self._lib.qe_pages_append(
             self._ref, layer, self._seqs(seqs), self._chunks(q_start, rows, total),
             _APPEND.pack(k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1], qp, op, qs[0], qs[1], os[0], os[1], hq,
@@ -259,7 +262,9 @@ class PagePool:
         qs = self._tokens("q", q, total, hq)
         if out is None:
             out = torch.empty_like(q, memory_format=_DENSE)
-        os = self._tokens("out", out, total, hq)
+            os = (hq * self.head_dim, self.head_dim)
+        else:
+            os = self._tokens("out", out, total, hq)
         lse = torch.empty(total, hq, dtype=torch.float32, device=self.device) if return_lse else None
         ref, c = self._seqs(seqs), self._chunks(q_start, rows, total)
         a = _ATTEND.pack(q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else 0, qs[0], qs[1], os[0], os[1], hq,
@@ -334,7 +339,7 @@ class PagePool:
     def gather(self, layer: int, seqs: PageTable, start: int, n_tokens: int, *, rows: Optional[torch.Tensor] = None,
                out: Optional[Sequence[torch.Tensor]] = None):
         """qe_pages_gather: (k, v), each [n_rows][n_kv_heads][n_tokens][head_dim], the layout ``QECache.qe_append`` takes."""
-        n = seqs._s.n_rows if rows is None else _ints("rows", rows, self._index)
+        n = seqs._shape[0] if rows is None else _ints("rows", rows, self._index)
         shape = (n, self.n_kv_heads, max(0, n_tokens), self.head_dim)
         if out is None:
             out = [torch.empty(shape, dtype=self.dtype, device=self.device) for _ in range(2)]
