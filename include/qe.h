@@ -514,7 +514,8 @@ typedef struct {
 
 /* The sequences.  Row r holds the tokens [0, kv_len[r]) of one sequence, on the pages
  * table[r * row_stride + i], i < ceil(kv_len[r] / page_size); entries behind them are -1 after
- * the calls that manage pages.  A row holds at most 2^30 tokens.  refs[p] is how many table entries name page p, 0 for a free page
+ * the calls that manage pages.  A row holds at most 2^30 tokens; tables whose pages are managed have
+ * n_rows * (max_pages + 1) below 2^31.  refs[p] is how many table entries name page p, 0 for a free page
  * (qe_pages_append, _attend and _gather do not read it; it may be NULL for them).  A page that two rows
  * share is full: the calls below keep it so. */
 typedef struct {
@@ -579,8 +580,8 @@ typedef struct {
 
 /* Attention of a chunk of new tokens over the cached pages of one layer:
  * out = softmax(scale q K^T + mask) V per query head, over the keys and values of its KV head.  A query that
- * sees no key gets zeros (and lse = -inf).  Any finite inputs; what lies in the pages behind kv_len may
- * be anything.  The probabilities meet the values rounded to the pool's type, all sums are float32.
+ * sees no key gets zeros (and lse = -inf).  Inputs are finite and so are the logits in float32 (a value that is not may
+ * also reach the chunk's tokens before it); what lies in the pages behind kv_len may be anything.  The probabilities meet the values rounded to the pool's type, all sums are float32.
  * Deterministic for the same lengths.  n_seqs up to 65536. */
 qe_status qe_pages_attend(const qe_pages* pages, int layer, const qe_page_table* seqs, const qe_chunks* chunks,
                           const qe_pages_attend_args* args, void* workspace, size_t bytes, void* stream);

@@ -109,6 +109,12 @@ def test_refs_are_needed_where_pages_are_managed(env):
         refused(env, what, "refs")
 
 
+def test_managed_tables_are_counted_in_32_bits(env):
+    env.table.n_rows, env.table.max_pages, env.table.row_stride = 2 ** 15, 2 ** 16, 2 ** 16
+    for what in ("resize", "fork", "compact"):
+        refused(env, what, "too large")
+
+
 @pytest.mark.parametrize("field,value,text", [("q_start", None, "q_start"), ("n_seqs", -1, "n_seqs"), ("n_seqs", 65537, "n_seqs"),
                                               ("total_q", -1, "total_q"), ("total_q", 2 ** 30 + 1, "total_q"), ("rows", 4098, "aligned")])
 def test_chunks_are_checked(env, field, value, text):

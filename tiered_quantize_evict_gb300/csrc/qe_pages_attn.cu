@@ -7,8 +7,8 @@
 //
 // Tiles.  A tile is NH halves of 128 rows: T tokens x the G query heads of one KV head per half (row t G + g,
 // T = floor(128 / G)), so a block's keys and values are read once for all of them.  NH = 2 for chunks: while one half's
-// softmax runs, the other half's products keep the tensor cores busy.  NH = 1 for a few rows (decode, drafts): bound by
-// the memory the cache is read from, so one half and the S buffers of both to run ahead.
+// softmax runs, the other half's products keep the tensor cores busy.  NH = 1 where a chunk's rows fit one half (drafts): bound by
+// the memory the cache is read from, so one half and the S buffers of both to run ahead.  (At most 16 rows: qe_pages_few.cu.)
 //
 // Split.  All (tile, block) pairs of the call form one line, cut into equal pieces, one per CTA (one CTA per SM): long
 // caches with few rows are split along the keys, prompts are balanced whatever their causal shape.  A tile inside a piece is
@@ -28,8 +28,8 @@
 //    a second operand and multiplied too: error against 64 bits 1.45 -> 1.0 times that of the result's own rounding.
 // mbarriers: kfull / kempty per slot, qfull / qempty per query buffer, s[i] (S i complete; tensor-core commit),
 // p[i][0], p[i][1] (P i's first and second half of the keys written; one arrival per softmax warp), o[h] (half
-// h's O of a tile complete; with NH = 1 o[i], the P V of an even or odd block complete: an S tells only that the P V two blocks before is,
-// which the parity of a single barrier could not tell from the last), turn[h] (half h may issue).  Every wait is bounded (0.2 s); one that expires sets
+// h's O of a tile complete; with NH = 1 o[i]: the P V of an even or odd block complete.  An S tells only that the P V two blocks
+// before is, so one barrier's parity could mean the last P V or the one before), turn[h] (half h may issue).  Every wait is bounded (0.2 s); one that expires sets
 // QE_PAGES_ERR_TIMEOUT and an abort flag that ends all loops, and the CTA leaves after what it issued has landed.
 #include <atomic>
 
@@ -37,7 +37,7 @@
 
 namespace qe {
 
-// threads: 8 softmax warps per half, 4 others
+// threads: 8 softmax warps per half, 4 more warps
 template <int NH>
 constexpr int PA_THREADS = 256 * NH + 128;
 
@@ -740,7 +740,7 @@ cudaError_t launch_pages_attend(const PagesAttendParams& a, int fp16, int device
   p.causal = a.causal;
   p.scale = a.scale;
   p.scale2 = a.scale * 1.44269504088896341f;
-  // One half where the chunk's rows fit it (a few rows: bound by reading the cache), else two.  The tile takes no more
+  // One half where the longest chunk's rows fit it (bound by reading the cache), else two.  The tile takes no more
   // tokens than the longest chunk, so that its query copy does not read the next sequences' rows.
   const int fit = 128 / p.G;
   const bool one = a.max_q_len > 0 && a.max_q_len <= fit;

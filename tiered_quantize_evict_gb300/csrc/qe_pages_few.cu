@@ -14,8 +14,7 @@
 //    warps otherwise).
 // CTA: warps 0-3 softmax, 4 TMA of keys and values, 5 tensor-core issue, 6 TMA of the queries, 7 tensor memory.
 // mbarriers: kfull / kempty per slot, qfull / qempty per query buffer, s[i] (S i complete), p[i] (P i written; one arrival per
-// softmax warp), o[i] (the P V of an even or odd
-// block complete: an S tells only that the P V two blocks before is, which the parity of a single barrier could not tell from the last).  Waits are bounded as in qe_pages_attn.cu.
+// softmax warp), o[i] (the P V of an even or odd block complete, as with NH = 1 there).  Waits are bounded as in qe_pages_attn.cu.
 #include <atomic>
 
 #include "qe_pages_attn.cuh"

@@ -101,6 +101,8 @@ qe_status check_table(const qe_page_table* t, bool refs, qe::TableView* o) {
   if (!t || !t->table || !t->kv_len) return fail(QE_ERR_INVALID_ARG, "page table: null pointer");
   if (refs && !t->refs) return fail(QE_ERR_INVALID_ARG, "page table: refs is null");
   if (t->n_rows < 1 || t->max_pages < 1) return fail(QE_ERR_INVALID_ARG, "page table: n_rows and max_pages must be >= 1");
+  if (refs && ((long long)t->max_pages + 1) * t->n_rows > 0x7FFFFFFF)   // (pages are counted in 32 bits)
+    return fail(QE_ERR_INVALID_ARG, "page table: too large to be managed: n_rows * (max_pages + 1) must be below 2^31");
   if (t->n_rows > 1 && t->row_stride < t->max_pages) return fail(QE_ERR_INVALID_ARG, "page table: row_stride is below max_pages");
   if (misaligned(t->table, 4) || misaligned(t->kv_len, 4) || misaligned(t->refs, 4))
     return fail(QE_ERR_INVALID_ARG, "page table: pointers must be 4-byte aligned");
