@@ -583,39 +583,75 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
   }
 }
 
-// Joins the parts of the tiles that were cut: block (c, y) takes the tile that piece c starts inside of, if no earlier
-// piece starts inside of it too, and of it half y / (D / 16) and 16 channels.  A thread per row; where there are fewer rows than
-// threads, several threads share a row's parts (a decode step cuts a few rows into many).
-constexpr int PJ_THREADS = 128, PJ_CH = 16;
-template <int D, int NH, bool FP16>
-__global__ void __launch_bounds__(PJ_THREADS) pages_join_kernel(const __grid_constant__ PaParams p) {
-  __shared__ float s_m[PJ_THREADS], s_sum[PJ_THREADS], s_o[PJ_CH][PJ_THREADS];
+// Joins the parts of the tiles that were cut: block (x, y) takes one of them, and of it half y / (D / 16) and 16 channels.  A thread
+// per row; where there are fewer rows than threads, several threads share a row's parts.  A call of few tiles, which are then cut
+// into many parts, has a block of 512 threads for each of its tiles (180 rows over 30K tokens, two tiles: 74 -> 34 us with the attention
+// itself); one of many tiles 128 threads for each piece, most of which leave at once: looking for the tiles first costs 1.5 us more.
+constexpr int PJ_CH = 16;
+template <int D, int NH, bool FP16, int NT>
+__global__ void __launch_bounds__(NT) pages_join_kernel(const __grid_constant__ PaParams p) {
+  __shared__ float s_m[NT], s_sum[NT], s_o[PJ_CH][NT];
+  __shared__ uint2 s_piece[NT == 128 ? 1 : PA_MAX_CTAS / 32];
   griddep_wait();
   griddep_launch_dependents();
-  const int c = blockIdx.x, h = blockIdx.y / (D / PJ_CH), ch = blockIdx.y % (D / PJ_CH) * PJ_CH;
-  const PaRec r = p.rec[c];
-  if (r.begin < 0 || r.b == 0) return;
-  if (p.rec[c - 1].begin == r.begin && p.rec[c - 1].b > 0) return;
-  const int rows = (min(r.ntok, (h + 1) * p.T) - h * p.T) * p.G;
-  if (rows <= 0) return;
-  int end = c + 1;   // the pieces [c, end) hold the rest of the tile
-  for (int in = PJ_THREADS; in == PJ_THREADS && end < r.pieces; end += in) {
-    const int q = end + threadIdx.x;
-    in = __syncthreads_count(q < r.pieces && p.rec[q].begin == r.begin);
+  const int h = blockIdx.y / (D / PJ_CH), ch = blockIdx.y % (D / PJ_CH) * PJ_CH;
+  // the tile's pieces but its first: [c, end)
+  int c = blockIdx.x, end, rows;
+  PaRec r;
+  if constexpr (NT == 128) {   // piece x, if it is the first that starts inside of its tile
+    r = p.rec[c];
+    if (r.begin < 0 || r.b == 0) return;
+    if (p.rec[c - 1].begin == r.begin && p.rec[c - 1].b > 0) return;
+    rows = (min(r.ntok, (h + 1) * p.T) - h * p.T) * p.G;
+    if (rows <= 0) return;
+    end = c + 1;
+    for (int in = NT; in == NT && end < r.pieces; end += in) {
+      const int q = end + threadIdx.x;
+      in = __syncthreads_count(q < r.pieces && p.rec[q].begin == r.begin);
+    }
+  } else {   // the x-th of the tiles that are cut
+    const int words = (p.ctas + 31) >> 5;
+    for (int i = threadIdx.x; i < words * 32; i += NT) {
+      bool first = false, more = false;   // piece i is the first that starts inside of its tile, or another one
+      if (i > 0 && i < p.ctas) {
+        const long long at = p.rec[i].begin, last = p.rec[i - 1].begin;
+        const int b = p.rec[i].b, last_b = p.rec[i - 1].b;
+        more = (at >= 0) & (b > 0) & (last == at) & (last_b > 0);
+        first = (at >= 0) & (b > 0) & !more;
+      }
+      const unsigned f = __ballot_sync(~0u, first), m = __ballot_sync(~0u, more);
+      if ((threadIdx.x & 31) == 0) s_piece[i >> 5] = make_uint2(f, m);
+    }
+    __syncthreads();
+    int w = 0;
+    while (w < words && __popc(s_piece[w].x) <= c) c -= __popc(s_piece[w++].x);
+    if (w == words) return;
+    unsigned x = s_piece[w].x;
+    for (; c > 0; --c) x &= x - 1;
+    c = w * 32 + __ffs(x) - 1;
+    r = p.rec[c];
+    end = c + 1;
+    w = end >> 5;
+    x = w < words ? ~s_piece[w].y & ~0u << (end & 31) : 0;
+    while (x == 0 && ++w < words) x = ~s_piece[w].y;
+    end = w < words ? w * 32 + __ffs(x) - 1 : p.ctas;
+    rows = (min(r.ntok, (h + 1) * p.T) - h * p.T) * p.G;
+    if (rows <= 0) return;
   }
   int lg = 0;
   while ((1 << lg) < rows) ++lg;
-  const int row = threadIdx.x & ((1 << lg) - 1), grp = threadIdx.x >> lg, grps = PJ_THREADS >> lg;
+  const int row = threadIdx.x & ((1 << lg) - 1), grp = threadIdx.x >> lg, grps = NT >> lg;
+  const int used = min(grps, end - c + 1);   // groups that have a part
   auto part = [&](int q) { return ((long long)q * 2 + (q < c ? 1 : 0)) * NH + h; };
   float m = -INFINITY;
   for (int q = c - 1 + grp; q < end; q += grps) m = fmaxf(m, p.part_ml[part(q) * 128 + row].x);
   if (grps > 1) {
     s_m[threadIdx.x] = m;
     __syncthreads();
-    for (int g = 0; g < grps; ++g) m = fmaxf(m, s_m[(g << lg) + row]);
+    for (int g = 0; g < used; ++g) m = fmaxf(m, s_m[(g << lg) + row]);
   }
   float sum = 0.f, o[PJ_CH] = {};
-#pragma unroll 2
+#pragma unroll (NT == 512 ? 4 : 2)
   for (int q = c - 1 + grp; q < end; q += grps) {
     const float2 ml = p.part_ml[part(q) * 128 + row];
     const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
@@ -638,7 +674,7 @@ __global__ void __launch_bounds__(PJ_THREADS) pages_join_kernel(const __grid_con
     for (int e = 0; e < PJ_CH; ++e) s_o[e][threadIdx.x] = o[e];
     __syncthreads();
     if (grp == 0)
-      for (int g = 1; g < grps; ++g) {
+      for (int g = 1; g < used; ++g) {
         sum += s_sum[(g << lg) + row];
 #pragma unroll
         for (int e = 0; e < PJ_CH; ++e) o[e] += s_o[e][(g << lg) + row];
@@ -680,7 +716,7 @@ static EncodeFn encode_fn() {
 }
 
 template <int D, int NH, bool FP16>
-static cudaError_t launch_t(const PaParams& p, const CUtensorMap* maps, int device, int n_sm, cudaStream_t st) {
+static cudaError_t launch_t(const PaParams& p, const CUtensorMap* maps, int device, cudaStream_t st) {
   static std::atomic<unsigned long long> ready{0};   // devices whose copy of the kernel has its attribute
   if (device >= 64 || !(ready.load() >> device & 1)) {
     const cudaError_t e = cudaFuncSetAttribute(pages_attend_kernel<D, NH, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, PaShape<D>::SMEM);
@@ -691,36 +727,39 @@ static cudaError_t launch_t(const PaParams& p, const CUtensorMap* maps, int devi
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(n_sm);
+  cfg.gridDim = dim3(p.ctas);
   cfg.blockDim = dim3(PA_THREADS<NH>);
   cfg.dynamicSmemBytes = PaShape<D>::SMEM;
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, pages_attend_kernel<D, NH, FP16>, p, maps[0], maps[1], maps[2]);
-  return e != cudaSuccess || !p.rec ? e : launch_pages_join(p, NH, FP16, n_sm, st);   // (no rec: no tile is cut)
+  return e != cudaSuccess || !p.rec ? e : launch_pages_join(p, NH, FP16, st);   // (no rec: no tile is cut)
 }
 
 template <int D, int NH, bool FP16>
-static cudaError_t join_t(const PaParams& p, int n_sm, cudaStream_t st) {
+static cudaError_t join_t(const PaParams& p, cudaStream_t st) {
+  // at most so many tiles; few: their blocks all run at once, two to an SM
+  const long long tt = (long long)NH * p.T, tiles = (p.c.n + (p.c.total > p.c.n ? (p.c.total - p.c.n) / tt : 0)) * p.pg.H;
+  const bool few = tiles * NH * (D / PJ_CH) <= 2 * p.ctas;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(n_sm, NH * (D / PJ_CH));
-  cfg.blockDim = dim3(PJ_THREADS);
+  cfg.gridDim = dim3(few ? (unsigned)tiles : p.ctas, NH * (D / PJ_CH));
+  cfg.blockDim = dim3(few ? 512 : 128);
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, pages_join_kernel<D, NH, FP16>, p);
+  return few ? cudaLaunchKernelEx(&cfg, pages_join_kernel<D, NH, FP16, 512>, p) : cudaLaunchKernelEx(&cfg, pages_join_kernel<D, NH, FP16, 128>, p);
 }
-cudaError_t launch_pages_join(const PaParams& p, int nh, int fp16, int n_sm, cudaStream_t st) {
+cudaError_t launch_pages_join(const PaParams& p, int nh, int fp16, cudaStream_t st) {
   if (p.pg.D == 128) {
-    if (nh == 1) return fp16 ? join_t<128, 1, true>(p, n_sm, st) : join_t<128, 1, false>(p, n_sm, st);
-    return fp16 ? join_t<128, 2, true>(p, n_sm, st) : join_t<128, 2, false>(p, n_sm, st);
+    if (nh == 1) return fp16 ? join_t<128, 1, true>(p, st) : join_t<128, 1, false>(p, st);
+    return fp16 ? join_t<128, 2, true>(p, st) : join_t<128, 2, false>(p, st);
   }
-  if (nh == 1) return fp16 ? join_t<64, 1, true>(p, n_sm, st) : join_t<64, 1, false>(p, n_sm, st);
-  return fp16 ? join_t<64, 2, true>(p, n_sm, st) : join_t<64, 2, false>(p, n_sm, st);
+  if (nh == 1) return fp16 ? join_t<64, 1, true>(p, st) : join_t<64, 1, false>(p, st);
+  return fp16 ? join_t<64, 2, true>(p, st) : join_t<64, 2, false>(p, st);
 }
 
 cudaError_t launch_pages_attend(const PagesAttendParams& a, int fp16, int device, int n_sm, void* ws, cudaStream_t st) {
@@ -738,6 +777,7 @@ cudaError_t launch_pages_attend(const PagesAttendParams& a, int fp16, int device
   p.Hq = a.Hq;
   p.G = a.Hq / g.H;
   p.causal = a.causal;
+  p.ctas = n_sm < PA_MAX_CTAS ? n_sm : PA_MAX_CTAS;
   p.scale = a.scale;
   p.scale2 = a.scale * 1.44269504088896341f;
   // One half where the longest chunk's rows fit it (bound by reading the cache), else two.  The tile takes no more
@@ -777,13 +817,13 @@ cudaError_t launch_pages_attend(const PagesAttendParams& a, int fp16, int device
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  if (one && p.T * p.G <= PAGES_FEW_ROWS) return launch_pages_few(p, maps, fp16, device, n_sm, st);
+  if (one && p.T * p.G <= PAGES_FEW_ROWS) return launch_pages_few(p, maps, fp16, device, st);
   if (g.D == 128) {
-    if (one) return fp16 ? launch_t<128, 1, true>(p, maps, device, n_sm, st) : launch_t<128, 1, false>(p, maps, device, n_sm, st);
-    return fp16 ? launch_t<128, 2, true>(p, maps, device, n_sm, st) : launch_t<128, 2, false>(p, maps, device, n_sm, st);
+    if (one) return fp16 ? launch_t<128, 1, true>(p, maps, device, st) : launch_t<128, 1, false>(p, maps, device, st);
+    return fp16 ? launch_t<128, 2, true>(p, maps, device, st) : launch_t<128, 2, false>(p, maps, device, st);
   }
-  if (one) return fp16 ? launch_t<64, 1, true>(p, maps, device, n_sm, st) : launch_t<64, 1, false>(p, maps, device, n_sm, st);
-  return fp16 ? launch_t<64, 2, true>(p, maps, device, n_sm, st) : launch_t<64, 2, false>(p, maps, device, n_sm, st);
+  if (one) return fp16 ? launch_t<64, 1, true>(p, maps, device, st) : launch_t<64, 1, false>(p, maps, device, st);
+  return fp16 ? launch_t<64, 2, true>(p, maps, device, st) : launch_t<64, 2, false>(p, maps, device, st);
 }
 
 }  // namespace qe

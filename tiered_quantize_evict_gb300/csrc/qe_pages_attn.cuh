@@ -15,6 +15,7 @@
 namespace qe {
 
 constexpr int PA_BN = 128;                       // keys of a block
+constexpr int PA_MAX_CTAS = 1024;
 constexpr unsigned long long PA_WAIT_NS = 200000000ull;
 constexpr float PA_LAZY = 8.f;                   // log2 of how far a row's maximum may pass its reference
 
@@ -36,6 +37,7 @@ struct PaParams {
   long long ots, ohs;
   int Hq, G, T, causal, min_piece;
   int q_rows;              // rows of a query buffer
+  int ctas;                // CTAs of the attention kernel: one per SM
   float scale, scale2;     // of the logits; and times log2(e)
   PaRec* rec;              // [CTAs]; NULL: no tile is cut
   float2* part_ml;         // [CTAs][2][NH][128]: reference, sum
@@ -415,7 +417,7 @@ constexpr unsigned long long PA_DESC_V = (1024ull << 16) | (64ull << 32) | (1ull
 // Attention of tiles of at most 16 rows (qe_pages_few.cu).  With 17 to 32 rows as 32 columns it took 148 us where the one half of
 // qe_pages_attn.cu takes 134 (8 drafts of 16 sequences of up to 16K tokens), so those stay there.
 constexpr int PAGES_FEW_ROWS = 16;
-cudaError_t launch_pages_few(const PaParams& p, const CUtensorMap* maps, int fp16, int device, int n_sm, cudaStream_t st);
-cudaError_t launch_pages_join(const PaParams& p, int nh, int fp16, int n_sm, cudaStream_t st);
+cudaError_t launch_pages_few(const PaParams& p, const CUtensorMap* maps, int fp16, int device, cudaStream_t st);
+cudaError_t launch_pages_join(const PaParams& p, int nh, int fp16, cudaStream_t st);
 
 }  // namespace qe

@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
 }
 
 template <int D, bool FP16>
-static cudaError_t few_t(const PaParams& p, const CUtensorMap* maps, int device, int n_sm, cudaStream_t st) {
+static cudaError_t few_t(const PaParams& p, const CUtensorMap* maps, int device, cudaStream_t st) {
   static std::atomic<unsigned long long> ready{0};   // devices whose copy of the kernel has its attribute
   if (device >= 64 || !(ready.load() >> device & 1)) {
     const cudaError_t e = cudaFuncSetAttribute(pages_few_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfShape<D>::SMEM);
@@ -466,19 +466,19 @@ static cudaError_t few_t(const PaParams& p, const CUtensorMap* maps, int device,
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(n_sm);
+  cfg.gridDim = dim3(p.ctas);
   cfg.blockDim = dim3(PF_THREADS);
   cfg.dynamicSmemBytes = PfShape<D>::SMEM;
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, pages_few_kernel<D, FP16>, p, maps[0], maps[1], maps[2]);
-  return e != cudaSuccess || !p.rec ? e : launch_pages_join(p, 1, FP16, n_sm, st);   // (no rec: no tile is cut)
+  return e != cudaSuccess || !p.rec ? e : launch_pages_join(p, 1, FP16, st);   // (no rec: no tile is cut)
 }
 
-cudaError_t launch_pages_few(const PaParams& p, const CUtensorMap* maps, int fp16, int device, int n_sm, cudaStream_t st) {
-  if (p.pg.D == 128) return fp16 ? few_t<128, true>(p, maps, device, n_sm, st) : few_t<128, false>(p, maps, device, n_sm, st);
-  return fp16 ? few_t<64, true>(p, maps, device, n_sm, st) : few_t<64, false>(p, maps, device, n_sm, st);
+cudaError_t launch_pages_few(const PaParams& p, const CUtensorMap* maps, int fp16, int device, cudaStream_t st) {
+  if (p.pg.D == 128) return fp16 ? few_t<128, true>(p, maps, device, st) : few_t<128, false>(p, maps, device, st);
+  return fp16 ? few_t<64, true>(p, maps, device, st) : few_t<64, false>(p, maps, device, st);
 }
 
 }  // namespace qe
