@@ -124,8 +124,8 @@ __device__ __forceinline__ SeqInfo seq_info(const PagesView& pg, const TableView
   const int q1 = min(max(b, r.q0), c.total);
   r.m = q1 - r.q0;
   r.row = c.rows ? c.rows[s] : s;
+  r.len = row_len(pg, t, r.row, report);   // (before q_start is looked at: their loads go together)
   if ((a != r.q0 || b != q1) && report) pages_report(pg, QE_PAGES_ERR_ROW);
-  r.len = row_len(pg, t, r.row, report);
   return r;
 }
 

@@ -583,18 +583,18 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
   }
 }
 
-// Joins the parts of the tiles that were cut: block (x, y) takes one of them, and of it half y / (D / 16) and 16 channels.  A thread
+// Joins the parts of the tiles that were cut: block (x, y) takes one of them, and of it half y / (D / CH) and CH channels.  A thread
 // per row; where there are fewer rows than threads, several threads share a row's parts.  A call of few tiles, which are then cut
-// into many parts, has a block of 512 threads for each of its tiles (180 rows over 30K tokens, two tiles: 74 -> 34 us with the attention
-// itself); one of many tiles 128 threads for each piece, most of which leave at once: looking for the tiles first costs 1.5 us more.
-constexpr int PJ_CH = 16;
-template <int D, int NH, bool FP16, int NT>
+// into many parts, has blocks of 512 threads for each of its tiles, of as few channels as let all run at once (180 rows over 30K tokens,
+// two tiles of 64 channels: 74 -> 21 us with the attention itself; with 8 channels always 23.5); one of many tiles 128 threads for each
+// piece, most of which leave at once: looking for the tiles first costs 1.5 us more.
+template <int D, int NH, bool FP16, int NT, int CH>
 __global__ void __launch_bounds__(NT) pages_join_kernel(const __grid_constant__ PaParams p) {
-  __shared__ float s_m[NT], s_sum[NT], s_o[PJ_CH][NT];
+  __shared__ float s_m[NT], s_sum[NT], s_o[CH][NT];
   __shared__ uint2 s_piece[NT == 128 ? 1 : PA_MAX_CTAS / 32];
   griddep_wait();
   griddep_launch_dependents();
-  const int h = blockIdx.y / (D / PJ_CH), ch = blockIdx.y % (D / PJ_CH) * PJ_CH;
+  const int h = blockIdx.y / (D / CH), ch = blockIdx.y % (D / CH) * CH;
   // the tile's pieces but its first: [c, end)
   int c = blockIdx.x, end, rows;
   PaRec r;
@@ -640,54 +640,80 @@ __global__ void __launch_bounds__(NT) pages_join_kernel(const __grid_constant__ 
   }
   int lg = 0;
   while ((1 << lg) < rows) ++lg;
-  const int row = threadIdx.x & ((1 << lg) - 1), grp = threadIdx.x >> lg, grps = NT >> lg;
-  const int used = min(grps, end - c + 1);   // groups that have a part
-  auto part = [&](int q) { return ((long long)q * 2 + (q < c ? 1 : 0)) * NH + h; };
-  float m = -INFINITY;
-  for (int q = c - 1 + grp; q < end; q += grps) m = fmaxf(m, p.part_ml[part(q) * 128 + row].x);
+  const int row = threadIdx.x & ((1 << lg) - 1), grp = threadIdx.x >> lg;
+  // groups of threads that share a row's parts, so that a group has AT parts (whose loads are all under way before the first is used)
+  constexpr int AT = NT == 512 ? 4 : 2;
+  const int grps = min(NT >> lg, (end - c + AT) / AT);
+  float m = -INFINITY, sum = 0.f, o[CH] = {};
+  if (grp < grps)
+#pragma unroll 1
+    for (int q0 = c - 1 + grp; q0 < end; q0 += AT * grps) {
+      float2 ml[AT];
+      float4 x[AT][CH / 4];
+#pragma unroll
+      for (int a = 0; a < AT; ++a) {
+        const int q = q0 + a * grps;
+        ml[a] = make_float2(-INFINITY, 0.f);
+        if (q < end) {
+          const long long part = ((long long)q * 2 + (q < c ? 1 : 0)) * NH + h;
+          ml[a] = p.part_ml[part * 128 + row];
+          const float4* po = reinterpret_cast<const float4*>(p.part_o + (part * (D / 4) + ch / 4) * 512) + row;
+#pragma unroll
+          for (int e = 0; e < CH / 4; ++e) x[a][e] = po[e * 128];
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int a = 0; a < AT; ++a) top = fmaxf(top, ml[a].x);
+      const float base = top == -INFINITY ? 0.f : top, f0 = ex2(m - base);
+      m = top;
+      sum *= f0;
+#pragma unroll
+      for (int e = 0; e < CH; ++e) o[e] *= f0;
+#pragma unroll
+      for (int a = 0; a < AT; ++a) {
+        const float f = ex2(ml[a].x - base);
+        sum += ml[a].y * f;
+        if (f != 0.f)   // (a part without keys may hold anything)
+#pragma unroll
+          for (int e = 0; e < CH / 4; ++e) {
+            o[4 * e] += x[a][e].x * f;
+            o[4 * e + 1] += x[a][e].y * f;
+            o[4 * e + 2] += x[a][e].z * f;
+            o[4 * e + 3] += x[a][e].w * f;
+          }
+      }
+    }
   if (grps > 1) {
     s_m[threadIdx.x] = m;
     __syncthreads();
-    for (int g = 0; g < used; ++g) m = fmaxf(m, s_m[(g << lg) + row]);
-  }
-  float sum = 0.f, o[PJ_CH] = {};
-#pragma unroll (NT == 512 ? 4 : 2)
-  for (int q = c - 1 + grp; q < end; q += grps) {
-    const float2 ml = p.part_ml[part(q) * 128 + row];
-    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-    sum += ml.y * f;
-    const float4* po = reinterpret_cast<const float4*>(p.part_o + (part(q) * (D / 4) + ch / 4) * 512) + row;
+    for (int g = 0; g < grps; ++g) m = fmaxf(m, s_m[(g << lg) + row]);
+    const float mine = s_m[threadIdx.x], f = mine == -INFINITY ? 0.f : ex2(mine - m);
+    s_sum[threadIdx.x] = sum * f;
 #pragma unroll
-    for (int e = 0; e < PJ_CH / 4; ++e) {
-      const float4 x = po[e * 128];
-      if (f != 0.f) {   // (a part without keys may hold anything)
-        o[4 * e] += x.x * f;
-        o[4 * e + 1] += x.y * f;
-        o[4 * e + 2] += x.z * f;
-        o[4 * e + 3] += x.w * f;
-      }
-    }
-  }
-  if (grps > 1) {
-    s_sum[threadIdx.x] = sum;
-#pragma unroll
-    for (int e = 0; e < PJ_CH; ++e) s_o[e][threadIdx.x] = o[e];
+    for (int e = 0; e < CH; ++e) s_o[e][threadIdx.x] = o[e] * f;
     __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < CH; ++e) o[e] = 0.f;
     if (grp == 0)
-      for (int g = 1; g < used; ++g) {
+      for (int g = 0; g < grps; ++g) {
         sum += s_sum[(g << lg) + row];
 #pragma unroll
-        for (int e = 0; e < PJ_CH; ++e) o[e] += s_o[e][(g << lg) + row];
+        for (int e = 0; e < CH; ++e) o[e] += s_o[e][(g << lg) + row];
       }
   }
   if (grp != 0 || row >= rows) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int t = row / p.G, head = r.kvh * p.G + (row - t * p.G);
   const long long tok = r.tok + h * p.T + t;
-  unsigned x[PJ_CH / 2];
+  unsigned x[CH / 2];
 #pragma unroll
-  for (int e = 0; e < PJ_CH / 2; ++e) x[e] = pa_pack<FP16>(o[2 * e] * inv, o[2 * e + 1] * inv);
-  pa_store32(p.out + tok * p.ots + head * p.ohs + ch, x);
+  for (int e = 0; e < CH / 2; ++e) x[e] = pa_pack<FP16>(o[2 * e] * inv, o[2 * e + 1] * inv);
+  uint16_t* dst = p.out + tok * p.ots + head * p.ohs + ch;
+  if constexpr (CH == 16) pa_store32(dst, x);
+  else if constexpr (CH == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
+  else *reinterpret_cast<uint2*>(dst) = make_uint2(x[0], x[1]);
   if (p.lse && ch == 0) p.lse[tok * p.Hq + head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
 }
 
@@ -739,19 +765,24 @@ static cudaError_t launch_t(const PaParams& p, const CUtensorMap* maps, int devi
 
 template <int D, int NH, bool FP16>
 static cudaError_t join_t(const PaParams& p, cudaStream_t st) {
-  // at most so many tiles; few: their blocks all run at once, two to an SM
+  // at most so many tiles; few: the blocks for them all run at once, two to an SM
   const long long tt = (long long)NH * p.T, tiles = (p.c.n + (p.c.total > p.c.n ? (p.c.total - p.c.n) / tt : 0)) * p.pg.H;
-  const bool few = tiles * NH * (D / PJ_CH) <= 2 * p.ctas;
+  auto few = [&](int ch) { return tiles * NH * (D / ch) <= 2 * p.ctas; };
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(few ? (unsigned)tiles : p.ctas, NH * (D / PJ_CH));
-  cfg.blockDim = dim3(few ? 512 : 128);
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, pages_join_kernel<D, NH, FP16, 512>, p) : cudaLaunchKernelEx(&cfg, pages_join_kernel<D, NH, FP16, 128>, p);
+  auto launch = [&](auto kernel, long long x, int ch, int threads) {
+    cfg.gridDim = dim3((unsigned)x, NH * (D / ch));
+    cfg.blockDim = dim3(threads);
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+  };
+  if (few(4)) return launch(pages_join_kernel<D, NH, FP16, 512, 4>, tiles, 4, 512);
+  if (few(8)) return launch(pages_join_kernel<D, NH, FP16, 512, 8>, tiles, 8, 512);
+  return launch(pages_join_kernel<D, NH, FP16, 128, 16>, p.ctas, 16, 128);
 }
 cudaError_t launch_pages_join(const PaParams& p, int nh, int fp16, cudaStream_t st) {
   if (p.pg.D == 128) {
@@ -786,7 +817,6 @@ cudaError_t launch_pages_attend(const PagesAttendParams& a, int fp16, int device
   const bool one = a.max_q_len > 0 && a.max_q_len <= fit;
   p.T = one ? a.max_q_len : fit;
   p.q_rows = one && p.T * p.G <= 64 ? 64 : 128;
-  p.min_piece = 2;
   const int nh = one ? 1 : 2;
   if (pages_attend_cuts(g, a.t)) {
     char* at = static_cast<char*>(ws);

@@ -35,7 +35,7 @@ struct PaParams {
   uint16_t* out;
   float* lse;
   long long ots, ohs;
-  int Hq, G, T, causal, min_piece;
+  int Hq, G, T, causal;
   int q_rows;              // rows of a query buffer
   int ctas;                // CTAs of the attention kernel: one per SM
   float scale, scale2;     // of the logits; and times log2(e)
@@ -91,6 +91,7 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
 constexpr int PA_TILE_COST = 1;
 // A tile of so few blocks is never cut: a block takes a CTA 1.4 us, a join 3 us.
 constexpr int PA_WHOLE = 4;
+constexpr int PA_LEAST = 2;      // length of a piece, at least
 
 struct PaSeq {
   SeqInfo s;
@@ -176,20 +177,25 @@ struct PaCursor {
   __device__ __forceinline__ bool second_half(const PaParams& p) const { return NH == 2 && j * 2 * p.T + p.T < q.s.m; }
 };
 
-// Every CTA (of NT threads) finds its piece: sums the sequences' lengths on the line, cuts it, finds the places of its two cuts.
+// Every CTA (of NT threads) finds its piece: sums the sequences' lengths on the line, cuts it, finds the places of its two cuts.  Up
+// to 32 sequences are a warp's work: two warps do it, one for each cut, without barriers in between (one token over a short cache, the
+// whole call: 9.7 -> 9.2 us).
 template <int NH, int NT>
 __device__ __noinline__ void pa_find(const PaParams& p, PaPlace* pl, long long* s_w) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int W = NT / 32;
   const int c = blockIdx.x;
-  // exclusive prefix of x over the block, and the total
-  auto scan = [&](long long x, long long& total) {
-    long long y = x;
+  auto warp_scan = [&](long long y) {
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) {
       const long long z = __shfl_up_sync(~0u, y, k);
       if (lane >= k) y += z;
     }
+    return y;
+  };
+  // exclusive prefix of x over the block, and the total
+  auto scan = [&](long long x, long long& total) {
+    const long long y = warp_scan(x);
     if (lane == 31) s_w[warp] = y;
     __syncthreads();
     long long before = 0, all = 0;
@@ -209,44 +215,67 @@ __device__ __noinline__ void pa_find(const PaParams& p, PaPlace* pl, long long* 
     s = q.s;
     return pa_head_length<NH>(p, q) * p.pg.H;
   };
-  if (tid < 2) pl[tid].i = p.c.n, pl[tid].h = pl[tid].j = pl[tid].b = 0;
+  // where the two cuts of piece c are on a line; false: there are not so many pieces
+  long long cut[2];
+  int pieces;
+  auto make_cuts = [&](long long line) {
+    const long long most = line / PA_LEAST;
+    pieces = most < 1 ? 1 : (most > gridDim.x ? (int)gridDim.x : (int)most);
+    const long long each = div_ll(line, pieces);
+    const int over = (int)(line - each * pieces);
+    cut[0] = each * c + over * c / pieces;
+    cut[1] = each * (c + 1) + over * (c + 1) / pieces;
+    const bool there = c < pieces && line > 0;
+    if (!there && tid == 0 && p.rec) p.rec[c] = PaRec{-1, 0, 0, 0, 0, 0};
+    return there;
+  };
   SeqInfo s;
-  long long line, x = length(tid, c == 0, s), pre = scan(x, line);
-#pragma unroll 1
-  for (int base = NT; base < p.c.n; base += NT) {   // (more sequences than threads)
-    long long tot;
-    SeqInfo z;
-    scan(length(base + tid, c == 0, z), tot);
-    line += tot;
-  }
-  const long long most = div_ll(line, p.min_piece);
-  const int pieces = most < 1 ? 1 : (most > gridDim.x ? (int)gridDim.x : (int)most);
-  const long long each = div_ll(line, pieces);
-  const int over = (int)(line - each * pieces);
-  const long long cut[2] = {each * c + over * c / pieces, each * (c + 1) + over * (c + 1) / pieces};
-  if (c >= pieces || line == 0) {
-    if (tid == 0 && p.rec) p.rec[c] = PaRec{-1, 0, 0, 0, 0, 0};
-    __syncthreads();
-    return;
-  }
-  long long at = 0;
-#pragma unroll 1
-  for (int base = 0; base < p.c.n; base += NT) {
-    if (base > 0) x = length(base + tid, false, s);
-    if (p.c.n > NT) {
-      long long tot;
-      pre = at + scan(x, tot);
-      at += tot;
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (cut[k] >= pre && cut[k] < pre + x) {
-        pl[k].i = base + tid;
-        pl[k].s = s;
-        pl[k].rem = cut[k] - pre;
+  if (p.c.n <= 32) {
+    if (warp < 2) {
+      const long long x = length(lane, c == 0 && warp == 0, s), y = warp_scan(x);
+      const bool there = make_cuts(__shfl_sync(~0u, y, 31));
+      const long long mine = warp == 0 ? cut[0] : cut[1];
+      const bool here = there && mine >= y - x && mine < y;
+      if (!__any_sync(~0u, here)) {
+        if (lane == 0) pl[warp].i = p.c.n, pl[warp].h = pl[warp].j = pl[warp].b = 0;
+      } else if (here) {
+        pl[warp].i = lane;
+        pl[warp].s = s;
+        pl[warp].rem = mine - (y - x);
       }
+      __syncwarp();
+    }
+  } else {
+    if (tid < 2) pl[tid].i = p.c.n, pl[tid].h = pl[tid].j = pl[tid].b = 0;
+    long long line, x = length(tid, c == 0, s), pre = scan(x, line);
+#pragma unroll 1
+    for (int base = NT; base < p.c.n; base += NT) {   // (more sequences than threads)
+      long long tot;
+      SeqInfo z;
+      scan(length(base + tid, c == 0, z), tot);
+      line += tot;
+    }
+    if (make_cuts(line)) {
+      long long at = 0;
+#pragma unroll 1
+      for (int base = 0; base < p.c.n; base += NT) {
+        if (base > 0) x = length(base + tid, false, s);
+        if (p.c.n > NT) {
+          long long tot;
+          pre = at + scan(x, tot);
+          at += tot;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (cut[k] >= pre && cut[k] < pre + x) {
+            pl[k].i = base + tid;
+            pl[k].s = s;
+            pl[k].rem = cut[k] - pre;
+          }
+      }
+    }
+    __syncthreads();
   }
-  __syncthreads();
   if (warp < 2 && pl[warp].i < p.c.n) {
     PaSeq q;
     q.s = pl[warp].s;
