@@ -29,119 +29,152 @@ __device__ __forceinline__ unsigned pages_pack(float lo, float hi) {
   return pack_bf16x2(lo, hi);
 }
 
-constexpr int APPEND_MAX_TOKENS = 8;
+constexpr int APPEND_MAX_TOKENS = 8, APPEND_THREADS = 256;
+constexpr int APPEND_BLOCKS = 4;   // of an SM
+constexpr int APPEND_DEEP = 3;     // rows that a thread loads at a time (2: 68.4 us where 3 takes 65.7; 6, with three blocks: 68.6)
+// Tokens that a block takes at a time, times head_dim: 4 of 128 channels or 8 of 64, so that a thread has one angle at most.
+constexpr int APPEND_CHANNELS = 2 * APPEND_THREADS;
 
-// A block rotates and stores tokens_per_block packed tokens.  The angle of (token, pair) is taken once
+// Which sequence token tok belongs to: how many of q_start[1 ..] are at or below it.  A warp looks at 32 of them at a time.
+__device__ __forceinline__ int pages_find_seq(const ChunksView& c, int tok) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = c.n;
+  while (lo < hi) {
+    const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
+    const int k = __popc(__ballot_sync(~0u, i < hi && c.q_start[i + 1] <= tok));
+    if (step == 1) return lo + k;
+    hi = min(hi, lo + k * step);
+    lo = k > 0 ? lo + (k - 1) * step + 1 : hi;
+  }
+  return lo;
+}
+
+// A block rotates and stores its share of the packed tokens, a few at a time.  The angle of (token, pair) is taken once
 // for all heads: position * turn mod 2^64 is the exact fraction of a turn (64-bit integers wrap at
 // whole turns), whose upper 32 bits, as a signed number of 2^-31 half turns, go to sincospif -- no
 // 64-bit floating point, and no loss at far positions.
+// Bound by memory, and before that by a chain of dependent loads (sequence, its length, page): the positions and the first rows
+// are on their way while a warp per token follows it.  All blocks run at once, with equal shares of the tokens (16K tokens of 48 heads of
+// 128 channels: 65.7 us, 5.7 TB/s read and written; blocks of 4 tokens each: 68; 256 sequences of a token: 4.9 us).
 template <bool FP16>
-__global__ void __launch_bounds__(256) pages_append_kernel(const __grid_constant__ PagesAppendParams p) {
+__global__ void __launch_bounds__(APPEND_THREADS, APPEND_BLOCKS) pages_append_kernel(const __grid_constant__ PagesAppendParams p) {
   __shared__ float2 s_cs[APPEND_MAX_TOKENS][64];
   __shared__ int s_pos[APPEND_MAX_TOKENS];         // cache position, < 0: none; INT_MIN: not a token of the call
   __shared__ long long s_at[APPEND_MAX_TOKENS];    // offset of head 0 in the pool, < 0: dropped
-  const int t0 = blockIdx.x * p.tokens_per_block;
-  const int nt = min(p.tokens_per_block, p.c.total - t0);
   if (blockIdx.x == 0) check_starts(p.pg, p.c);
-  if (threadIdx.x < nt) {
-    const int tok = t0 + threadIdx.x;
-    int lo = 0, hi = p.c.n;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (p.c.q_start[mid + 1] <= tok) lo = mid + 1; else hi = mid;
-    }
-    int pos = INT_MIN;
-    long long at = -1;
-    if (lo < p.c.n) {
-      const SeqInfo s = seq_info(p.pg, p.t, p.c, lo, true);
-      if (tok >= s.q0 && tok < s.q0 + s.m) {
-        pos = s.len - s.m + (tok - s.q0);
-        if (pos >= 0 && s.len > 0) {
-          const int page = page_at(p.pg, p.t, s.row, pos);
-          if (page >= 0) at = p.layer * p.pg.ls + page * p.pg.ps + (pos & (p.pg.S - 1)) * p.pg.ts;
-        }
-      }
-    }
-    s_pos[threadIdx.x] = pos;
-    s_at[threadIdx.x] = at;
-  }
-  __syncthreads();
-  const int half = p.R / 2;
-  for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
-    const int t = i / half, c = i - t * half;
-    const long long pos = p.positions ? p.positions[p.axis[c] * p.pos_stride + t0 + t] : max(s_pos[t], 0);
-    const int x = (int)(((unsigned long long)pos * p.turn[c]) >> 32);
-    float sn, cs;
-    sincospif((float)x * 0x1p-31f, &sn, &cs);
-    s_cs[t][c] = make_float2(cs, sn);
-  }
-  __syncthreads();
+  const int most = APPEND_CHANNELS / p.pg.D, half = p.R / 2, Hq = p.q ? p.Hq : 0;
   // A thread keeps one token and one vector (8 adjacent channels; with halves 8 of the first half and their partners) and
   // walks the heads, so the sines and cosines stay in registers and several heads' loads are in flight.
   const int nv = p.halves ? p.R / 16 + (p.pg.D - p.R) / 8 : p.pg.D / 8;
   const int grp = threadIdx.x / nv, v = threadIdx.x - grp * nv;
-  const int slots = (int)blockDim.x / nv / nt;                 // threads that share a token's heads
-  const int t = grp / slots, h0 = grp - t * slots;
-  if (t >= nt || s_pos[t] == INT_MIN) return;
-  const long long tok = t0 + t;
   const bool paired = p.halves && v < p.R / 16;
   const int c0 = paired ? v * 8 : (p.halves ? p.R + (v - p.R / 16) * 8 : v * 8);   // first channel, and its partner's
   const int c1 = c0 + half;
   const int angles = paired ? 8 : (p.halves ? 0 : min(4, max(0, half - v * 4)));
-  float2 cs[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) cs[k] = k < angles ? s_cs[t][paired ? c0 + k : v * 4 + k] : make_float2(1.f, 0.f);
-  auto walk = [&](const uint16_t* src, long long shs, uint16_t* dst, long long dhs, int heads, bool rot) {
-    constexpr int DEEP = 4;
+  const int at = half ? (int)threadIdx.x / half : APPEND_MAX_TOKENS, ac = threadIdx.x - at * half;   // this thread's angle: token, pair
+  const int end = (int)((long long)p.c.total * (blockIdx.x + 1) / gridDim.x);
+  int t0 = (int)((long long)p.c.total * blockIdx.x / gridDim.x);
 #pragma unroll 1
-    for (int h = h0; h < heads; h += DEEP * slots) {
-      uint4 x[DEEP], y[DEEP];
+  for (int nt; t0 < end; t0 += nt) {
+    nt = min(most, end - t0);
+    const int slots = APPEND_THREADS / nv / nt;                // threads that share a token's heads
+    const int t = grp / slots, h0 = grp - t * slots;
+    const long long tok = t0 + t;
+    // the token's rows: query heads, keys, values; first what a thread of slot h0 loads before it knows where they go
+    constexpr int DEEP = APPEND_DEEP;
+    uint4 x[DEEP], y[DEEP];
+    auto load = [&](int rows, int h) {
 #pragma unroll
-      for (int k = 0; k < DEEP; ++k)
-        if (h + k * slots < heads) {
-          x[k] = *reinterpret_cast<const uint4*>(src + (h + k * slots) * shs + c0);
-          if (paired) y[k] = *reinterpret_cast<const uint4*>(src + (h + k * slots) * shs + c1);
+      for (int k = 0; k < DEEP; ++k) {
+        const int r = h + k * slots;
+        if (r < rows) {
+          const uint16_t* src = r < Hq ? p.q + tok * p.qts + r * p.qhs
+                                       : (r < Hq + p.pg.H ? p.k + tok * p.kts + (r - Hq) * p.khs : p.v + tok * p.vts + (r - Hq - p.pg.H) * p.vhs);
+          x[k] = *reinterpret_cast<const uint4*>(src + c0);
+          if (paired) y[k] = *reinterpret_cast<const uint4*>(src + c1);
         }
-#pragma unroll
-      for (int k = 0; k < DEEP; ++k)
-        if (h + k * slots < heads) {
-          unsigned *a = &x[k].x, *b = &y[k].x;
-          if (rot && paired) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 xa = pages_unpack<FP16>(a[e]), ya = pages_unpack<FP16>(b[e]), q0 = cs[2 * e], q1 = cs[2 * e + 1];
-              a[e] = pages_pack<FP16>(xa.x * q0.x - ya.x * q0.y, xa.y * q1.x - ya.y * q1.y);
-              b[e] = pages_pack<FP16>(xa.x * q0.y + ya.x * q0.x, xa.y * q1.y + ya.y * q1.x);
+      }
+    };
+    long long turns = 0;
+    if (p.positions && at < nt) turns = p.positions[p.axis[ac] * p.pos_stride + t0 + at];
+    if (t < nt) load(Hq + 2 * p.pg.H, h0);
+
+    const int warp = threadIdx.x >> 5;
+    if (warp < nt) {
+      const int mine = t0 + warp, seq = pages_find_seq(p.c, mine);
+      if ((threadIdx.x & 31) == 0) {
+        int pos = INT_MIN;
+        long long to = -1;
+        if (seq < p.c.n) {
+          const SeqInfo s = seq_info(p.pg, p.t, p.c, seq, true);
+          if (mine >= s.q0 && mine < s.q0 + s.m) {
+            pos = s.len - s.m + (mine - s.q0);
+            if (pos >= 0 && s.len > 0) {
+              const int page = page_at(p.pg, p.t, s.row, pos);
+              if (page >= 0) to = p.layer * p.pg.ls + page * p.pg.ps + (pos & (p.pg.S - 1)) * p.pg.ts;
             }
-          } else if (rot) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (e < angles) {
-                const float2 xa = pages_unpack<FP16>(a[e]);
-                a[e] = pages_pack<FP16>(xa.x * cs[e].x - xa.y * cs[e].y, xa.x * cs[e].y + xa.y * cs[e].x);
-              }
           }
-          *reinterpret_cast<uint4*>(dst + (h + k * slots) * dhs + c0) = x[k];
-          if (paired) *reinterpret_cast<uint4*>(dst + (h + k * slots) * dhs + c1) = y[k];
         }
+        s_pos[warp] = pos;
+        s_at[warp] = to;
+      }
     }
-  };
-  if (p.q) walk(p.q + tok * p.qts, p.qhs, p.q_out + tok * p.ots, p.ohs, p.Hq, true);
-  if (s_at[t] >= 0) {
-    walk(p.k + tok * p.kts, p.khs, p.pg.k + s_at[t], p.pg.hs, p.pg.H, true);
-    walk(p.v + tok * p.vts, p.vhs, p.pg.v + s_at[t], p.pg.hs, p.pg.H, false);
+    __syncthreads();
+    if (at < nt) {
+      if (!p.positions) turns = max(s_pos[at], 0);
+      const int turn = (int)(((unsigned long long)turns * p.turn[ac]) >> 32);
+      float sn, cs;
+      sincospif((float)turn * 0x1p-31f, &sn, &cs);
+      s_cs[at][ac] = make_float2(cs, sn);
+    }
+    __syncthreads();
+    if (t < nt && s_pos[t] != INT_MIN) {
+      float2 cs[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) cs[k] = k < angles ? s_cs[t][paired ? c0 + k : v * 4 + k] : make_float2(1.f, 0.f);
+      const long long to = s_at[t];
+      const int rows = to >= 0 ? Hq + 2 * p.pg.H : Hq;
+#pragma unroll 1
+      for (int h = h0; h < rows; h += DEEP * slots) {
+        if (h != h0) load(rows, h);
+#pragma unroll
+        for (int k = 0; k < DEEP; ++k) {
+          const int r = h + k * slots;
+          if (r < rows) {
+            unsigned *a = &x[k].x, *b = &y[k].x;
+            const bool rot = r < Hq + p.pg.H;
+            if (rot && paired) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 xa = pages_unpack<FP16>(a[e]), ya = pages_unpack<FP16>(b[e]), q0 = cs[2 * e], q1 = cs[2 * e + 1];
+                a[e] = pages_pack<FP16>(xa.x * q0.x - ya.x * q0.y, xa.y * q1.x - ya.y * q1.y);
+                b[e] = pages_pack<FP16>(xa.x * q0.y + ya.x * q0.x, xa.y * q1.y + ya.y * q1.x);
+              }
+            } else if (rot) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (e < angles) {
+                  const float2 xa = pages_unpack<FP16>(a[e]);
+                  a[e] = pages_pack<FP16>(xa.x * cs[e].x - xa.y * cs[e].y, xa.x * cs[e].y + xa.y * cs[e].x);
+                }
+            }
+            uint16_t* dst = r < Hq ? p.q_out + tok * p.ots + r * p.ohs
+                                   : (rot ? p.pg.k + to + (r - Hq) * p.pg.hs : p.pg.v + to + (r - Hq - p.pg.H) * p.pg.hs);
+            *reinterpret_cast<uint4*>(dst + c0) = x[k];
+            if (paired) *reinterpret_cast<uint4*>(dst + c1) = y[k];
+          }
+        }
+      }
+    }
+    __syncthreads();   // (positions, places and angles are read)
   }
 }
 
-cudaError_t launch_pages_append(const PagesAppendParams& p0, int fp16, int n_sm, cudaStream_t st) {
-  PagesAppendParams p = p0;
-  // few tokens: a block each, so that they spread over the SMs; many: 8 a block, one table search for 8
-  int tb = p.c.total / (2 * n_sm);
-  tb = tb < 1 ? 1 : (tb > APPEND_MAX_TOKENS ? APPEND_MAX_TOKENS : tb);
-  p.tokens_per_block = tb;
-  const int blocks = (p.c.total + tb - 1) / tb;
-  if (fp16) pages_append_kernel<true><<<blocks, 256, 0, st>>>(p);
-  else pages_append_kernel<false><<<blocks, 256, 0, st>>>(p);
+cudaError_t launch_pages_append(const PagesAppendParams& p, int fp16, int n_sm, cudaStream_t st) {
+  // all blocks run at once, with equal shares of the tokens
+  const int blocks = p.c.total < n_sm * APPEND_BLOCKS ? p.c.total : n_sm * APPEND_BLOCKS;
+  if (fp16) pages_append_kernel<true><<<blocks, APPEND_THREADS, 0, st>>>(p);
+  else pages_append_kernel<false><<<blocks, APPEND_THREADS, 0, st>>>(p);
   return cudaGetLastError();
 }
 

@@ -41,7 +41,6 @@ struct PagesAppendParams {
   int R, halves;              // rotated channels (0: none)
   const int* positions;
   long long pos_stride;
-  int tokens_per_block;
   signed char axis[64];
   unsigned long long turn[64];   // inv_freq / (2 pi) mod 1, in units of 2^-64 turns
 };
