@@ -11,6 +11,21 @@
 
 namespace qe {
 
+// a launch that may start while the one before it still runs (it waits inside)
+template <class K, class... A>
+static cudaError_t launch_after(K kernel, unsigned blocks, unsigned threads, cudaStream_t st, A... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---------------------------------------------------------------------------- append
 template <bool FP16>
 __device__ __forceinline__ float2 pages_unpack(unsigned x) {
@@ -61,6 +76,7 @@ __global__ void __launch_bounds__(APPEND_THREADS, APPEND_BLOCKS) pages_append_ke
   __shared__ float2 s_cs[APPEND_MAX_TOKENS][64];
   __shared__ int s_pos[APPEND_MAX_TOKENS];         // cache position, < 0: none; INT_MIN: not a token of the call
   __shared__ long long s_at[APPEND_MAX_TOKENS];    // offset of head 0 in the pool, < 0: dropped
+  griddep_wait();
   if (blockIdx.x == 0) check_starts(p.pg, p.c);
   const int most = APPEND_CHANNELS / p.pg.D, half = p.R / 2, Hq = p.q ? p.Hq : 0;
   // A thread keeps one token and one vector (8 adjacent channels; with halves 8 of the first half and their partners) and
@@ -173,9 +189,7 @@ __global__ void __launch_bounds__(APPEND_THREADS, APPEND_BLOCKS) pages_append_ke
 cudaError_t launch_pages_append(const PagesAppendParams& p, int fp16, int n_sm, cudaStream_t st) {
   // all blocks run at once, with equal shares of the tokens
   const int blocks = p.c.total < n_sm * APPEND_BLOCKS ? p.c.total : n_sm * APPEND_BLOCKS;
-  if (fp16) pages_append_kernel<true><<<blocks, APPEND_THREADS, 0, st>>>(p);
-  else pages_append_kernel<false><<<blocks, APPEND_THREADS, 0, st>>>(p);
-  return cudaGetLastError();
+  return fp16 ? launch_after(pages_append_kernel<true>, blocks, APPEND_THREADS, st, p) : launch_after(pages_append_kernel<false>, blocks, APPEND_THREADS, st, p);
 }
 
 // ---------------------------------------------------------------------------- planning
@@ -474,21 +488,6 @@ __global__ void __launch_bounds__(256) pages_apply_kernel(const __grid_constant_
                                                           const __grid_constant__ PlanSpace ws) {
   griddep_wait();
   apply_moves<FORK, 256>(pg, t, n, ws, blockIdx.x, gridDim.x);
-}
-
-// a launch that may start while the one before it still runs (it waits inside)
-template <class K, class... A>
-static cudaError_t launch_after(K kernel, unsigned blocks, unsigned threads, cudaStream_t st, A... args) {
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <bool FORK>
