@@ -27,7 +27,8 @@
 //    is of the unrounded ones.  With NH = 1, where the tensor cores wait for memory anyway, what the rounding leaves is kept as
 //    a second operand and multiplied too: error against 64 bits 1.45 -> 1.0 times that of the result's own rounding.
 // mbarriers: kfull / kempty per slot, qfull / qempty per query buffer, s[i] (S i complete; tensor-core commit),
-// p[i][0], p[i][1] (P i's first and second half of the keys written; one arrival per softmax warp), o[h] (half
+// p[i][0], p[i][1] (P i's first and last 32 of each 64 keys
+// written; one arrival per softmax warp: the products of the first start while the softmax is at the last, 32K chunk 705 -> 682 us), o[h] (half
 // h's O of a tile complete; with NH = 1 o[i]: the P V of an even or odd block complete.  An S tells only that the P V two blocks
 // before is, so one barrier's parity could mean the last P V or the one before), turn[h] (half h may issue).  Every wait is bounded (0.2 s); one that expires sets
 // QE_PAGES_ERR_TIMEOUT and an abort flag that ends all loops, and the CTA leaves after what it issued has landed.
@@ -147,8 +148,8 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
       mbar_init(smem_u32(&b_qfull[i]), 1);
       mbar_init(smem_u32(&b_qempty[i]), 1);
       mbar_init(smem_u32(&b_s[i]), 1);
-      mbar_init(smem_u32(&b_p[i][0]), 4);
-      mbar_init(smem_u32(&b_p[i][1]), 4);
+      mbar_init(smem_u32(&b_p[i][0]), 8);
+      mbar_init(smem_u32(&b_p[i][1]), 8);
       mbar_init(smem_u32(&b_o[i]), 1);
       mbar_init(smem_u32(&b_turn[i]), 1);
     }
@@ -247,14 +248,20 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
         pa_commit(smem_u32(&b_kempty[kslot]));
         if (q_done) pa_commit(smem_u32(&b_qempty[qb]));
       };
-      auto pv = [&](int part, int sb, int vslot, bool acc) {   // O += P sb V over one half of the keys (by one lane)
-        const unsigned long long b = (PA_DESC_V | ((sm_kv + vslot * Sh::TILE) >> 4)) + part * 512;
+      // O += P sb V over the first (part 0) or last 32 of each 64 keys (by one lane)
+      auto pv = [&](int part, int sb, int vslot, bool acc) {
+        const unsigned long long b = PA_DESC_V | ((sm_kv + vslot * Sh::TILE) >> 4);
 #pragma unroll
-        for (int k = 0; k < PA_BN / 32; ++k)
-          pa_mma_ts(t_o, tm + sb * 128 + part * 32 + k * 8, b + k * 128, ID_O, acc || k > 0);
+        for (int i = 0; i < 4; ++i) {
+          const int k = (i >> 1) * 4 + part * 2 + (i & 1);   // 16 keys
+          pa_mma_ts(t_o, tm + sb * 128 + k * 8, b + k * 128, ID_O, acc || i > 0);
+        }
         if (NH == 1)   // the remainders of P
 #pragma unroll
-          for (int k = 0; k < PA_BN / 32; ++k) pa_mma_ts(t_o, tm + sb * 128 + 64 + part * 32 + k * 8, b + k * 128, ID_O, true);
+          for (int i = 0; i < 4; ++i) {
+            const int k = (i >> 1) * 4 + part * 2 + (i & 1);
+            pa_mma_ts(t_o, tm + sb * 128 + 64 + k * 8, b + k * 128, ID_O, true);
+          }
       };
 #pragma unroll 1
       for (int n = 0; more; ++n) {
@@ -506,14 +513,22 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
               }
               pa_st16(t_s + ch * 32 + c * 16, pk);
               if (NH == 1) pa_st16(t_s + 64 + ch * 32 + c * 16, rest);
+              if (c == 0) {   // the products of these may start
+                pa_wait_st();
+                pa_fence_before();
+                __syncwarp();
+                if (lane == 0) pa_arrive(smem_u32(&b_p[sb][0]));
+              }
             }
             const unsigned long long a = f2_add(acc[0], acc[1]);
             sum += f2_lo(a) + f2_hi(a);
             pa_wait_st();
+          } else {
+            if (lane == 0) pa_arrive(smem_u32(&b_p[sb][0]));
           }
           pa_fence_before();
           __syncwarp();
-          if (lane == 0) pa_arrive(smem_u32(&b_p[sb][ch]));
+          if (lane == 0) pa_arrive(smem_u32(&b_p[sb][1]));
         }
 
         // ------------------------------ the tile's end in this piece

@@ -342,11 +342,13 @@ class PagePool:
         n = seqs._shape[0] if rows is None else _ints("rows", rows, self._index)
         shape = (n, self.n_kv_heads, max(0, n_tokens), self.head_dim)
         if out is None:
-            out = [torch.empty(shape, dtype=self.dtype, device=self.device) for _ in range(2)]
-        k, v = out
-        for t in (k, v):
-            if t.dtype is not self.dtype or t.get_device() != self._index or t.shape != shape or not t.is_contiguous():
-                raise _bad(f"out must be two contiguous {self.dtype} tensors {list(shape)} on {self.device}")
+            k = torch.empty(shape, dtype=self.dtype, device=self.device)
+            v = torch.empty_like(k)
+        else:
+            k, v = out
+            for t in (k, v):
+                if t.dtype is not self.dtype or t.get_device() != self._index or t.shape != shape or not t.is_contiguous():
+                    raise _bad(f"out must be two contiguous {self.dtype} tensors {list(shape)} on {self.device}")
         st = self._lib.qe_pages_gather(self._ref, layer, self._seqs(seqs), rows.data_ptr() if rows is not None else None, n, start,
                                        n_tokens, k.data_ptr(), v.data_ptr(), _raw_stream(self._index))
         if st:
