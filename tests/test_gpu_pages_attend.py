@@ -141,6 +141,22 @@ def test_long_caches_of_several_sequences(torch, d, m, hint):
     run(torch, [(m, int(x)) for x in rng.integers(4000, 9000, n)], hq=4 if m < 16 else 2, hkv=2 if m < 16 else 1, d=d, ps=64, hint=hint, seed=m)
 
 
+@pytest.mark.parametrize("lens,hq,hkv,d,hint", [
+    ([(60, 15000)], 6, 2, 64, 0), ([(100, 6000), (3, 5000)], 1, 1, 128, 100), ([(300, 3000), (7, 900), (40, 700)], 4, 2, 128, 0),
+    ([(1, 9000), (1, 300)], 4, 4, 64, 1), ([(5, 4000)] * 3, 9, 3, 128, 5), ([(70, 2500)] + [(1, 600)] * 5, 8, 4, 64, 70)])
+def test_rows_cut_into_many_parts(torch, lens, hq, hkv, d, hint):
+    """Few tiles over long caches: each is cut into many parts, joined by blocks of 4, 8 or 16 channels."""
+    run(torch, lens, hq=hq, hkv=hkv, d=d, ps=32, hint=hint, seed=len(lens))
+
+
+@pytest.mark.parametrize("n,hint", [(32, 0), (33, 0), (33, 9), (33, 1), (64, 40)])
+def test_as_many_sequences_as_a_warp(torch, n, hint):
+    """Sequences of very different lengths, some empty, around the number whose pieces a warp finds."""
+    rng = np.random.default_rng(n + hint)
+    m = np.minimum(rng.integers(0, 10 if hint != 1 else 2, n), hint or 100)
+    run(torch, [(int(a), int(a + b)) for a, b in zip(m, rng.integers(0, 300, n) + 4000 * (np.arange(n) == n - 1))], hq=4, hkv=2, d=64, ps=16, hint=hint)
+
+
 @pytest.mark.parametrize("hint", [0, 1])
 def test_many_short_sequences(torch, hint):
     rng = np.random.default_rng(7)

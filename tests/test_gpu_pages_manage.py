@@ -95,6 +95,31 @@ def test_append_without_queries_positions_or_rope(torch):
         assert torch.equal(c.k[0, c.table[r][p // 16], :, p % 16].cpu(), k[i])
 
 
+@pytest.mark.parametrize("n,most,hq,hkv,d,rot,halves", [(1100, 3, 5, 3, 64, 64, True), (40, 130, 16, 1, 128, 32, False), (3, 900, 1, 1, 128, 128, True)])
+def test_append_many_tokens(torch, n, most, hq, hkv, d, rot, halves):
+    """More sequences than two steps of the search tell apart, more tokens than blocks; chunks of no token among them."""
+    import tiered_quantize_evict_gb300 as qe
+    rng = np.random.default_rng(n)
+    m = rng.integers(0, most + 1, n)
+    lens = m + rng.integers(0, 20, n)
+    ps = 16
+    c = Case(torch, lens.tolist(), hkv=hkv, d=d, ps=ps)
+    pool, seqs = c.objects(qe)
+    starts = np.cumsum([0, *m])
+    total = int(starts[-1])
+    k, v, q = (c.draw(total, h, d) for h in (hkv, hkv, hq))
+    f = [1e4 ** (-2 * i / rot) for i in range(rot // 2)]
+    got = pool.append(0, k.to(c.dev), v.to(c.dev), c.ints(starts), seqs, q=q.to(c.dev), rope=qe.Rope(d, rot_dim=rot, halves=halves))
+    pool.check()
+    seq = np.repeat(np.arange(n), m)
+    pos = lens[seq] - m[seq] + np.arange(total) - starts[seq]
+    axis = [0] * (rot // 2)
+    check_rotated(torch, c.dt, bits(got), op.rotate(bits(q), pos[None].astype(np.int32), axis, f, rot, halves), bits(q))
+    page, row = torch.from_numpy(c.table[seq, pos // ps].astype(np.int64)).to(c.dev), torch.from_numpy(pos % ps).to(c.dev)
+    check_rotated(torch, c.dt, bits(c.k[0][page, :, row]), op.rotate(bits(k), pos[None].astype(np.int32), axis, f, rot, halves), bits(k))
+    assert torch.equal(c.v[0][page, :, row].cpu(), v)
+
+
 def test_append_longer_than_the_cache_drops_keys(torch):
     import tiered_quantize_evict_gb300 as qe
     c = Case(torch, [3, 0], hkv=1, d=64, ps=16, garbage=0.0)
