@@ -46,37 +46,19 @@ struct PaParams {
 
 // ---------------------------------------------------------------------------- the line of blocks
 
-// sum over i < n of floor((a i + b) / 128), a >= 0, b >= 0.  With i = 128 k + j the term is a k + floor((a j + b) / 128), so it
-// comes down to n <= 128: over a whole period the residues of a j + b are b mod g, + g, + 2 g, ... g times over (g = gcd(a, 128)),
-// which gives the sum in closed form; the rest by Euclid's recursion on (128, a) in 32 bits.
+// sum over i < n of floor((a i + b) / 128), a >= 0, b >= 0.  With a and c = b reduced below 128, g = gcd(a, 128) and L = 128 / g, the
+// residues of a j + c over a period j < L are c mod g, + g, + 2 g, ...: a period's sum is (a / g - 1) (L - 1) / 2 + floor(c / g), and a
+// period later every term is a / g larger.  What is left, fewer than L terms, is added up one by one (L is 2 where a tile is 64 tokens).
 __device__ __forceinline__ long long floor_sum128(int n, int a, long long b) {
   long long ans = n * (b >> 7) + (long long)n * (n - 1) / 2 * (a >> 7);
   a &= 127;
   const int c = (int)(b & 127);
-  const int q = n >> 7;
-  unsigned r = n & 127;
-  if (q) {
-    const int g = a ? a & -a : 128;
-    ans += 64ll * a * q * (q - 1) + (long long)q * ((127 * a + g) / 2 - 64 + c - (c & (g - 1))) + (long long)r * a * q;
-  }
-  unsigned m = 128, x = a, y = c, sum = 0;
-  while (r) {
-    if (x >= m) {
-      sum += r * (r - 1) / 2 * (x / m);
-      x %= m;
-    }
-    if (y >= m) {
-      sum += r * (y / m);
-      y %= m;
-    }
-    const unsigned top = x * r + y;
-    if (top < m) break;
-    r = top / m;
-    y = top % m;
-    const unsigned z = m;
-    m = x;
-    x = z;
-  }
+  const int lg = a ? __ffs(a) - 1 : 7, L = 128 >> lg, A = a >> lg;
+  const int q = n >> (7 - lg), r = n & (L - 1);
+  ans += (long long)q * (q - 1) / 2 * (L * A) + (long long)q * (((A - 1) * (L - 1) >> 1) + (c >> lg)) + (long long)r * A * q;
+  int sum = 0;
+#pragma unroll 4
+  for (int j = 0; j < r; ++j) sum += (a * j + c) >> 7;
   return ans + sum;
 }
 
@@ -128,7 +110,7 @@ __device__ __forceinline__ long long pa_head_length(const PaParams& p, const PaS
 struct PaPlace {
   int i, h, j, b;
   SeqInfo s;
-  long long rem;      // (while it is being found) how far behind the sequence's start
+  long long rem, head;   // (while it is being found) how far behind the sequence's start; length of a KV head
 };
 
 // A walk from one place to another, tile by tile.
@@ -209,11 +191,11 @@ __device__ __noinline__ void pa_find(const PaParams& p, PaPlace* pl, long long* 
     __syncthreads();
     return before + y - x;
   };
-  auto length = [&](int i, bool report, SeqInfo& s) {
+  auto length = [&](int i, bool report, SeqInfo& s, long long& head) {
     if (i >= p.c.n) return 0ll;
     const PaSeq q = pa_seq<NH>(p, i, report);
     s = q.s;
-    return pa_head_length<NH>(p, q) * p.pg.H;
+    return (head = pa_head_length<NH>(p, q)) * p.pg.H;
   };
   // where the two cuts of piece c are on a line; false: there are not so many pieces
   long long cut[2];
@@ -230,9 +212,10 @@ __device__ __noinline__ void pa_find(const PaParams& p, PaPlace* pl, long long* 
     return there;
   };
   SeqInfo s;
+  long long head;
   if (p.c.n <= 32) {
     if (warp < 2) {
-      const long long x = length(lane, c == 0 && warp == 0, s), y = warp_scan(x);
+      const long long x = length(lane, c == 0 && warp == 0, s, head), y = warp_scan(x);
       const bool there = make_cuts(__shfl_sync(~0u, y, 31));
       const long long mine = warp == 0 ? cut[0] : cut[1];
       const bool here = there && mine >= y - x && mine < y;
@@ -241,25 +224,26 @@ __device__ __noinline__ void pa_find(const PaParams& p, PaPlace* pl, long long* 
       } else if (here) {
         pl[warp].i = lane;
         pl[warp].s = s;
+        pl[warp].head = head;
         pl[warp].rem = mine - (y - x);
       }
       __syncwarp();
     }
   } else {
     if (tid < 2) pl[tid].i = p.c.n, pl[tid].h = pl[tid].j = pl[tid].b = 0;
-    long long line, x = length(tid, c == 0, s), pre = scan(x, line);
+    long long line, x = length(tid, c == 0, s, head), pre = scan(x, line);
 #pragma unroll 1
     for (int base = NT; base < p.c.n; base += NT) {   // (more sequences than threads)
       long long tot;
       SeqInfo z;
-      scan(length(base + tid, c == 0, z), tot);
+      scan(length(base + tid, c == 0, z, head), tot);
       line += tot;
     }
     if (make_cuts(line)) {
       long long at = 0;
 #pragma unroll 1
       for (int base = 0; base < p.c.n; base += NT) {
-        if (base > 0) x = length(base + tid, false, s);
+        if (base > 0 || p.c.n > NT) x = length(base + tid, false, s, head);
         if (p.c.n > NT) {
           long long tot;
           pre = at + scan(x, tot);
@@ -270,6 +254,7 @@ __device__ __noinline__ void pa_find(const PaParams& p, PaPlace* pl, long long* 
           if (cut[k] >= pre && cut[k] < pre + x) {
             pl[k].i = base + tid;
             pl[k].s = s;
+            pl[k].head = head;
             pl[k].rem = cut[k] - pre;
           }
       }
@@ -280,19 +265,20 @@ __device__ __noinline__ void pa_find(const PaParams& p, PaPlace* pl, long long* 
     PaSeq q;
     q.s = pl[warp].s;
     q.tiles = (q.s.m + NH * p.T - 1) / (NH * p.T);
-    const long long head = pa_head_length<NH>(p, q);
     long long rem = pl[warp].rem;
-    const int h = (int)div_ll(rem, head);
-    rem -= h * head;
+    const int h = (int)div_ll(rem, pl[warp].head);
+    rem -= h * pl[warp].head;
     int lo = 0, hi = q.tiles;   // the last tile that begins at or before rem: 32 places a round
+    long long before = 0;
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32, cand = lo + lane * step;
-      const bool le = cand < hi && pa_before<NH>(p, q.s, cand) <= rem;
-      const int top = 31 - __clz(__ballot_sync(~0u, le));
+      const long long at = cand < hi ? pa_before<NH>(p, q.s, cand) : LLONG_MAX;
+      const int top = 31 - __clz(__ballot_sync(~0u, at <= rem));
+      before = __shfl_sync(~0u, at, top);
       lo += top * step;
       hi = min(hi, lo + step);
     }
-    rem -= pa_before<NH>(p, q.s, lo);
+    rem -= before;
     // a cut in what the tile costs besides, or in a short tile, is one before the tile
     const int b = pa_blocks<NH>(p, q.s, lo) <= PA_WHOLE ? 0 : max(0, (int)rem - PA_TILE_COST);
     if (lane == 0) {
