@@ -614,13 +614,15 @@ __global__ void __launch_bounds__(NT) pages_join_kernel(const __grid_constant__ 
   int c = blockIdx.x, end, rows;
   PaRec r;
   if constexpr (NT == 128) {   // piece x, if it is the first that starts inside of its tile
+    if (c == 0) return;
     r = p.rec[c];
-    if (r.begin < 0 || r.b == 0) return;
-    if (p.rec[c - 1].begin == r.begin && p.rec[c - 1].b > 0) return;
+    const long long last = p.rec[c - 1].begin, next = c + 1 < p.ctas ? p.rec[c + 1].begin : -1;   // (all loads at once)
+    const int last_b = p.rec[c - 1].b;
+    if (r.begin < 0 || r.b == 0 || (last == r.begin && last_b > 0)) return;
     rows = (min(r.ntok, (h + 1) * p.T) - h * p.T) * p.G;
     if (rows <= 0) return;
     end = c + 1;
-    for (int in = NT; in == NT && end < r.pieces; end += in) {
+    for (int in = NT; in == NT && next == r.begin && end < r.pieces; end += in) {
       const int q = end + threadIdx.x;
       in = __syncthreads_count(q < r.pieces && p.rec[q].begin == r.begin);
     }
