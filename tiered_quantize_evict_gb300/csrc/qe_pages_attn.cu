@@ -26,12 +26,14 @@
 //  * P is rounded to the pool's type (the tensor cores' operand): off by half a step at most, as the result itself is; the sum
 //    is of the unrounded ones.  With NH = 1, where the tensor cores wait for memory anyway, what the rounding leaves is kept as
 //    a second operand and multiplied too: error against 64 bits 1.45 -> 1.0 times that of the result's own rounding.
-// mbarriers: kfull / kempty per slot, qfull / qempty per query buffer, s[i] (S i complete; tensor-core commit),
-// p[i][0], p[i][1] (P i's first and last 32 of each 64 keys
-// written; one arrival per softmax warp: the products of the first start while the softmax is at the last, 32K chunk 705 -> 682 us), o[h] (half
-// h's O of a tile complete; with NH = 1 o[i]: the P V of an even or odd block complete.  An S tells only that the P V two blocks
-// before is, so one barrier's parity could mean the last P V or the one before), turn[h] (half h may issue).  Every wait is bounded (0.2 s); one that expires sets
-// QE_PAGES_ERR_TIMEOUT and an abort flag that ends all loops, and the CTA leaves after what it issued has landed.
+// mbarriers (every wait is bounded, 0.2 s; one that expires sets QE_PAGES_ERR_TIMEOUT and an abort flag that ends all loops, and the
+// CTA leaves after what it issued has landed):
+//  * kfull / kempty per slot, qfull / qempty per query buffer, s[i]: S i complete (tensor-core commit);
+//  * p[i][0], p[i][1]: P i's first and last 32 of each 64 keys written, one arrival per softmax warp (the products of the first start
+//    while the softmax is at the last: 32K chunk 705 -> 682 us);
+//  * o[h]: half h's O of a tile complete; with NH = 1 o[i]: the P V of an even or odd block complete (an S tells only that the P V two
+//    blocks before is, so one barrier's parity could mean the last P V or the one before);
+//  * turn[h]: half h may issue.
 #include <atomic>
 
 #include "qe_pages_attn.cuh"
