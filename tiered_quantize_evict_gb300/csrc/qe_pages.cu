@@ -476,6 +476,7 @@ template <bool FORK, bool ALL>
 __global__ void __launch_bounds__(PLAN_THREADS) pages_plan_kernel(const __grid_constant__ PagesView pg, const __grid_constant__ TableView t,
                                                                   const int* a, const int* b, int n,
                                                                   const __grid_constant__ PlanSpace ws) {
+  griddep_wait();
   griddep_launch_dependents();
   plan_moves<FORK>(pg, t, a, b, n, ws);
   if constexpr (ALL) {
@@ -499,11 +500,9 @@ static cudaError_t launch_planned(const PagesView& pg, const TableView& t, const
   const long long copied = !FORK && !b ? 0 : (long long)n * pg.L * 2 * pg.H * pg.S * pg.D * 2;
   // (one block: 4 rows of 19 pages forked and freed 12.8 us, with two launches each 14.4; 64 rows of 94 pages 50.8 against 48.2)
   if (copied <= 128 * 1024 && (long long)n * t.cols <= 2048) {
-    pages_plan_kernel<FORK, true><<<1, PLAN_THREADS, 0, st>>>(pg, t, a, b, n, s);
-    return cudaGetLastError();
+    return launch_after(pages_plan_kernel<FORK, true>, 1, PLAN_THREADS, st, pg, t, a, b, n, s);
   }
-  pages_plan_kernel<FORK, false><<<1, PLAN_THREADS, 0, st>>>(pg, t, a, b, n, s);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_after(pages_plan_kernel<FORK, false>, 1, PLAN_THREADS, st, pg, t, a, b, n, s);
   return e != cudaSuccess ? e : launch_after(pages_apply_kernel<FORK>, n_sm * 8, 256, st, pg, t, n, s);
 }
 cudaError_t launch_pages_resize(const PagesView& pg, const TableView& t, const int* rows, const int* new_len, int n, void* ws,
@@ -518,6 +517,7 @@ cudaError_t launch_pages_fork(const PagesView& pg, const TableView& t, const int
 // ---------------------------------------------------------------------------- compact
 __global__ void __launch_bounds__(PLAN_THREADS) pages_plan_compact_kernel(const PagesView pg, const TableView t, const PlanSpace ws,
                                                                           int* n_live_out) {
+  griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x;
   int live = 0;
@@ -585,24 +585,24 @@ cudaError_t launch_pages_compact(const PagesView& pg, const TableView& t, int* t
                                  int n_sm, cudaStream_t st) {
   PlanSpace s;
   plan_layout(ws, pg.P, t.rows, 0, &s);
-  pages_plan_compact_kernel<<<1, PLAN_THREADS, 0, st>>>(pg, t, s, n_live);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_after(pages_plan_compact_kernel, 1, PLAN_THREADS, st, pg, t, s, n_live);
   return e != cudaSuccess ? e : launch_after(pages_compact_kernel, n_sm * 8, 256, st, pg, t, s, table_out, refs_out);
 }
 
 // ---------------------------------------------------------------------------- copy, gather
 __global__ void __launch_bounds__(256) pages_copy_kernel(const PagesView pg, const int* src, const int* dst, int n) {
+  griddep_wait();
   copy_pairs(pg, nullptr, src, dst, n, blockIdx.x, gridDim.x);
 }
 cudaError_t launch_pages_copy(const PagesView& pg, const int* src, const int* dst, int n, int n_sm, cudaStream_t st) {
   const long long blocks = ((long long)n * pg.L * 2 * pg.H + 7) / 8;   // a warp per unit
-  pages_copy_kernel<<<(unsigned)(blocks < n_sm * 8 ? blocks : n_sm * 8), 256, 0, st>>>(pg, src, dst, n);
-  return cudaGetLastError();
+  return launch_after(pages_copy_kernel, (unsigned)(blocks < n_sm * 8 ? blocks : n_sm * 8), 256, st, pg, src, dst, n);
 }
 
 // a warp per head of one page's worth of tokens of one row, of the keys or the values
 __global__ void __launch_bounds__(256) pages_gather_kernel(const PagesView pg, const TableView t, int layer, const int* rows, int n,
                                                            int start, int n_tok, uint16_t* k, uint16_t* v) {
+  griddep_wait();
   const int first = start >> pg.lgS, np = ((start + n_tok - 1) >> pg.lgS) - first + 1, vpr = pg.D / 8, lane = threadIdx.x & 31;
   const long long units = (long long)n * np * 2 * pg.H;
   for (long long u = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += (long long)gridDim.x * 8) {
@@ -635,8 +635,7 @@ cudaError_t launch_pages_gather(const PagesView& pg, const TableView& t, int lay
                                 uint16_t* k, uint16_t* v, int n_sm, cudaStream_t st) {
   const int np = ((start + n_tok - 1) >> pg.lgS) - (start >> pg.lgS) + 1;
   const long long blocks = ((long long)n * np * 2 * pg.H + 7) / 8;
-  pages_gather_kernel<<<(unsigned)(blocks < n_sm * 8 ? blocks : n_sm * 8), 256, 0, st>>>(pg, t, layer, rows, n, start, n_tok, k, v);
-  return cudaGetLastError();
+  return launch_after(pages_gather_kernel, (unsigned)(blocks < n_sm * 8 ? blocks : n_sm * 8), 256, st, pg, t, layer, rows, n, start, n_tok, k, v);
 }
 
 }  // namespace qe
