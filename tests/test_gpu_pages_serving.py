@@ -121,3 +121,76 @@ def test_two_pools_and_a_side_stream(torch):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_captured_step_with_copies_between(torch):
+    """A whole step in one graph, every call right behind a copy of its inputs (not a kernel of ours), replayed with other inputs."""
+    import tiered_quantize_evict_gb300 as qe
+
+    def state():
+        k = torch.zeros(2, 24, 2, 16, 64, device="cuda", dtype=torch.bfloat16)
+        pool, seqs = qe.PagePool(k, torch.zeros_like(k)), qe.PageTable.empty(4, 8, 24, k.device)
+        ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        return {"pool": pool, "seqs": seqs, "rows": ints(0, 1), "lens": ints(0, 0), "starts": ints(0, 0, 0), "src": ints(0), "dst": ints(2),
+                "k": torch.zeros(9, 2, 64, device="cuda", dtype=torch.bfloat16), "v": torch.zeros(9, 2, 64, device="cuda", dtype=torch.bfloat16),
+                "q": torch.zeros(9, 4, 64, device="cuda", dtype=torch.bfloat16)}
+
+    rope = qe.Rope(64, halves=True)
+
+    def step(s, new):
+        pool, seqs = s["pool"], s["seqs"]
+        s["lens"].copy_(new["lens"])
+        pool.resize(seqs, s["rows"], s["lens"])
+        out = []
+        for layer in range(2):
+            s["starts"].copy_(new["starts"])
+            s["k"].copy_(new["k"])
+            s["v"].copy_(new["v"])
+            s["q"].copy_(new["q"])
+            q = pool.append(layer, s["k"], s["v"], s["starts"], seqs, rows=s["rows"], q=s["q"], rope=rope)
+            s["starts"].copy_(new["starts"])
+            out.append(pool.attend(layer, q, s["starts"], seqs, rows=s["rows"]))
+        s["src"].copy_(new["src"])
+        pool.fork(seqs, s["src"], s["dst"])
+        s["src"].copy_(new["src"])
+        out += pool.gather(1, seqs, 0, 40)
+        out += [seqs.table.clone(), seqs.refs.clone()]
+        pool.free(seqs, s["dst"])
+        s["src"].copy_(new["src"])
+        pool.compact(seqs)
+        return out
+
+    def inputs(seed, lens, starts, src):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rnd = lambda h: torch.randn(9, h, 64, device="cuda", generator=g).bfloat16()  # noqa: E731
+        ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        return {"lens": ints(lens), "starts": ints(starts), "src": ints(src), "k": rnd(2), "v": rnd(2), "q": rnd(4)}
+
+    steps = [inputs(1, [5, 4], [0, 5, 9], [1]), inputs(2, [6, 12], [0, 1, 9], [0]), inputs(3, [40, 13], [0, 8, 9], [1]), inputs(4, [3, 17], [0, 1, 5], [0])]
+    eager, replayed = state(), state()
+    step(eager, steps[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(replayed, steps[0])          # the same first step, outside of the graph
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    new = {n: x.clone() for n, x in steps[1].items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(replayed, new)
+    for x in steps[1:]:
+        for n in new:
+            new[n].copy_(x[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step(eager, x)
+        live = int(x["starts"][-1])       # packed tokens behind the last sequence are left alone
+        for a, b in zip(got[:2], want[:2]):
+            assert torch.equal(a[:live], b[:live])
+        for a, b in zip(got[2:], want[2:]):
+            assert torch.equal(a, b)
+        for a in ("k", "v"):
+            assert torch.equal(getattr(replayed["pool"], a), getattr(eager["pool"], a))
+    eager["pool"].check()
+    replayed["pool"].check()
