@@ -29,8 +29,8 @@
 // mbarriers (every wait is bounded, 0.2 s; one that expires sets QE_PAGES_ERR_TIMEOUT and an abort flag that ends all loops, and the
 // CTA leaves after what it issued has landed):
 //  * kfull / kempty per slot, qfull / qempty per query buffer, s[i]: S i complete (tensor-core commit);
-//  * p[i][0], p[i][1]: P i's first and last 32 of each 64 keys written, one arrival per softmax warp (the products of the first start
-//    while the softmax is at the last: 32K chunk 705 -> 682 us);
+//  * p[i][c]: part c of P i written (so many of each 64 keys), one arrival per softmax warp (the products of the first part start while
+//    the softmax is at the others: 32K chunk 705 -> 682 us with two parts);
 //  * o[h]: half h's O of a tile complete; with NH = 1 o[i]: the P V of an even or odd block complete (an S tells only that the P V two
 //    blocks before is, so one barrier's parity could mean the last P V or the one before);
 //  * turn[h]: half h may issue.
@@ -39,6 +39,11 @@
 #include "qe_pages_attn.cuh"
 
 namespace qe {
+
+// Parts that a block's probabilities are handed over in.  Four with two halves (512 tokens over 8K 54.5 -> 52.9 us against two, 32K chunk
+// 688 -> 683); with one half, where a part more is a wait more for two stores, 64-channel drafts take 105 us with four and 92 with two.
+template <int NH>
+constexpr int PA_PARTS = NH == 2 ? 4 : 2;
 
 // threads: 8 softmax warps per half, 4 more warps
 template <int NH>
@@ -121,10 +126,11 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
     pages_attend_kernel(const __grid_constant__ PaParams p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                         const __grid_constant__ CUtensorMap mv) {
   using Sh = PaShape<D>;
+  constexpr int PARTS = PA_PARTS<NH>;
   const int NS = NH == 1 && p.q_rows == 64 ? Sh::slots(64) : Sh::slots(128);
   const int q_cb = (NH == 1 ? p.q_rows : 128) * 128, q_buf = Sh::CB * q_cb;   // bytes of a query buffer's column block, and of the buffer
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) unsigned long long b_kfull[Sh::MOST], b_kempty[Sh::MOST], b_qfull[2], b_qempty[2], b_s[2], b_p[2][2], b_o[2], b_turn[2], b_end;
+  __shared__ __align__(8) unsigned long long b_kfull[Sh::MOST], b_kempty[Sh::MOST], b_qfull[2], b_qempty[2], b_s[2], b_p[2][PARTS], b_o[2], b_turn[2], b_end;
   __shared__ unsigned s_tmem;
   __shared__ int s_abort;
   __shared__ PaPlace s_place[2];
@@ -150,8 +156,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
       mbar_init(smem_u32(&b_qfull[i]), 1);
       mbar_init(smem_u32(&b_qempty[i]), 1);
       mbar_init(smem_u32(&b_s[i]), 1);
-      mbar_init(smem_u32(&b_p[i][0]), 8);
-      mbar_init(smem_u32(&b_p[i][1]), 8);
+      for (int c = 0; c < PARTS; ++c) mbar_init(smem_u32(&b_p[i][c]), 8);
       mbar_init(smem_u32(&b_o[i]), 1);
       mbar_init(smem_u32(&b_turn[i]), 1);
     }
@@ -250,19 +255,16 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
         pa_commit(smem_u32(&b_kempty[kslot]));
         if (q_done) pa_commit(smem_u32(&b_qempty[qb]));
       };
-      // O += P sb V over the first (part 0) or last 32 of each 64 keys (by one lane)
+      // O += P sb V over one part of each 64 keys (by one lane)
       auto pv = [&](int part, int sb, int vslot, bool acc) {
         const unsigned long long b = PA_DESC_V | ((sm_kv + vslot * Sh::TILE) >> 4);
+        constexpr int KS = 4 / PARTS;   // steps of 16 keys of a part of 64
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = (i >> 1) * 4 + part * 2 + (i & 1);   // 16 keys
-          pa_mma_ts(t_o, tm + sb * 128 + k * 8, b + k * 128, ID_O, acc || i > 0);
-        }
-        if (NH == 1)   // the remainders of P
+        for (int rest = 0; rest < (NH == 1 ? 2 : 1); ++rest)   // (with the remainders of P)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int k = (i >> 1) * 4 + part * 2 + (i & 1);
-            pa_mma_ts(t_o, tm + sb * 128 + 64 + k * 8, b + k * 128, ID_O, true);
+          for (int i = 0; i < 2 * KS; ++i) {
+            const int k = i / KS * 4 + part * KS + i % KS;
+            pa_mma_ts(t_o, tm + sb * 128 + rest * 64 + k * 8, b + k * 128, ID_O, acc || rest > 0 || i > 0);
           }
       };
 #pragma unroll 1
@@ -295,17 +297,20 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
           // to themselves they interleave, and both softmaxes and then both halves' products run at the same time.)
           ok = wait(smem_u32(&b_turn[h]), (n & 1) ^ h ^ 1);
           if (do_pv) {
-            ok = wait(smem_u32(&b_p[h][0]), pp) && ok;
-            pa_fence_after();
-            if (pa_elect()) pv(0, h, vslot, !was_first);
-            __syncwarp();
-            ok = wait(smem_u32(&b_p[h][1]), pp) && ok;
+#pragma unroll
+            for (int c = 0; c < PARTS - 1; ++c) {
+              ok = wait(smem_u32(&b_p[h][c]), pp) && ok;
+              pa_fence_after();
+              if (pa_elect()) pv(c, h, vslot, c > 0 || !was_first);
+              __syncwarp();
+            }
+            ok = wait(smem_u32(&b_p[h][PARTS - 1]), pp) && ok;
             pp ^= 1;
           }
           pa_fence_after();
           if (pa_elect()) {
             if (do_pv) {
-              pv(1, h, vslot, true);
+              pv(PARTS - 1, h, vslot, true);
               if (was_last) pa_commit(smem_u32(&b_o[h]));
               pa_commit(smem_u32(&b_kempty[vslot]));
             } else if (n > 0) {
@@ -338,14 +343,18 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
             ok = ok && wait(smem_u32(&b_kfull[vslot]), ph);
             ok = ok && wait(smem_u32(&b_p[sb][0]), pp >> sb & 1);
             if (!__all_sync(~0u, ok)) break;
-            pa_fence_after();
-            if (pa_elect()) pv(0, sb, vslot, !was_first);
-            __syncwarp();
-            ok = wait(smem_u32(&b_p[sb][1]), pp >> sb & 1);
+#pragma unroll
+            for (int c = 0; c < PARTS - 1; ++c) {
+              if (c > 0) ok = wait(smem_u32(&b_p[sb][c]), pp >> sb & 1) && ok;
+              pa_fence_after();
+              if (pa_elect()) pv(c, sb, vslot, c > 0 || !was_first);
+              __syncwarp();
+            }
+            ok = wait(smem_u32(&b_p[sb][PARTS - 1]), pp >> sb & 1) && ok;
             pp ^= 1 << sb;
             pa_fence_after();
             if (pa_elect()) {
-              pv(1, sb, vslot, true);
+              pv(PARTS - 1, sb, vslot, true);
               pa_commit(smem_u32(&b_kempty[vslot]));
               pa_commit(smem_u32(&b_o[sb]));
             }
@@ -498,12 +507,13 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
             const unsigned long long sc2 = f2_pack(p.scale2, p.scale2), ba2 = f2_pack(base, base);
             unsigned long long acc[2] = {0ull, 0ull};
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              unsigned pk[16], rest[16];
+            for (int c = 0; c < PARTS; ++c) {
+              constexpr int N = 32 / PARTS;   // pairs of keys
+              unsigned pk[N], rest[N];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
+              for (int e = 0; e < N; ++e) {
                 const unsigned long long x =
-                    f2_fma((unsigned long long)s[c * 32 + 2 * e] | ((unsigned long long)s[c * 32 + 2 * e + 1] << 32), sc2, ba2);
+                    f2_fma((unsigned long long)s[2 * (c * N + e)] | ((unsigned long long)s[2 * (c * N + e) + 1] << 32), sc2, ba2);
                 const float e0 = ex2(f2_lo(x)), e1 = ex2(f2_hi(x));
                 acc[e & 1] = f2_add(acc[e & 1], f2_pack(e0, e1));
                 pk[e] = pa_pack<FP16>(e0, e1);
@@ -513,24 +523,29 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
                   rest[e] = pa_pack<FP16>(f2_lo(d), f2_hi(d));
                 }
               }
-              pa_st16(t_s + ch * 32 + c * 16, pk);
-              if (NH == 1) pa_st16(t_s + 64 + ch * 32 + c * 16, rest);
-              if (c == 0) {   // the products of these may start
+              if constexpr (NH == 1) {
+                pa_st16(t_s + ch * 32 + c * N, pk);
+                pa_st16(t_s + 64 + ch * 32 + c * N, rest);
+              } else {
+                pa_st8(t_s + ch * 32 + c * N, pk);
+              }
+              if (c < PARTS - 1) {   // the products of these may start
                 pa_wait_st();
                 pa_fence_before();
                 __syncwarp();
-                if (lane == 0) pa_arrive(smem_u32(&b_p[sb][0]));
+                if (lane == 0) pa_arrive(smem_u32(&b_p[sb][c]));
               }
             }
             const unsigned long long a = f2_add(acc[0], acc[1]);
             sum += f2_lo(a) + f2_hi(a);
             pa_wait_st();
           } else {
-            if (lane == 0) pa_arrive(smem_u32(&b_p[sb][0]));
+            if (lane == 0)
+              for (int c = 0; c < PARTS - 1; ++c) pa_arrive(smem_u32(&b_p[sb][c]));
           }
           pa_fence_before();
           __syncwarp();
-          if (lane == 0) pa_arrive(smem_u32(&b_p[sb][1]));
+          if (lane == 0) pa_arrive(smem_u32(&b_p[sb][PARTS - 1]));
         }
 
         // ------------------------------ the tile's end in this piece
