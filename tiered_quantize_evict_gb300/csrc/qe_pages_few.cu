@@ -335,7 +335,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           for (int c = 0; c < N; ++c) {
             const float4 w = *reinterpret_cast<const float4*>(s_red[c]);
             const float top = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)) * p.scale2;
-            const float nb = top == -INFINITY ? 0.f : -top;   // (a row that sees none of these keys: any reference)
+            // (a row that sees none of these keys keeps its reference; of a first block, any)
+            const float nb = top == -INFINITY ? (k == 0 ? 0.f : base[c]) : -top;
             const float use = k == 0 ? nb : fminf(base[c], nb);
             f[c] = k == 0 ? 1.f : ex2(use - base[c]);
             base[c] = use;
