@@ -581,7 +581,8 @@ typedef struct {
 /* Attention of a chunk of new tokens over the cached pages of one layer:
  * out = softmax(scale q K^T + mask) V per query head, over the keys and values of its KV head.  A query that
  * sees no key gets zeros (and lse = -inf).  Inputs are finite and so are the logits in float32 (a value that is not may
- * also reach the chunk's tokens before it); what lies in the pages behind kv_len may be anything.  The probabilities meet the values rounded to the pool's type, all sums are float32.
+ * also reach the chunk's tokens before it); what lies in the pages behind kv_len may be anything.  The probabilities meet the values rounded to the pool's type
+ * (fp16: a key's weight, relative to the row's largest, is off by 2^-32 at most where its half step is less), all sums are float32.
  * Deterministic for the same lengths.  n_seqs up to 65536. */
 qe_status qe_pages_attend(const qe_pages* pages, int layer, const qe_page_table* seqs, const qe_chunks* chunks,
                           const qe_pages_attend_args* args, void* workspace, size_t bytes, void* stream);

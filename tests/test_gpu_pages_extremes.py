@@ -48,3 +48,71 @@ def test_rows_without_keys_of_the_last_block(torch, d, dtype, blocks, m, hint, h
     err, off = np.abs(bits(out)[:m] - ref), np.abs(lse.cpu().numpy()[:m] - lref)
     assert (off <= ltol).all(), f"lse: {lse.cpu().numpy()[:m]} and {lref}"
     assert (err <= tol).all(), f"off by {err.max():.3e}"
+
+
+# The kernels by their tiles: (chunk, hint, query heads) of one KV head
+KERNELS = {"few": (2, 2, 2), "one_half": (20, 20, 1), "two_halves": (140, 0, 2)}
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [500, 512, 4000])
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("causal", [True, False])
+def test_small_weights_of_fp16(torch, d, n, kernel, causal):
+    """Weights of 2^-24.5 to 2^-29 beside one of 1 whose value is zero: all of the result comes from them.
+
+    Probabilities meet the values in fp16, 2^7 times as large as the weights or more, so where they are below 2^-14 they are off by at
+    most half a step of 2^-24: a weight by 2^-25 / 2^7 = 2^-32, absolutely.  A probability above is off by half a step relatively (u), as
+    in attend_bounds, whose other terms stay."""
+    import tiered_quantize_evict_gb300 as qe
+    m, hint, hq = KERNELS[kernel]
+    c = Case(torch, [n], hkv=1, d=d, ps=32, dtype="fp16", seed=n + d)
+    k, v = torch.zeros(n, 1, d, dtype=c.dt), torch.from_numpy(c.rng.uniform(500, 2000, (n, 1, d))).to(c.dt)
+    k[1:, 0, 0] = torch.from_numpy(c.rng.uniform(-29, -24.5, n - 1) * np.log(2)).to(c.dt)
+    v[0] = 0
+    c.kh[0][0].copy_(k)
+    c.vh[0][0].copy_(v)
+    put_keys(torch, c, 0)
+    pool, seqs = c.objects(qe)
+    q = torch.zeros(m, hq, d, dtype=c.dt)
+    q[:, :, 0] = 1.0
+    out = pool.attend(0, q.to(c.dev), c.ints([0, m]), seqs, scale=1.0, causal=causal, max_q_len=hint)
+    pool.check()
+    ref, tol, _, _ = attend_bounds(torch, c, bits(q), m, 0, hq, 1.0, causal)
+    from oracle import pages as op
+    den = op.attend(bits(q), bits(k), bits(v), 1, 1.0, causal)[3]
+    tol -= 1.01 * (2.0 ** -25 - 2.0 ** -32) * np.abs(bits(v)).sum(0)[None] / den[..., None]   # (attend_bounds' share of probabilities below 2^-14)
+    assert (tol > 0).all() and (tol < 0.05 * ref).all()
+    err = np.abs(bits(out) - ref)
+    assert (err <= tol).all(), f"off by {(err / ref).max():.3e} of the result, {(err / tol).max():.1f} of the bound"
+
+
+@pytest.mark.parametrize("kernel", ["few", "one_half", "two_halves"])
+def test_small_weights_of_fp16_in_a_long_cache(torch, kernel):
+    """131071 keys of a weight near 2^-25.5 under one of 1, walked by single CTAs (more tiles than SMs; their rows share the pages).
+
+    Beside the roundings of the result and of the probabilities (u each) and 2^-32 of each weight: sums of 1024 blocks, a term of each
+    added in float32 (2^-24 of the sum each, and 64 terms within a block), and products accumulated over 8192 steps of 16 keys (2^-23 of
+    the sum of their sizes each, were every step cut off)."""
+    import tiered_quantize_evict_gb300 as qe
+    n, ps, d, dt, dev = 131072, 256, 64, torch.float16, torch.device("cuda:0")
+    rng = np.random.default_rng(3)
+    k, v = torch.zeros(1, n // ps, 1, ps, d, dtype=dt), torch.from_numpy(64 + rng.uniform(-4, 4, (1, n // ps, 1, ps, d))).to(dt)
+    k[..., 0] = float(torch.tensor(-25.5 * np.log(2)).to(dt))
+    k[0, 0, 0, 0], v[0, 0, 0, 0] = 0, 1
+    seqs_n, m, hint = {"few": (400, 1, 1), "one_half": (400, 20, 20), "two_halves": (1, 80000, 0)}[kernel]
+    ints = lambda x: torch.tensor(np.asarray(x, np.int32)).to(dev)  # noqa: E731
+    pool = qe.PagePool(k.to(dev), v.to(dev))
+    seqs = qe.PageTable(ints(np.tile(np.arange(n // ps), (seqs_n, 1))), ints([n] * seqs_n))
+    q = torch.zeros(seqs_n * m, 1, d, dtype=dt, device=dev)
+    q[..., 0] = 1
+    out = pool.attend(0, q, ints(np.arange(seqs_n + 1) * m), seqs, scale=1.0, causal=False, max_q_len=hint)
+    pool.check()
+    logit = bits(k)[0, :, 0, :, 0].reshape(-1)
+    w = np.exp(logit)
+    vv = bits(v)[0, :, 0].reshape(-1, d)
+    ref, u = w @ vv / w.sum(), 2.0 ** -11
+    dl = (d + 4) * 2.0 ** -24 * np.abs(logit).max()
+    tol = u * ref + (u + 2 * dl + (1024 + 64) * 2.0 ** -24 + 8192 * 2.0 ** -23) * ref + 2.0 ** -32 * vv.sum(0) / w.sum() + 2.0 ** -20
+    err = (out.double().cpu() - torch.from_numpy(ref)).abs().amax((0, 1)).numpy()
+    assert (err <= tol).all(), f"off by {err.max():.3e} of {ref.max():.3f}, {(err / tol).max():.1f} of the bound"

@@ -23,8 +23,9 @@
 //    MN-major operand (its rows are tokens).
 //  * The reference M is raised only when a row's maximum passes it by 2^8 (then the softmax warps rescale O in tensor
 //    memory); up to that P and the sums are larger than 1, exactly as precise.
-//  * P is rounded to the pool's type (the tensor cores' operand): off by half a step at most, as the result itself is; the sum
-//    is of the unrounded ones.  With NH = 1, where the tensor cores wait for memory anyway, what the rounding leaves is kept as
+//  * P is rounded to the pool's type (the tensor cores' operand): off by half a step at most, as the result itself is, but for fp16 by
+//    2^-32 of the reference's weight where that is more (P is taken 2^7 times as large, or it would be 2^-25); the sum is of the
+//    unrounded ones.  With NH = 1, where the tensor cores wait for memory anyway, what the rounding leaves is kept as
 //    a second operand and multiplied too: error against 64 bits 1.45 -> 1.0 times that of the result's own rounding.
 // mbarriers (every wait is bounded, 0.2 s; one that expires sets QE_PAGES_ERR_TIMEOUT and an abort flag that ends all loops, and the
 // CTA leaves after what it issued has landed):
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
                 pa_pair_sync(pair);   // O is scaled whole before either half of the keys is handed over
               }
             }
-            const float base = ref == -INFINITY ? 0.f : -ref * p.scale2;
+            const float base = PA_UP<FP16> - (ref == -INFINITY ? 0.f : ref * p.scale2);
             const unsigned long long sc2 = f2_pack(p.scale2, p.scale2), ba2 = f2_pack(base, base);
             unsigned long long acc[2] = {0ull, 0ull};
 #pragma unroll
@@ -600,8 +601,8 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
                   *reinterpret_cast<uint4*>(po + (c / 4 + e) * 512) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             }
           }
-          if (live && whole && p.lse && ch == 0) p.lse[(long long)tok * p.Hq + head] = sum == 0.f ? -INFINITY : ref * p.scale + logf(sum);
-          if (live && !whole && ch == 0) p.part_ml[part * 128 + r] = make_float2(sum == 0.f ? -INFINITY : ref * p.scale2, sum);
+          if (live && whole && p.lse && ch == 0) p.lse[(long long)tok * p.Hq + head] = sum == 0.f ? -INFINITY : ref * p.scale + logf(sum * PA_DOWN<FP16>);
+          if (live && !whole && ch == 0) p.part_ml[part * 128 + r] = make_float2(sum == 0.f ? -INFINITY : ref * p.scale2 - PA_UP<FP16>, sum);
           pa_fence_before();
           pa_pair_sync(pair);   // O is read whole before the next tile's first P is handed over
         }
@@ -748,7 +749,7 @@ __global__ void __launch_bounds__(NT) pages_join_kernel(const __grid_constant__ 
   if constexpr (CH == 16) pa_store32(dst, x);
   else if constexpr (CH == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
   else *reinterpret_cast<uint2*>(dst) = make_uint2(x[0], x[1]);
-  if (p.lse && ch == 0) p.lse[tok * p.Hq + head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+  if (p.lse && ch == 0) p.lse[tok * p.Hq + head] = sum == 0.f ? -INFINITY : (m + PA_UP<FP16> + log2f(sum * PA_DOWN<FP16>)) * 0.69314718055994531f;
 }
 
 // ---------------------------------------------------------------------------- launch

@@ -18,6 +18,12 @@ constexpr int PA_BN = 128;                       // keys of a block
 constexpr int PA_MAX_CTAS = 1024;
 constexpr unsigned long long PA_WAIT_NS = 200000000ull;
 constexpr float PA_LAZY = 8.f;                   // log2 of how far a row's maximum may pass its reference
+// log2 of what probabilities and sums are multiplied by: an fp16 probability below 2^-14 is subnormal, off by up to 2^-25 and zero from there
+// down.  7 above the weight, and PA_LAZY more at most, they stay within fp16's 2^16, and a weight is off by 2^-32 at most.
+template <bool FP16>
+constexpr float PA_UP = FP16 ? 7.f : 0.f;
+template <bool FP16>
+constexpr float PA_DOWN = FP16 ? 0x1p-7f : 1.f;  // 2^-PA_UP
 
 // what a CTA's piece of the line starts with (read by the join kernel)
 struct PaRec {

@@ -285,7 +285,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     for (int cnt; (cnt = cur.count()) > 0; cur.next_tile(p)) {
       const int off = cur.q.s.len - cur.q.s.m + cur.j * p.T;        // the tile's first token sees the keys [0, off]
       const int every = p.causal ? off + 1 : cur.q.s.len;           // keys that all rows see
-      float base[N], sum[N];                                        // -reference (log2 units), and this key's part of the sum
+      constexpr float UP = PA_UP<FP16>;
+      float base[N], sum[N];                                        // UP - reference (log2 units), and this key's part of the sum
 #pragma unroll
       for (int c = 0; c < N; ++c) sum[c] = 0.f;
 #pragma unroll 1
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         bool over = false;
         if (k > 0) {
 #pragma unroll
-          for (int c = 0; c < N; ++c) over |= fmaf(__uint_as_float(s[c]), p.scale2, base[c]) > PA_LAZY;
+          for (int c = 0; c < N; ++c) over |= fmaf(__uint_as_float(s[c]), p.scale2, base[c]) > PA_LAZY + UP;
         }
         if (__builtin_expect(k == 0 || pf_or(over), 0)) {
           float m[N], f[N];
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             const float4 w = *reinterpret_cast<const float4*>(s_red[c]);
             const float top = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)) * p.scale2;
             // (a row that sees none of these keys keeps its reference; of a first block, any)
-            const float nb = top == -INFINITY ? (k == 0 ? 0.f : base[c]) : -top;
+            const float nb = top == -INFINITY ? (k == 0 ? UP : base[c]) : UP - top;
             const float use = k == 0 ? nb : fminf(base[c], nb);
             f[c] = k == 0 ? 1.f : ex2(use - base[c]);
             base[c] = use;
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       const long long part = (long long)blockIdx.x * 2 + (cur.b == 0 ? 1 : 0);
       if (kl < rows) {   // a thread per row
         const int row = kl;
-        float ref = 0.f;
+        float ref = 0.f;   // (of the sums: UP below the reference)
 #pragma unroll
         for (int c = 0; c < N; ++c)
           if (c == kl) ref = -base[c];
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         } else if (p.lse) {
           const int t = row / p.G;
           p.lse[(long long)(cur.q.s.q0 + cur.j * p.T + t) * p.Hq + cur.h * p.G + (row - t * p.G)] =
-              all == 0.f ? -INFINITY : (ref + log2f(all)) * 0.69314718055994531f;
+              all == 0.f ? -INFINITY : (ref + UP + log2f(all * PA_DOWN<FP16>)) * 0.69314718055994531f;
         }
       }
       pf_sync();
