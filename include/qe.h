@@ -377,7 +377,7 @@ long long qe_kernel_launches(qe_handle h);
  *
  * Not part of the method on the pages (H2O page §5.1 asks for failure canaries and a fallback;
  * this is how the library's failure paths are exercised).  Every injection acts on the host or
- * on a wait whose data has already arrived: none faults, traps or hangs a GPU.
+ * on a wait whose data has already arrived or is then waited for: none faults, traps or hangs a GPU.
  *  QE_DEBUG_FAIL_DEVICE_ALLOC (h unused, may be NULL; process-wide): value n >= 1 makes the n-th
  *    device allocation of the next qe_init fail as out of memory: qe_init frees what it had
  *    allocated and returns QE_ERR_OOM naming the buffer.  0 clears.  One-shot.
@@ -394,10 +394,16 @@ long long qe_kernel_launches(qe_handle h);
  *    be faster), 1 the fused launch whenever it is allowed (keys used as stored, n_q *
  *    group <= 64), 2 draft by draft.  Both paths compute the same results up to float32
  *    summation order; this lets tests cover each.  Not a fault: it persists until changed.
+ *  QE_DEBUG_EXPIRE_PAGES_WAIT (h unused; process-wide): value 4 k + role, k >= 1: in the next
+ *    qe_pages_attend that has work, every CTA whose warp of that role (0: copies of keys and values, 1: products,
+ *    2: copies of queries) makes at least k waits of one kind (a slot of the ring, keys, a
+ *    query buffer) takes the k-th as expired without waiting, as a real expiry would end it: copies and products that were
+ *    issued are waited for, the CTA leaves, QE_PAGES_ERR_TIMEOUT is set and the call's outputs are
+ *    undefined.  0 clears.  One-shot.
  * Errors: QE_ERR_INVALID_ARG (unknown kind, negative value, NULL handle for the wait or the
- * verify path, a path outside 0..2). */
+ * verify path, a path outside 0..2, a role outside 0..2 or k = 0). */
 enum { QE_DEBUG_FAIL_DEVICE_ALLOC = 1, QE_DEBUG_FAIL_HOST_STORE = 2, QE_DEBUG_EXPIRE_WAIT = 3,
-       QE_DEBUG_VERIFY_PATH = 4 };
+       QE_DEBUG_VERIFY_PATH = 4, QE_DEBUG_EXPIRE_PAGES_WAIT = 5 };
 qe_status qe_debug_inject(qe_handle h, int what, long long value);
 
 /* ---------------------------------------------------------------- snapshots (session restore)

@@ -34,6 +34,7 @@ thread_local std::string g_init_error;
 std::atomic<int> g_fail_alloc_nth{0};
 std::atomic<int> g_alloc_count{0};
 std::atomic<int> g_fail_host_store{0};
+std::atomic<int> g_pages_expire{0};   // the next qe_pages_attend's expiring wait
 std::atomic<int> g_fired{0};   // an injected allocation failure has fired and is not yet reported
 
 }  // namespace
@@ -49,6 +50,7 @@ bool inject_alloc_failure() {
   return true;
 }
 void set_global_error(const char* msg) { g_init_error = msg; }
+int take_pages_expire() { return g_pages_expire.load(std::memory_order_relaxed) ? g_pages_expire.exchange(0) : 0; }
 const char* injected_note() { return g_fired.exchange(0) ? " (injected by qe_debug_inject)" : ""; }
 }  // namespace qe
 
@@ -1047,6 +1049,10 @@ qe_status qe_debug_inject(qe_handle h, int what, long long value) {
       return QE_OK;
     case QE_DEBUG_FAIL_HOST_STORE:
       g_fail_host_store.store(value != 0 ? 1 : 0);
+      return QE_OK;
+    case QE_DEBUG_EXPIRE_PAGES_WAIT:
+      if (value < 0 || value > (1 << 30) || (value & 3) == 3 || (value && value < 4)) return QE_ERR_INVALID_ARG;
+      g_pages_expire.store((int)value);
       return QE_OK;
     case QE_DEBUG_EXPIRE_WAIT:
       if (!h) return QE_ERR_INVALID_ARG;

@@ -54,6 +54,7 @@ struct PagesAttendParams {
   float* lse;
   long long qts, qhs, ots, ohs;
   int layer, Hq, causal, max_q_len;
+  int expire;                 // qe_debug_inject (qe_pages_attn.cuh); 0: none
   float scale;
 };
 
@@ -85,6 +86,8 @@ size_t pages_manage_bytes(int n_pages, int n_rows, int n);
 
 // qe_host.cu: the message behind qe_last_error(NULL)
 void set_global_error(const char* msg);
+// qe_host.cu: the injected expiry of the next attention, once
+int take_pages_expire();
 
 #if defined(__CUDACC__)
 __device__ __forceinline__ void pages_report(const PagesView& pg, unsigned bit) {

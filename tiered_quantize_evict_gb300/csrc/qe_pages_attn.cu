@@ -28,7 +28,7 @@
 //    unrounded ones.  With NH = 1, where the tensor cores wait for memory anyway, what the rounding leaves is kept as
 //    a second operand and multiplied too: error against 64 bits 1.45 -> 1.0 times that of the result's own rounding.
 // mbarriers (every wait is bounded, 0.2 s; one that expires sets QE_PAGES_ERR_TIMEOUT and an abort flag that ends all loops, and the
-// CTA leaves after what it issued has landed):
+// CTA leaves after what it issued has landed: each warp that issues waits for its own last, whether it or another warp gave up):
 //  * kfull / kempty per slot, qfull / qempty per query buffer, s[i]: S i complete (tensor-core commit);
 //  * p[i][c]: part c of P i written (so many of each 64 keys), one arrival per softmax warp (the products of the first part start while
 //    the softmax is at the others: 32K chunk 705 -> 682 us with two parts);
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
         return key < cur.q.s.len ? p.t.table[(long long)cur.q.s.row * p.t.stride + (key >> p.pg.lgS)] : INT_MIN;
       };
       int slot = 0, ph = 1, issued = 0, left = cur.count();
-      int next = entry();
+      int next = entry(), till = PaWait::counted(p, PaWait::KEYS);
       bool ok = true;
 #pragma unroll 1
       while (left > 0 && ok) {
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
         if (left > 0) next = entry();
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
-          ok = ok && wait(smem_u32(&b_kempty[slot]), ph);
+          ok = ok && wait(smem_u32(&b_kempty[slot]), ph, till);
           if (!__all_sync(~0u, ok)) {
             ok = false;
             break;
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
           }
         }
       }
-      if (!ok && lane == 0)   // leaving early: the copies in flight land first
+      if (lane == 0)   // the copies land before the CTA leaves (early, it may be, and for another warp's wait)
         for (int i = max(0, issued - NS); i < issued; ++i) wait.drain(smem_u32(&b_kfull[i % NS]), (i / NS) & 1);
     } else if (work && aux - 1 < NH) {
       // ============================== tensor cores: a warp per half, so that the waits and the issue of one half pass while
@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
       cur.set(p, s_place);
       // The ring is consumed in its order: K 0, then V n - 1 and K n in turn.
       int slot = 0, ph = 0, pp = 0, qp = 0, tile = 0, left = 0;   // (bit i of pp, qp: the parity of p[i], qfull[i])
+      int till = PaWait::counted(p, PaWait::PRODUCTS);
       bool was_first = false, was_last = false, was_mine = false, mine = false, ok = true, more = true;
       auto step = [&]() {
         if (++slot == NS) {
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
             step();
           }
           if (more) {
-            ok = ok && wait(smem_u32(&b_kfull[slot]), ph);
+            ok = ok && wait(smem_u32(&b_kfull[slot]), ph, till);
             if (first && mine) {
               ok = ok && wait(smem_u32(&b_qfull[h]), qp & 1);
               qp ^= 1;
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
               ok = ok && wait(smem_u32(&b_qfull[qb]), qp >> qb & 1);
               qp ^= 1 << qb;
             }
-            ok = ok && wait(smem_u32(&b_kfull[kslot]), kph);
+            ok = ok && wait(smem_u32(&b_kfull[kslot]), kph, till);
             if (!__all_sync(~0u, ok)) break;
             pa_fence_after();
             if (pa_elect()) qk(qb, n & 1, kslot, last);
@@ -377,28 +378,27 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
       if (lane == 0) {
         PaCursor<NH> cur;
         cur.set(p, s_place);
-        int ph[2] = {1, 1}, tile = 0;
-        bool sent[2] = {false, false}, ok = true;
+        PaFill fill[2];
+        int tile = 0, till = PaWait::counted(p, PaWait::QUERIES);
+        bool ok = true;
 #pragma unroll 1
         for (; ok && cur.count() > 0; cur.next_tile(p)) {
           const int halves = cur.second_half(p) ? 2 : 1;
 #pragma unroll 1
           for (int h = 0; h < halves; ++h) {
             const int qb = NH == 2 ? h : tile & 1;
-            ok = wait(smem_u32(&b_qempty[qb]), ph[qb]);
-            ph[qb] ^= 1;
+            ok = wait(smem_u32(&b_qempty[qb]), fill[qb].empty(), till);
             if (!ok) break;
             const unsigned full = smem_u32(&b_qfull[qb]);
             mbar_expect_tx(full, p.T * p.G * 128 * Sh::CB);
             for (int cb = 0; cb < Sh::CB; ++cb)
               pa_tma3(sm_q + qb * q_buf + cb * q_cb, &mq, cb * 64, cur.h * p.G, cur.q.s.q0 + (cur.j * NH + h) * p.T, full);
-            sent[qb] = true;
+            ++fill[qb].sent;
           }
           ++tile;
         }
-        if (!ok)
-          for (int qb = 0; qb < 2; ++qb)
-            if (sent[qb]) wait.drain(smem_u32(&b_qfull[qb]), ph[qb]);
+        for (int qb = 0; qb < 2; ++qb)
+          if (fill[qb].sent > 0) wait.drain(smem_u32(&b_qfull[qb]), fill[qb].landed());
       }
     }
   } else {
@@ -845,6 +845,7 @@ cudaError_t launch_pages_attend(const PagesAttendParams& a, int fp16, int device
   p.causal = a.causal;
   p.ctas = n_sm < PA_MAX_CTAS ? n_sm : PA_MAX_CTAS;
   p.scale = a.scale;
+  p.expire = a.expire;
   p.scale2 = a.scale * 1.44269504088896341f;
   // One half where the longest chunk's rows fit it (bound by reading the cache), else two.  The tile takes no more
   // tokens than the longest chunk, so that its query copy does not read the next sequences' rows.

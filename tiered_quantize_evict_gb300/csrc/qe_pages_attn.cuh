@@ -11,6 +11,7 @@
 
 #include "qe_common.cuh"
 #include "qe_pages.cuh"
+#include "qe_pages_fill.cuh"
 
 namespace qe {
 
@@ -44,6 +45,7 @@ struct PaParams {
   int Hq, G, T, causal;
   int q_rows;              // rows of a query buffer
   int ctas;                // CTAs of the attention kernel: one per SM
+  int expire;              // qe_debug_inject: 4 k + role, the k-th counted wait of these warps is taken as expired; 0: none
   float scale, scale2;     // of the logits; and times log2(e)
   PaRec* rec;              // [CTAs]; NULL: no tile is cut
   float2* part_ml;         // [CTAs][2][NH][128]: reference, sum
@@ -408,6 +410,15 @@ struct PaWait {
       }
     }
     return true;
+  }
+  // The warps whose waits a test may take as expired, one wait per block or tile: those that send keys and values, issue products, send queries.
+  enum Role { KEYS, PRODUCTS, QUERIES };
+  static __device__ __forceinline__ int counted(const PaParams& p, Role role) { return (p.expire & 3) == role ? p.expire >> 2 : 0; }
+  __device__ __forceinline__ bool operator()(unsigned bar, unsigned parity, int& left) const {
+    if (--left != 0) return (*this)(bar, parity);
+    pages_report(*pg, QE_PAGES_ERR_TIMEOUT);
+    *abort = 1;
+    return false;
   }
   // the same on the way out, for what has been issued
   __device__ __forceinline__ void drain(unsigned bar, unsigned parity) const {

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       return key < cur.q.s.len ? p.t.table[(long long)cur.q.s.row * p.t.stride + (key >> p.pg.lgS)] : INT_MIN;
     };
     int slot = 0, ph = 1, issued = 0, left = cur.count();
-    int next = entry();
+    int next = entry(), till = PaWait::counted(p, PaWait::KEYS);
     bool ok = true;
 #pragma unroll 1
     while (left > 0 && ok) {
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       if (left > 0) next = entry();
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
-        ok = ok && wait(smem_u32(&b_kempty[slot]), ph);
+        ok = ok && wait(smem_u32(&b_kempty[slot]), ph, till);
         if (!__all_sync(~0u, ok)) {
           ok = false;
           break;
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         }
       }
     }
-    if (!ok && lane == 0)   // leaving early: the copies in flight land first
+    if (lane == 0)   // the copies land before the CTA leaves (early, it may be, and for another warp's wait)
       for (int i = max(0, issued - NS); i < issued; ++i) wait.drain(smem_u32(&b_kfull[i % NS]), (i / NS) & 1);
   } else if (work && aux == 1) {
     // ============================== tensor cores (the whole warp walks the loop, one lane issues)
@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     cur.set(p, s_place);
     // The ring is consumed in its order (K 0, V 0, K 1, ...), but S runs a block ahead: K n is used before V n - 1.
     int slot = 0, ph = 0, pp = 0, qp = 0, tile = 0, left = 0;   // (bit i of pp, qp: the parity of p[i], qfull[i])
+    int till = PaWait::counted(p, PaWait::PRODUCTS);
     bool was_first = false, ok = true, more = true;
     auto step = [&]() {
       if (++slot == NS) {
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           ok = ok && wait(smem_u32(&b_qfull[qb]), qp >> qb & 1);
           qp ^= 1 << qb;
         }
-        ok = ok && wait(smem_u32(&b_kfull[kslot]), kph);
+        ok = ok && wait(smem_u32(&b_kfull[kslot]), kph, till);
         if (!__all_sync(~0u, ok)) break;
         pa_fence_after();
         if (pa_elect()) {   // S n = K Q^T
@@ -251,24 +252,21 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     if (lane == 0) {
       PaCursor<1> cur;
       cur.set(p, s_place);
-      int ph[2] = {1, 1}, tile = 0;
-      bool sent[2] = {false, false}, ok = true;
+      PaFill fill[2];
+      int tile = 0, till = PaWait::counted(p, PaWait::QUERIES);
 #pragma unroll 1
-      for (; ok && cur.count() > 0; cur.next_tile(p)) {
+      for (; cur.count() > 0; cur.next_tile(p)) {
         const int qb = tile & 1;
-        ok = wait(smem_u32(&b_qempty[qb]), ph[qb]);
-        ph[qb] ^= 1;
-        if (!ok) break;
+        if (!wait(smem_u32(&b_qempty[qb]), fill[qb].empty(), till)) break;
         const unsigned full = smem_u32(&b_qfull[qb]);
         mbar_expect_tx(full, p.T * p.G * 128 * Sh::CB);
         for (int cb = 0; cb < Sh::CB; ++cb)
           pa_tma3(sm_q + qb * Sh::Q_BUF + cb * Sh::Q_CB, &mq, cb * 64, cur.h * p.G, cur.q.s.q0 + cur.j * p.T, full);
-        sent[qb] = true;
+        ++fill[qb].sent;
         ++tile;
       }
-      if (!ok)
-        for (int qb = 0; qb < 2; ++qb)
-          if (sent[qb]) wait.drain(smem_u32(&b_qfull[qb]), ph[qb]);
+      for (int qb = 0; qb < 2; ++qb)
+        if (fill[qb].sent > 0) wait.drain(smem_u32(&b_qfull[qb]), fill[qb].landed());
     }
   } else if (work && aux < 0) {
     // ============================== softmax: a key of every block, all rows

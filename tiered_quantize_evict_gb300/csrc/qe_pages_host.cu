@@ -255,6 +255,7 @@ qe_status qe_pages_attend(const qe_pages* pages, int layer, const qe_page_table*
   p.causal = a->causal != 0;
   p.max_q_len = a->max_q_len;
   p.scale = a->scale;
+  p.expire = qe::take_pages_expire();
   DeviceGuard guard(pages->device);
   if (guard.err != cudaSuccess) return cuda_fail(guard.err, "cudaSetDevice");
   return launched(qe::launch_pages_attend(p, pages->dtype == QE_DTYPE_FP16, pages->device, n_sm, workspace, static_cast<cudaStream_t>(stream)),
