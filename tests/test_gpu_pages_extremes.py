@@ -116,3 +116,20 @@ def test_small_weights_of_fp16_in_a_long_cache(torch, kernel):
     tol = u * ref + (u + 2 * dl + (1024 + 64) * 2.0 ** -24 + 8192 * 2.0 ** -23) * ref + 2.0 ** -32 * vv.sum(0) / w.sum() + 2.0 ** -20
     err = (out.double().cpu() - torch.from_numpy(ref)).abs().amax((0, 1)).numpy()
     assert (err <= tol).all(), f"off by {err.max():.3e} of {ref.max():.3f}, {(err / tol).max():.1f} of the bound"
+
+
+@pytest.mark.parametrize("m,hint", [((77824,), 0), ((1, 200) * 152, 0), ((1,) * 456, 1), ((20,) * 456, 20)],
+                         ids=["two_halves", "one_or_two_halves", "few", "one_half"])
+def test_tiles_of_a_third_of_a_second(torch, m, hint):
+    """2^25 keys (one page, named over and over), so that a CTA walks its second or third tile more than 0.2 s after its first: no wait expires.
+    Logits are 0 and values powers of two, so all sums are whole numbers of them that float32 holds: the result is the values."""
+    import tiered_quantize_evict_gb300 as qe
+    n, ps, d, dev = 2 ** 25, 256, 128, torch.device("cuda:0")
+    ints = lambda x: torch.tensor(np.asarray(x, np.int32)).to(dev)  # noqa: E731
+    v = 2.0 ** (torch.arange(d) % 8 - 4).to(torch.bfloat16)
+    pool = qe.PagePool(torch.randn(1, 1, 1, ps, d).to(torch.bfloat16).to(dev), v.expand(1, 1, 1, ps, d).contiguous().to(dev))
+    seqs = qe.PageTable(torch.zeros(1, n // ps, dtype=torch.int32, device=dev), ints([n]))
+    q = torch.zeros(sum(m), 1, d, dtype=torch.bfloat16, device=dev)
+    out = pool.attend(0, q, ints(np.cumsum([0, *m])), seqs, rows=ints([0] * len(m)), causal=False, max_q_len=hint)
+    pool.check()
+    assert torch.equal(out[:, 0], v.to(dev).expand(sum(m), d))

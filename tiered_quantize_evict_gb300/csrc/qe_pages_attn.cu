@@ -27,8 +27,9 @@
 //    2^-32 of the reference's weight where that is more (P is taken 2^7 times as large, or it would be 2^-25); the sum is of the
 //    unrounded ones.  With NH = 1, where the tensor cores wait for memory anyway, what the rounding leaves is kept as
 //    a second operand and multiplied too: error against 64 bits 1.45 -> 1.0 times that of the result's own rounding.
-// mbarriers (every wait is bounded, 0.2 s; one that expires sets QE_PAGES_ERR_TIMEOUT and an abort flag that ends all loops, and the
-// CTA leaves after what it issued has landed: each warp that issues waits for its own last, whether it or another warp gave up):
+// mbarriers.  Every wait is bounded, by 0.2 s and 10 us for each block that it may sit out; one that expires sets QE_PAGES_ERR_TIMEOUT
+// and an abort flag that ends all loops, and the CTA leaves after what it issued has landed: each warp that issues waits for its own
+// last, whether it or another warp gave up.
 //  * kfull / kempty per slot, qfull / qempty per query buffer, s[i]: S i complete (tensor-core commit);
 //  * p[i][c]: part c of P i written (so many of each 64 keys), one arrival per softmax warp (the products of the first part start while
 //    the softmax is at the others: 32K chunk 705 -> 682 us with two parts);
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
         if (left > 0) next = entry();
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
-          ok = ok && wait(smem_u32(&b_kempty[slot]), ph, till);
+          ok = ok && wait.count(till, smem_u32(&b_kempty[slot]), ph);
           if (!__all_sync(~0u, ok)) {
             ok = false;
             break;
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
             step();
           }
           if (more) {
-            ok = ok && wait(smem_u32(&b_kfull[slot]), ph, till);
+            ok = ok && wait.count(till, smem_u32(&b_kfull[slot]), ph);
             if (first && mine) {
               ok = ok && wait(smem_u32(&b_qfull[h]), qp & 1);
               qp ^= 1;
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
               ok = ok && wait(smem_u32(&b_qfull[qb]), qp >> qb & 1);
               qp ^= 1 << qb;
             }
-            ok = ok && wait(smem_u32(&b_kfull[kslot]), kph, till);
+            ok = ok && wait.count(till, smem_u32(&b_kfull[kslot]), kph);
             if (!__all_sync(~0u, ok)) break;
             pa_fence_after();
             if (pa_elect()) qk(qb, n & 1, kslot, last);
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
         PaCursor<NH> cur;
         cur.set(p, s_place);
         PaFill fill[2];
-        int tile = 0, till = PaWait::counted(p, PaWait::QUERIES);
+        int tile = 0, blocks = 0, till = PaWait::counted(p, PaWait::QUERIES);   // (blocks: of the tiles before)
         bool ok = true;
 #pragma unroll 1
         for (; ok && cur.count() > 0; cur.next_tile(p)) {
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
 #pragma unroll 1
           for (int h = 0; h < halves; ++h) {
             const int qb = NH == 2 ? h : tile & 1;
-            ok = wait(smem_u32(&b_qempty[qb]), fill[qb].empty(), till);
+            ok = wait.count(till, smem_u32(&b_qempty[qb]), fill[qb].empty(), blocks);
             if (!ok) break;
             const unsigned full = smem_u32(&b_qfull[qb]);
             mbar_expect_tx(full, p.T * p.G * 128 * Sh::CB);
@@ -396,6 +397,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
             ++fill[qb].sent;
           }
           ++tile;
+          blocks += cur.count();
         }
         for (int qb = 0; qb < 2; ++qb)
           if (fill[qb].sent > 0) wait.drain(smem_u32(&b_qfull[qb]), fill[qb].landed());
@@ -439,7 +441,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
 #pragma unroll 1
         for (int k = 0; k < cnt; ++k, ++n) {
           const int sb = NH == 2 ? half : n & 1;
-          wait(smem_u32(&b_s[sb]), sp >> sb & 1);
+          wait(smem_u32(&b_s[sb]), sp >> sb & 1, NH == 2 ? n : 0);   // (half 1 may have sat out tiles before)
           sp ^= 1 << sb;
           __syncwarp();
           pa_fence_after();

@@ -17,7 +17,8 @@ namespace qe {
 
 constexpr int PA_BN = 128;                       // keys of a block
 constexpr int PA_MAX_CTAS = 1024;
-constexpr unsigned long long PA_WAIT_NS = 200000000ull;
+constexpr unsigned long long PA_WAIT_NS = 200000000ull;    // how long a wait may take,
+constexpr unsigned long long PA_BLOCK_NS = 10000ull;       // and for each block that is walked meanwhile (measured 1.4 us)
 constexpr float PA_LAZY = 8.f;                   // log2 of how far a row's maximum may pass its reference
 // log2 of what probabilities and sums are multiplied by: an fp16 probability below 2^-14 is subnormal, off by up to 2^-25 and zero from there
 // down.  7 above the weight, and PA_LAZY more at most, they stay within fp16's 2^16, and a weight is off by 2^-32 at most.
@@ -395,15 +396,17 @@ __device__ __forceinline__ void pa_wait_st() { asm volatile("tcgen05.wait::st.sy
 struct PaWait {
   const PagesView* pg;
   volatile int* abort;
-  // Bounded wait for the phase; false when it expired or the CTA is leaving.
-  __device__ __forceinline__ bool operator()(unsigned bar, unsigned parity) const {
-    return mbar_try_wait(bar, parity) || slow(bar, parity);
+  // Bounded wait for the phase; false when it expired or the CTA is leaving.  A warp that sits out whole tiles (the queries', the softmax
+  // of a second half that a tile does not have) says how many blocks its CTA has walked by the time the wait ends: a tile of 2^25 keys
+  // takes 0.4 s.
+  __device__ __forceinline__ bool operator()(unsigned bar, unsigned parity, int blocks = 0) const {
+    return mbar_try_wait(bar, parity) || slow(bar, parity, blocks);
   }
-  __device__ __forceinline__ bool slow(unsigned bar, unsigned parity) const {
+  __device__ __forceinline__ bool slow(unsigned bar, unsigned parity, int blocks) const {
     const unsigned long long t0 = globaltimer_ns();
     while (!mbar_try_wait(bar, parity)) {
       if (*abort) return false;
-      if (globaltimer_ns() - t0 > PA_WAIT_NS) {
+      if (globaltimer_ns() - t0 > PA_WAIT_NS + blocks * PA_BLOCK_NS) {
         pages_report(*pg, QE_PAGES_ERR_TIMEOUT);
         *abort = 1;
         return false;
@@ -414,8 +417,8 @@ struct PaWait {
   // The warps whose waits a test may take as expired, one wait per block or tile: those that send keys and values, issue products, send queries.
   enum Role { KEYS, PRODUCTS, QUERIES };
   static __device__ __forceinline__ int counted(const PaParams& p, Role role) { return (p.expire & 3) == role ? p.expire >> 2 : 0; }
-  __device__ __forceinline__ bool operator()(unsigned bar, unsigned parity, int& left) const {
-    if (--left != 0) return (*this)(bar, parity);
+  __device__ __forceinline__ bool count(int& left, unsigned bar, unsigned parity, int blocks = 0) const {
+    if (--left != 0) return (*this)(bar, parity, blocks);
     pages_report(*pg, QE_PAGES_ERR_TIMEOUT);
     *abort = 1;
     return false;

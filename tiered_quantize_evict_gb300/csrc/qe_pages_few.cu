@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       if (left > 0) next = entry();
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
-        ok = ok && wait(smem_u32(&b_kempty[slot]), ph, till);
+        ok = ok && wait.count(till, smem_u32(&b_kempty[slot]), ph);
         if (!__all_sync(~0u, ok)) {
           ok = false;
           break;
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           ok = ok && wait(smem_u32(&b_qfull[qb]), qp >> qb & 1);
           qp ^= 1 << qb;
         }
-        ok = ok && wait(smem_u32(&b_kfull[kslot]), kph, till);
+        ok = ok && wait.count(till, smem_u32(&b_kfull[kslot]), kph);
         if (!__all_sync(~0u, ok)) break;
         pa_fence_after();
         if (pa_elect()) {   // S n = K Q^T
@@ -253,17 +253,18 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       PaCursor<1> cur;
       cur.set(p, s_place);
       PaFill fill[2];
-      int tile = 0, till = PaWait::counted(p, PaWait::QUERIES);
+      int tile = 0, blocks = 0, till = PaWait::counted(p, PaWait::QUERIES);   // (blocks: of the tiles before)
 #pragma unroll 1
       for (; cur.count() > 0; cur.next_tile(p)) {
         const int qb = tile & 1;
-        if (!wait(smem_u32(&b_qempty[qb]), fill[qb].empty(), till)) break;
+        if (!wait.count(till, smem_u32(&b_qempty[qb]), fill[qb].empty(), blocks)) break;
         const unsigned full = smem_u32(&b_qfull[qb]);
         mbar_expect_tx(full, p.T * p.G * 128 * Sh::CB);
         for (int cb = 0; cb < Sh::CB; ++cb)
           pa_tma3(sm_q + qb * Sh::Q_BUF + cb * Sh::Q_CB, &mq, cb * 64, cur.h * p.G, cur.q.s.q0 + cur.j * p.T, full);
         ++fill[qb].sent;
         ++tile;
+        blocks += cur.count();
       }
       for (int qb = 0; qb < 2; ++qb)
         if (fill[qb].sent > 0) wait.drain(smem_u32(&b_qfull[qb]), fill[qb].landed());
