@@ -1,0 +1,99 @@
+"""Calls of the paged cache from other threads."""
+import threading
+
+import pytest
+
+from pages_testlib import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    return pytest.importorskip("torch")
+
+
+def in_thread(fn):
+    """fn's result on a thread of its own."""
+    got = []
+
+    def body():
+        try:
+            got.append((True, fn()))
+        except BaseException as e:  # noqa: BLE001
+            got.append((False, e))
+    t = threading.Thread(target=body)
+    t.start()
+    t.join()
+    ok, x = got[0]
+    if not ok:
+        raise x
+    return x
+
+
+@pytest.mark.parametrize("n", [40, 3000])
+def test_first_call_of_a_thread(torch, n):
+    """A thread that has made no CUDA call before; all it needs is there, so the binding allocates nothing either."""
+    import tiered_quantize_evict_gb300 as qe
+    c = Case(torch, [n], hkv=2, d=64, ps=16)
+    pool, seqs = c.objects(qe)
+    q, starts = c.draw(1, 4, 64).to(c.dev), c.ints([0, 1])
+    want = pool.attend(0, q, starts, seqs, max_q_len=1)
+    out = torch.zeros_like(q)
+    torch.cuda.synchronize()
+    in_thread(lambda: pool.attend(0, q, starts, seqs, max_q_len=1, out=out))
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    pool.check()
+
+
+def test_every_call_from_a_thread_of_its_own(torch):
+    import tiered_quantize_evict_gb300 as qe
+
+    def state():
+        k = torch.zeros(2, 24, 2, 16, 64, device="cuda", dtype=torch.bfloat16)
+        return qe.PagePool(k, torch.zeros_like(k)), qe.PageTable.empty(4, 8, 24, k.device)
+
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    k, q = torch.randn(30, 2, 64, device="cuda").bfloat16(), torch.randn(30, 4, 64, device="cuda").bfloat16()
+    rows, lens, starts, page = ints(0, 1), ints(20, 10), ints(0, 20, 30), ints(23)
+    rope = qe.Rope(64)
+
+    def steps(pool, seqs):
+        return [lambda: pool.resize(seqs, rows, lens), lambda: pool.append(1, k, k, starts, seqs, rows=rows, q=q, rope=rope),
+                lambda: pool.attend(1, q, starts, seqs, rows=rows), lambda: pool.fork(seqs, ints(0), ints(2)), lambda: pool.free(seqs, ints(1)),
+                lambda: pool.compact(seqs), lambda: pool.copy(ints(0), page), lambda: pool.gather(1, seqs, 0, 20), lambda: pool.check()]
+
+    here, there = state(), state()
+    want = [f() for f in steps(*here)]
+    got = [in_thread(f) for f in steps(*there)]
+    for a, b in zip(want, got):
+        for x, y in zip(*((t if isinstance(t, tuple) else (t,)) for t in (a, b))):
+            assert x is y is None or torch.equal(x, y)
+    for a, b in ((here[0].k, there[0].k), (here[1].table, there[1].table), (here[1].refs, there[1].refs)):
+        assert torch.equal(a, b)
+
+
+def test_threads_that_share_a_pool(torch):
+    """Each on a stream of its own, over rows that are cut (so that each needs scratch)."""
+    import tiered_quantize_evict_gb300 as qe
+    c = Case(torch, [5000, 1500, 900], hkv=2, d=128, ps=32)
+    pool, seqs = c.objects(qe)
+    q, starts = c.draw(6, 8, 128).to(c.dev), c.ints([0, 3, 4, 6])
+    want = {hint: pool.attend(0, q, starts, seqs, max_q_len=hint) for hint in (0, 1, 3, 16)}
+    torch.cuda.synchronize()
+    outs = {}
+
+    def work(hint):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            outs[hint] = [pool.attend(0, q, starts, seqs, max_q_len=hint) for _ in range(50)]
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(hint,)) for hint in want]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for hint, x in want.items():
+        assert all(torch.equal(x, y) for y in outs[hint])
+    pool.check()

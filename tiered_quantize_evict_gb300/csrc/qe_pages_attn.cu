@@ -868,22 +868,28 @@ cudaError_t launch_pages_attend(const PagesAttendParams& a, int fp16, int device
   CUtensorMap maps[3];
   const CUtensorMapDataType ty = fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const cuuint32_t ones[4] = {1, 1, 1, 1};
+  // (a driver call: a thread that has made none of the runtime's has no context yet, which cudaSetDevice gives it)
+  auto encode = [&](CUtensorMap* map, int rank, uint16_t* base, const cuuint64_t* dim, const cuuint64_t* str, const cuuint32_t* box) {
+    auto call = [&] {
+      return enc(map, ty, rank, base, dim, str, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = call();
+    if ((r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) && cudaSetDevice(device) == cudaSuccess) r = call();
+    return r == CUDA_SUCCESS;
+  };
   auto bytes = [&](long long stride) { return (cuuint64_t)(stride > 0 ? stride * 2 : g.D * 2); };   // (an axis of one entry: any)
   {
     const cuuint64_t dim[3] = {(cuuint64_t)g.D, (cuuint64_t)a.Hq, (cuuint64_t)a.c.total};
     const cuuint64_t str[2] = {bytes(a.Hq > 1 ? a.qhs : 0), bytes(a.c.total > 1 ? a.qts : 0)};
     const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.T};
-    if (enc(&maps[0], ty, 3, const_cast<uint16_t*>(a.q), dim, str, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
+    if (!encode(&maps[0], 3, const_cast<uint16_t*>(a.q), dim, str, box)) return cudaErrorInvalidValue;
   }
   for (int i = 0; i < 2; ++i) {
     const cuuint64_t dim[4] = {(cuuint64_t)g.D, (cuuint64_t)g.S, (cuuint64_t)g.H, (cuuint64_t)g.P};
     const cuuint64_t str[3] = {bytes(g.ts), bytes(g.hs), bytes(g.ps)};
     const cuuint32_t box[4] = {64, (cuuint32_t)(g.S < 128 ? g.S : 128), 1, 1};
-    if (enc(&maps[1 + i], ty, 4, (i ? g.v : g.k) + a.layer * g.ls, dim, str, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
+    if (!encode(&maps[1 + i], 4, (i ? g.v : g.k) + a.layer * g.ls, dim, str, box)) return cudaErrorInvalidValue;
   }
   if (one && p.T * p.G <= PAGES_FEW_ROWS) return launch_pages_few(p, maps, fp16, device, st);
   if (g.D == 128) {
