@@ -1,4 +1,4 @@
-"""Calls of the paged cache from other threads."""
+"""Calls of the paged cache from other threads, and with numbers outside of what a C int holds."""
 import threading
 
 import pytest
@@ -97,3 +97,23 @@ def test_threads_that_share_a_pool(torch):
     for hint, x in want.items():
         assert all(torch.equal(x, y) for y in outs[hint])
     pool.check()
+
+
+def test_numbers_outside_of_a_c_int(torch):
+    import tiered_quantize_evict_gb300 as qe
+    c = Case(torch, [40], hkv=1, d=64, ps=16, layers=2)
+    pool, seqs = c.objects(qe)
+    q, k, starts = c.draw(1, 1, 64).to(c.dev), c.draw(1, 1, 64).to(c.dev), c.ints([0, 1])
+    for bad in (2 ** 32, 2 ** 32 + 1, -2 ** 32, 2 ** 63, 2, -1):
+        with pytest.raises(qe.QEError, match="layer"):
+            pool.attend(bad, q, starts, seqs)
+        with pytest.raises(qe.QEError, match="layer"):
+            pool.append(bad, k, k, starts, seqs)
+        with pytest.raises(qe.QEError, match="layer"):
+            pool.gather(bad, seqs, 0, 8)
+    for start, n in ((2 ** 32, 8), (-2 ** 32, 8), (0, 2 ** 40), (2 ** 31 - 1, 8), (-1, 8), (0, -1)):
+        with pytest.raises(qe.QEError, match="start"):
+            pool.gather(0, seqs, start, n)
+    for bad in (2 ** 31, 2 ** 40, -1, -2 ** 40):
+        with pytest.raises(qe.QEError, match="max_q_len"):
+            pool.attend(0, q, starts, seqs, max_q_len=bad)

@@ -196,6 +196,12 @@ class PagePool:
             raise _bad(f"the page table is on {seqs.table.device}, the pool on {self.device}")
         return seqs._ref
 
+    def _layer(self, layer):
+        # (here, not in the call: ctypes cuts a number to a C int)
+        if not 0 <= layer < self.n_layers:
+            raise _bad(f"layer {layer} out of range")
+        return layer
+
     def _chunks(self, q_start, rows, total):
         n = _ints("q_start", q_start, self._index) - 1
         if rows is None:
@@ -246,7 +252,7 @@ class PagePool:
                 raise _bad(f"positions must be int32 [{rope.n_axes}, {total}] on {self.device}, tokens contiguous")
             pp, pst = positions.data_ptr(), ps[0]
         st = self._lib.qe_pages_append(
-            self._ref, layer, self._seqs(seqs), self._chunks(q_start, rows, total),
+            self._ref, self._layer(layer), self._seqs(seqs), self._chunks(q_start, rows, total),
             _APPEND.pack(k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1], qp, op, qs[0], qs[1], os[0], os[1], hq,
                          rope._addr if rope is not None else 0, pp, pst), _raw_stream(self._index))
         if st:
@@ -267,9 +273,11 @@ class PagePool:
             os = self._tokens("out", out, total, hq)
         lse = torch.empty(total, hq, dtype=torch.float32, device=self.device) if return_lse else None
         ref, c = self._seqs(seqs), self._chunks(q_start, rows, total)
+        if not 0 <= max_q_len < 2 ** 31:
+            raise _bad(f"max_q_len {max_q_len} out of range")
         a = _ATTEND.pack(q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else 0, qs[0], qs[1], os[0], os[1], hq,
                          1 if causal else 0, max_q_len, self._scale if scale is None else scale)
-        need, stream = self._need(seqs, -1), _raw_stream(self._index)
+        need, stream, layer = self._need(seqs, -1), _raw_stream(self._index), self._layer(layer)
         if need:
             with self._lock:
                 ws = self._scratch(need, stream)
@@ -340,7 +348,9 @@ class PagePool:
                out: Optional[Sequence[torch.Tensor]] = None):
         """qe_pages_gather: (k, v), each [n_rows][n_kv_heads][n_tokens][head_dim], the layout ``QECache.qe_append`` takes."""
         n = seqs._shape[0] if rows is None else _ints("rows", rows, self._index)
-        shape = (n, self.n_kv_heads, max(0, n_tokens), self.head_dim)
+        if start < 0 or n_tokens < 0 or start + n_tokens > 2 ** 31 - 257:
+            raise _bad("start and n_tokens must be >= 0, start + n_tokens below 2^31 - 256")
+        shape = (n, self.n_kv_heads, n_tokens, self.head_dim)
         if out is None:
             k = torch.empty(shape, dtype=self.dtype, device=self.device)
             v = torch.empty_like(k)
@@ -349,7 +359,7 @@ class PagePool:
             for t in (k, v):
                 if t.dtype is not self.dtype or t.get_device() != self._index or t.shape != shape or not t.is_contiguous():
                     raise _bad(f"out must be two contiguous {self.dtype} tensors {list(shape)} on {self.device}")
-        st = self._lib.qe_pages_gather(self._ref, layer, self._seqs(seqs), rows.data_ptr() if rows is not None else None, n, start,
+        st = self._lib.qe_pages_gather(self._ref, self._layer(layer), self._seqs(seqs), rows.data_ptr() if rows is not None else None, n, start,
                                        n_tokens, k.data_ptr(), v.data_ptr(), _raw_stream(self._index))
         if st:
             self._check(st)
