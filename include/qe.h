@@ -470,7 +470,7 @@ qe_status qe_decode_step_noalloc(qe_handle h, int layer, const void* q, void* ou
  * serving system, H2O page §6, KV Cache evolution page §10): what comes before the tiered cache.
  * Sequences of different lengths keep their exact keys and values in pages of one pool, share
  * the pages of common prefixes, and are prefilled in chunks; qe_pages_gather hands a prefilled
- * prompt to qe_append in the layout it takes.  One step of a serving loop is
+ * prompt to qe_append in the layout it takes (its limits are stated there).  One step of a serving loop is
  *   qe_pages_resize (pages for the new tokens), then per layer qe_pages_append (rotary
  *   positions, keys and values into the pages) and qe_pages_attend (the chunk's attention).
  *
@@ -623,7 +623,9 @@ qe_status qe_pages_copy(const qe_pages* pages, const int* src, const int* dst, i
 
 /* Tokens [start, start + n_tokens) of n_seqs rows (rows, or all from row 0 where NULL) of one layer, dense:
  * k_out, v_out [n_seqs][n_kv_heads][n_tokens][head_dim], the layout qe_append takes.  Tokens behind a row's kv_len
- * are zeros. */
+ * are zeros.  What qe_append takes further: bf16 (an fp16 pool's keys and values have to be converted); as many tokens of every
+ * row (a shorter row's zeros would be cached as tokens); and keys as its cache keeps them, which with rope_theta > 0 are not
+ * rotated yet, while qe_pages_append has stored them rotated: such a cache needs its keys from elsewhere. */
 qe_status qe_pages_gather(const qe_pages* pages, int layer, const qe_page_table* seqs, const int* rows, int n_seqs,
                           int start, int n_tokens, void* k_out, void* v_out, void* stream);
 

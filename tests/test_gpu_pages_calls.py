@@ -1,4 +1,5 @@
-"""Calls of the paged cache from other threads, and with numbers outside of what a C int holds."""
+"""Calls of the paged cache from other threads, with numbers outside of what a C int holds, and the hand-over of
+fp16 to the tiered cache."""
 import threading
 
 import pytest
@@ -117,3 +118,20 @@ def test_numbers_outside_of_a_c_int(torch):
     for bad in (2 ** 31, 2 ** 40, -1, -2 ** 40):
         with pytest.raises(qe.QEError, match="max_q_len"):
             pool.attend(0, q, starts, seqs, max_q_len=bad)
+
+
+def test_the_tiered_cache_takes_no_fp16(torch):
+    """Its keys, values and queries are bf16: fp16 bits are not read as if they were."""
+    import tiered_quantize_evict_gb300 as qe
+    c = Case(torch, [40], hkv=1, d=64, ps=16, dtype="fp16")
+    pool, seqs = c.objects(qe)
+    k, v = pool.gather(0, seqs, 0, 32)
+    cfg = qe.QEConfig(batch=1, n_layers=1, n_q_heads=4, n_kv_heads=1, head_dim=64, window=16, route_period=16, n_sink=4, n_recent=16,
+                      max_context=512, cap_mode=0, kf=8, kq=8, out_fp32=0)
+    cache = qe.QECache(cfg, torch.cuda.current_stream().cuda_stream)
+    for a, b in ((k, v), (k.bfloat16(), v), (k, v.bfloat16()), (k.cpu().numpy(), v.cpu().numpy())):
+        with pytest.raises(qe.QEError, match="bf16"):
+            cache.qe_append(0, a, b, 32)
+    cache.qe_append(0, k.bfloat16(), v.bfloat16(), 32)
+    cache.qe_synchronize()
+    cache.close()

@@ -162,6 +162,19 @@ def _ptr(x) -> int:
     raise TypeError(type(x))
 
 
+_HALF = {}   # dtype -> is it fp16
+
+
+def _bf16(name: str, x) -> int:
+    """Address of bf16 values (or of their bits as 16-bit integers); fp16 is refused, its bits would be read as bf16."""
+    half = _HALF.get(x.dtype)
+    if half is None:
+        half = _HALF[x.dtype] = str(x.dtype) in ("torch.float16", "float16")
+    if half:
+        raise QEError(QE_ERR_INVALID_ARG, f"{name} is fp16: the tiered cache takes bf16")
+    return _ptr(x)
+
+
 def _is_host(x) -> bool:
     if isinstance(x, np.ndarray):
         return True
@@ -206,22 +219,22 @@ class QECache:
     # ---------------------------------------------------------------- the path
     def qe_append(self, layer: int, k, v, n_tokens: int):
         flags = QE_HOST_PTRS if _is_host(k) else QE_DEVICE_PTRS
-        self._check(self._lib.qe_append(self.h, layer, _ptr(k), _ptr(v), n_tokens, flags))
+        self._check(self._lib.qe_append(self.h, layer, _bf16("k", k), _bf16("v", v), n_tokens, flags))
 
     def qe_decode_step(self, layer: int, q, out):
         flags = QE_HOST_PTRS if _is_host(q) else QE_DEVICE_PTRS
-        self._check(self._lib.qe_decode_step(self.h, layer, _ptr(q), _ptr(out), flags))
+        self._check(self._lib.qe_decode_step(self.h, layer, _bf16("q", q), _bf16("out", out), flags))
 
     def qe_decode_step_noalloc(self, layer: int, q, out):
         """qe_decode_step without any device allocation (device q/out only; scratch is a static array)."""
         if _is_host(q) or _is_host(out):
             raise ValueError("qe_decode_step_noalloc takes device tensors only")
-        self._check(self._lib.qe_decode_step_noalloc(self.h, layer, _ptr(q), _ptr(out)))
+        self._check(self._lib.qe_decode_step_noalloc(self.h, layer, _bf16("q", q), _bf16("out", out)))
 
     def qe_verify(self, layer: int, q, k, v, out, n_q: int):
         """Speculative verify of n_q drafts: q [n_q][B][Hq][D], k/v [n_q][B][Hkv][D], out [n_q][B][Hq][D]."""
         flags = QE_HOST_PTRS if _is_host(q) else QE_DEVICE_PTRS
-        self._check(self._lib.qe_verify(self.h, layer, _ptr(q), _ptr(k), _ptr(v), _ptr(out), n_q, flags))
+        self._check(self._lib.qe_verify(self.h, layer, _bf16("q", q), _bf16("k", k), _bf16("v", v), _bf16("out", out), n_q, flags))
 
     def qe_verify_commit(self, layer: int, n_accept: int):
         self._check(self._lib.qe_verify_commit(self.h, layer, n_accept))

@@ -8,7 +8,8 @@ and reference counts, ``Rope`` the rotary positions of several axes.  A serving 
         q = pool.append(layer, k, v, q_start, seqs, rows=rows, q=q, rope=rope, positions=positions)
         o = pool.attend(layer, q, q_start, seqs, rows=rows)
 
-and ``pool.gather(layer, seqs, 0, n)`` gives keys and values as ``QECache.qe_append`` takes them.
+and ``pool.gather(layer, seqs, 0, n)`` gives keys and values in the layout ``QECache.qe_append`` takes: of a bf16 pool, for
+rows that all have n tokens (shorter ones are filled up with zeros), and for a cache with ``rope_theta`` 0 (``append`` stores rotated keys).
 
 Work runs on the current stream of the pool's device; nothing waits for the GPU except ``check``.
 A pool keeps a scratch buffer for each stream it is used on; a call that is captured into a graph
@@ -346,7 +347,8 @@ class PagePool:
 
     def gather(self, layer: int, seqs: PageTable, start: int, n_tokens: int, *, rows: Optional[torch.Tensor] = None,
                out: Optional[Sequence[torch.Tensor]] = None):
-        """qe_pages_gather: (k, v), each [n_rows][n_kv_heads][n_tokens][head_dim], the layout ``QECache.qe_append`` takes."""
+        """qe_pages_gather: (k, v), each [n_rows][n_kv_heads][n_tokens][head_dim], the layout ``QECache.qe_append`` takes (bf16
+        rows of one length); zeros behind a row's length."""
         n = seqs._shape[0] if rows is None else _ints("rows", rows, self._index)
         if start < 0 or n_tokens < 0 or start + n_tokens > 2 ** 31 - 257:
             raise _bad("start and n_tokens must be >= 0, start + n_tokens below 2^31 - 256")
