@@ -6,10 +6,11 @@ and reference counts, ``Rope`` the rotary positions of several axes.  A serving 
     pool.resize(seqs, rows, new_len)                      # pages for the new tokens
     for layer in range(n_layers):
         q = pool.append(layer, k, v, q_start, seqs, rows=rows, q=q, rope=rope, positions=positions)
-        o = pool.attend(layer, q, q_start, seqs, rows=rows)
+        o = pool.attend(layer, q, q_start, seqs, rows=rows, max_q_len=longest)   # (the longest chunk, or 0 if it is not known)
 
 and ``pool.gather(layer, seqs, 0, n)`` gives keys and values in the layout ``QECache.qe_append`` takes: of a bf16 pool, for
 rows that all have n tokens (shorter ones are filled up with zeros), and for a cache with ``rope_theta`` 0 (``append`` stores rotated keys).
+Nothing here carries a gradient: tensors are read and written by address, whatever autograd would record.
 
 Work runs on the current stream of the pool's device; nothing waits for the GPU except ``check``.
 A pool keeps a scratch buffer for each stream it is used on; a call that is captured into a graph
