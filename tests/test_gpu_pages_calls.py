@@ -2,6 +2,7 @@
 fp16 to the tiered cache."""
 import threading
 
+import numpy as np
 import pytest
 
 from pages_testlib import Case
@@ -135,3 +136,24 @@ def test_the_tiered_cache_takes_no_fp16(torch):
     cache.qe_append(0, k.bfloat16(), v.bfloat16(), 32)
     cache.qe_synchronize()
     cache.close()
+
+
+def test_calls_of_no_token(torch):
+    """Empty chunks, as empty tensors come: with strides of 0 from numpy."""
+    import tiered_quantize_evict_gb300 as qe
+    c = Case(torch, [40], hkv=2, d=64, ps=16)
+    pool, seqs = c.objects(qe)
+    before = c.k.clone()
+    for x, q in ((torch.zeros(0, 2, 64), torch.zeros(0, 4, 64)), (torch.from_numpy(np.zeros((0, 2, 64), np.float32)), torch.from_numpy(np.zeros((0, 4, 64), np.float32)))):
+        x, q = x.to(c.dt).to(c.dev), q.to(c.dt).to(c.dev)
+        assert pool.append(0, x, x, c.ints([0, 0]), seqs, q=q, rope=qe.Rope(64)).shape == (0, 4, 64)
+        out, lse = pool.attend(0, q, c.ints([0, 0]), seqs, return_lse=True)
+        assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    none = c.ints(np.zeros(0))
+    pool, seqs = c.objects(qe, refs=True)
+    pool.resize(seqs, none, none)
+    pool.fork(seqs, none, none)
+    pool.copy(none, none)
+    assert pool.gather(0, seqs, 5, 0)[0].shape == (1, 2, 0, 64) and pool.gather(0, seqs, 0, 8, rows=none)[1].shape == (0, 2, 8, 64)
+    pool.check()
+    assert torch.equal(c.k.view(torch.int16), before.view(torch.int16))

@@ -217,7 +217,7 @@ class PagePool:
         if t.dtype is not self.dtype or t.get_device() != self._index or t.shape != (total, heads, self.head_dim):
             raise _bad(f"{name} must be a {self.dtype} tensor [{total}, {heads}, {self.head_dim}] on {self.device}")
         st = t.stride()
-        if st[2] != 1:
+        if st[2] != 1 and total > 0:   # (numpy's empty arrays have strides of 0)
             raise _bad(f"{name} must have contiguous channels")
         return st
 
