@@ -133,3 +133,65 @@ def test_tiles_of_a_third_of_a_second(torch, m, hint):
     out = pool.attend(0, q, ints(np.cumsum([0, *m])), seqs, rows=ints([0] * len(m)), causal=False, max_q_len=hint)
     pool.check()
     assert torch.equal(out[:, 0], v.to(dev).expand(sum(m), d))
+
+
+def remainder_bounds(torch, c, q, row, hq, scale):
+    """(out, tolerance) where probabilities are kept as a rounded value and its rounded remainder (bf16).
+
+    With u the half step 2^-8: the result is rounded once, u |out|.  A probability is off by u times its remainder, which is u of it at
+    most: u^2 sum w |v|.  Were every product and sum of the tensor cores cut off instead of rounded, a logit would be off by
+    (D + 4) 2^-23 of the sum of its terms' sizes (which moves numerator and denominator alike: 2 x) and a result by n 2^-23 of sum w |v|;
+    exponentials and running sums take 2^-20 + n 2^-24."""
+    from oracle import pages as op
+    k, v = bits(c.kh[row][0]), bits(c.vh[row][0])
+    out, _, spread, _ = op.attend(q, k, v, c.hkv, scale, True)
+    mag = np.stack([scale * (np.abs(q[:, h]) @ np.abs(k[:, h // (hq // c.hkv)]).T).max(-1) for h in range(hq)], 1)
+    u, n = 2.0 ** -8, k.shape[0]
+    rel = u * u + 2 * (c.d + 4) * 2.0 ** -23 * mag + 2.0 ** -20 + n * (2.0 ** -23 + 2.0 ** -24)
+    return out, (u * np.abs(out) + rel[..., None] * spread) * 1.01
+
+
+def rounded(x):
+    """float64 to bf16 and back, to nearest."""
+    m, e = np.frexp(x)
+    return np.ldexp(np.rint(m * 256) / 256, e)
+
+
+def plain_probabilities(q, k, v, hkv, scale, keep):
+    """Attention with probabilities in bf16, and their remainders (keep), all else in 64 bits; the result in bf16."""
+    m, hq, _ = q.shape
+    out = np.zeros(q.shape)
+    for h in range(hq):
+        for j in range(m):
+            vis = k.shape[0] - m + j + 1
+            s = scale * (k[:vis, h // (hq // hkv)] @ q[j, h])
+            p = np.exp(s - s.max())
+            hi = rounded(p)
+            out[j, h] = rounded((hi + (rounded(p - hi) if keep else 0)) @ v[:vis, h // (hq // hkv)] / p.sum())
+    return out
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("m,hint,hq,hkv", [(1, 1, 4, 1), (4, 4, 8, 2), (16, 16, 1, 1), (6, 6, 6, 2), (20, 20, 4, 2), (32, 32, 4, 1)])
+def test_remainders_of_the_probabilities(torch, d, m, hint, hq, hkv):
+    """Up to 128 rows a tile (in both kernels): the bound that holds only if the remainders of the probabilities meet their values
+    too -- without them, as the oracle shows, the same inputs pass it several times over."""
+    import tiered_quantize_evict_gb300 as qe
+    c = Case(torch, [200, 137], hkv=hkv, d=d, ps=32, seed=d + m)
+    for row in (0, 1):
+        c.kh[row][0].mul_(0.25)
+        put_keys(torch, c, row)
+    pool, seqs = c.objects(qe)
+    qh = c.draw(2 * m, hq, d)
+    out = pool.attend(0, qh.to(c.dev), c.ints([0, m, 2 * m]), seqs, max_q_len=hint)
+    pool.check()
+    worst = 0
+    for row in (0, 1):
+        q = bits(qh[row * m:(row + 1) * m])
+        ref, tol = remainder_bounds(torch, c, q, row, hq, d ** -0.5)
+        k, v = bits(c.kh[row][0]), bits(c.vh[row][0])
+        assert (np.abs(plain_probabilities(q, k, v, hkv, d ** -0.5, True) - ref) <= tol).all()
+        worst = max(worst, (np.abs(plain_probabilities(q, k, v, hkv, d ** -0.5, False) - ref) / tol).max())
+        err = np.abs(bits(out[row * m:(row + 1) * m]) - ref)
+        assert (err <= tol).all(), f"row {row}: {(err / tol).max():.2f} of the bound"
+    assert worst > 2
