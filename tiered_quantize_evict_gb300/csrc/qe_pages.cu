@@ -498,7 +498,8 @@ static cudaError_t launch_planned(const PagesView& pg, const TableView& t, const
   plan_layout(ws, pg.P, t.rows, n, &s);
   // at most a page per entry is copied (none where rows are only freed)
   const long long copied = !FORK && !b ? 0 : (long long)n * pg.L * 2 * pg.H * pg.S * pg.D * 2;
-  // (one block: 4 rows of 19 pages forked and freed 12.8 us, with two launches each 14.4; 64 rows of 94 pages 50.8 against 48.2)
+  // (one block: 4 rows of 19 pages forked and freed 12.8 us, with two launches each 14.4; 64 rows of 94 pages 50.8 against 48.2.  What
+  // could be copied counts as if every entry copied a page: a fork or resize to lengths of a usual cache of several layers is two launches)
   if (copied <= 128 * 1024 && (long long)n * t.cols <= 2048) {
     return launch_after(pages_plan_kernel<FORK, true>, 1, PLAN_THREADS, st, pg, t, a, b, n, s);
   }

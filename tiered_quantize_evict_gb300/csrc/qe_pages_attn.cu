@@ -42,8 +42,8 @@
 
 namespace qe {
 
-// Parts that a block's probabilities are handed over in.  Four with two halves (512 tokens over 8K 54.5 -> 52.9 us against two, 32K chunk
-// 688 -> 683); with one half, where a part more is a wait more for two stores, 64-channel drafts take 105 us with four and 92 with two.
+// Parts that a block's probabilities are handed over in.  Four with two halves (512 tokens over 8K 54.7 -> 53.1 us against two, 64-channel
+// chunk 491 -> 485); with one half, where a part more is a wait more for two stores, 64-channel drafts take 105 us with four and 92 with two.
 template <int NH>
 constexpr int PA_PARTS = NH == 2 ? 4 : 2;
 
