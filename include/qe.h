@@ -496,6 +496,7 @@ qe_status qe_decode_step_noalloc(qe_handle h, int layer, const void* q, void* ou
  * its own. */
 
 enum { QE_DTYPE_BF16 = 0, QE_DTYPE_FP16 = 1 };
+enum { QE_PAGES_DROPPED = -2 };   /* a table entry whose page qe_pages_drop gave back */
 enum {
   QE_PAGES_ERR_PAGE = 1,      /* a page index outside the pool, or a count of references that went wrong */
   QE_PAGES_ERR_ROW = 2,       /* a row index, length or q_start out of range, or a row named twice */
@@ -520,7 +521,7 @@ typedef struct {
 
 /* The sequences.  Row r holds the tokens [0, kv_len[r]) of one sequence, on the pages
  * table[r * row_stride + i], i < ceil(kv_len[r] / page_size); entries behind them are -1 after
- * the calls that manage pages.  A row holds at most 2^30 tokens; tables whose pages are managed have
+ * the calls that manage pages, and QE_PAGES_DROPPED where qe_pages_drop gave a page back.  A row holds at most 2^30 tokens; tables whose pages are managed have
  * n_rows * (max_pages + 1) below 2^31.  refs[p] is how many table entries name page p, 0 for a free page
  * (qe_pages_append, _attend and _gather do not read it; it may be NULL for them).  A page that two rows
  * share is full: the calls below keep it so. */
@@ -594,6 +595,41 @@ qe_status qe_pages_attend(const qe_pages* pages, int layer, const qe_page_table*
                           const qe_pages_attend_args* args, void* workspace, size_t bytes, void* stream);
 /* Bytes of workspace that qe_pages_attend needs with tables of this size (0 where a row is too short to be split). */
 qe_status qe_pages_attend_workspace(const qe_pages* pages, const qe_page_table* seqs, size_t* bytes);
+
+/* The same with a sliding window: the query at position p sees key i <= p if i > p - window or i < sinks
+ * (window >= 1; sinks >= 0, the first tokens, which stay visible; args->causal must be 1).  Pages that none of the call's
+ * queries sees are not looked at and may be gone (qe_pages_drop).  Keys and values that none of them sees may be anything.
+ * A value that is not finite may also reach the chunk's other tokens, those behind it as those before. */
+qe_status qe_pages_attend_window(const qe_pages* pages, int layer, const qe_page_table* seqs, const qe_chunks* chunks,
+                                 const qe_pages_attend_args* args, int window, int sinks, void* workspace, size_t bytes, void* stream);
+
+/* Groups of the call's sequences that share their first tokens: group g is the sequences [group_start[g], group_start[g + 1])
+ * of the chunks, and group_start runs from 0 to n_seqs.  The first prefix_len[g] tokens (rounded down to whole pages) of them
+ * all are those of the group's first sequence, which keeps them; the others' table entries there are not looked at. */
+typedef struct {
+  const int* group_start; /* [n_groups + 1] */
+  const int* prefix_len;  /* [n_groups] */
+  int n_groups;
+  int max_group_len;      /* the most packed tokens of a group, a hint that picks the tile (results are right for any): 0 = unknown */
+} qe_groups;
+
+/* qe_pages_attend for sequences that share prefixes: a prefix is read once for the queries of its whole group.  The same
+ * results (up to the order of sums) as qe_pages_attend on tables that repeat the prefix's pages.  Every prefix is at most
+ * kv_len - m of each of the group's chunks of m tokens (causal = 0: kv_len) and at most the first sequence's kv_len; one that is not, or a
+ * group_start that decreases or leaves [0, n_seqs], sets QE_PAGES_ERR_ROW (a prefix is cut to the first sequence's length; a
+ * chunk that begins inside its prefix sees all of it; sequences of no group are left alone).  args->max_q_len is not looked at.
+ * Sizes that can be served: (S + 1) max_pages page_size below 2^31, with S = min(n_seqs, 256 n_kv_heads / n_q_heads). */
+qe_status qe_pages_attend_shared(const qe_pages* pages, int layer, const qe_page_table* seqs, const qe_chunks* chunks,
+                                 const qe_pages_attend_args* args, const qe_groups* groups, void* workspace, size_t bytes, void* stream);
+/* Bytes of workspace that qe_pages_attend_shared needs; qe_pages_attend_window needs what qe_pages_attend does. */
+qe_status qe_pages_attend_shared_workspace(const qe_pages* pages, size_t* bytes);
+
+/* Give back the pages that a window has left: of each of n rows, those whose tokens are all behind the first `sinks` and all
+ * before kv_len - window + 1, which no later token sees.  Their entries become QE_PAGES_DROPPED; lengths and positions stay as
+ * they are.  Rows grow, are forked, cut, freed and compacted as before (a row that is cut back to inside of a dropped page is
+ * reported where that page is needed: tokens taken back widen the window, so drop with a window that much larger).  A row may
+ * be named twice.  Pages given back are free from the next call on. */
+qe_status qe_pages_drop(const qe_pages* pages, const qe_page_table* seqs, const int* rows, int n, int window, int sinks, void* stream);
 
 /* Set the length of n rows (rows[i] to new_len[i], device int32): pages are taken (the lowest free
  * ones, in the order of the call) or given back; a length of 0 frees the row (new_len NULL: all of them).  Where the page that ends up partly

@@ -10,6 +10,9 @@ import math
 import numpy as np
 
 
+DROPPED = -2   # a table entry whose page was given back
+
+
 class Pages:
     """Page table, lengths and reference counts (lists) over a pool [L][P][H][S][D] of keys and values."""
 
@@ -45,7 +48,8 @@ class Pages:
                 p = free.pop(0)
                 self.table[r][j], self.refs[p] = p, 1
             for j in range(-(-n // self.S), -(-old // self.S)):
-                self.refs[self.table[r][j]] -= 1
+                if self.table[r][j] != DROPPED:
+                    self.refs[self.table[r][j]] -= 1
                 self.table[r][j] = -1
             self.kv_len[r] = n
         return copies
@@ -61,13 +65,22 @@ class Pages:
             for j in range(full):
                 p = self.table[s][j]
                 self.table[d][j] = p
-                self.refs[p] += 1
+                if p != DROPPED:
+                    self.refs[p] += 1
             if lens[s] % self.S:
                 p = free.pop(0)
                 copies.append((self.table[s][full], p, lens[s] % self.S))
                 self.table[d][full], self.refs[p] = p, 1
             self.kv_len[d] = lens[s]
         return copies
+
+    def drop(self, rows, window, sinks):
+        """Pages without a sink and wholly before the next token's window are given back."""
+        for r in rows:
+            for j, p in enumerate(self.table[r]):
+                if p != DROPPED and j * self.S >= sinks and (j + 1) * self.S <= self.kv_len[r] - window + 1:
+                    self.refs[p] -= 1
+                    self.table[r][j] = DROPPED
 
     def compact(self):
         n = sum(r > 0 for r in self.refs)
@@ -96,21 +109,32 @@ def attend(q, k, v, n_kv_heads, scale, causal):
 
     spread is sum_i w_i |v_i| and the last the softmax's denominator relative to its maximum: what a rounding
     of the probabilities is measured against."""
+    m, n = q.shape[0], k.shape[0]
+    return attend_seen(q, k, v, n_kv_heads, scale, [range(max(0, n - m + j + 1) if causal else n) for j in range(m)])
+
+
+def window_seen(m, n, window, sinks):
+    """The keys that each of the last m of n tokens sees under a sliding window with sinks."""
+    return [[i for i in range(max(0, p + 1)) if i > p - window or i < sinks] for p in range(n - m, n)]
+
+
+def attend_seen(q, k, v, n_kv_heads, scale, seen):
+    """attend where query j sees the keys seen[j]."""
     m, hq, d = q.shape
-    n = k.shape[0]
     out, spread = np.zeros((m, hq, d)), np.zeros((m, hq, d))
     lse, den = np.full((m, hq), -np.inf), np.ones((m, hq))
-    for h in range(hq):
-        g = h // (hq // n_kv_heads)
-        for j in range(m):
-            vis = max(0, n - m + j + 1) if causal else n
-            if vis == 0:
-                continue
-            s = scale * (k[:vis, g].astype(np.float64) @ q[j, h].astype(np.float64))
+    for j in range(m):
+        vis = np.fromiter(seen[j], np.int64)
+        if vis.size == 0:
+            continue
+        for h in range(hq):
+            g = h // (hq // n_kv_heads)
+            kk, vv = k[vis, g].astype(np.float64), v[vis, g]
+            s = scale * (kk @ q[j, h].astype(np.float64))
             w = np.exp(s - s.max())
             den[j, h] = w.sum()
             lse[j, h] = s.max() + math.log(w.sum())
             w /= w.sum()
-            out[j, h] = w @ v[:vis, g]
-            spread[j, h] = w @ np.abs(v[:vis, g])
+            out[j, h] = w @ vv
+            spread[j, h] = w @ np.abs(vv)
     return out, lse, spread, den

@@ -33,6 +33,7 @@ EXPORTED = [
     "qe_launch_overhead",
     "qe_pages_append", "qe_pages_attend", "qe_pages_attend_workspace", "qe_pages_resize", "qe_pages_fork",
     "qe_pages_compact", "qe_pages_manage_workspace", "qe_pages_copy", "qe_pages_gather",
+    "qe_pages_attend_window", "qe_pages_attend_shared", "qe_pages_attend_shared_workspace", "qe_pages_drop",
 ]
 QE_DEBUG_FAIL_DEVICE_ALLOC, QE_DEBUG_FAIL_HOST_STORE, QE_DEBUG_EXPIRE_WAIT, QE_DEBUG_VERIFY_PATH = 1, 2, 3, 4
 QE_DEBUG_EXPIRE_PAGES_WAIT = 5
@@ -87,8 +88,8 @@ _lib: Optional[ctypes.CDLL] = None
 
 
 def __getattr__(name: str):
-    """PagePool, PageTable and Rope (the paged cache) import torch, so they are loaded when first asked for."""
-    if name in ("PagePool", "PageTable", "Rope"):
+    """PagePool, PageTable, Rope and QE_PAGES_DROPPED (the paged cache) import torch, so they are loaded when first asked for."""
+    if name in ("PagePool", "PageTable", "Rope", "QE_PAGES_DROPPED"):
         from . import paged
         return getattr(paged, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
@@ -137,6 +138,10 @@ def load_library() -> ctypes.CDLL:
         "qe_pages_append": ([P, I, P, P, P, P], I),
         "qe_pages_attend": ([P, I, P, P, P, P, S, P], I),
         "qe_pages_attend_workspace": ([P, P, P], I),
+        "qe_pages_attend_window": ([P, I, P, P, P, I, I, P, S, P], I),
+        "qe_pages_attend_shared": ([P, I, P, P, P, P, P, S, P], I),
+        "qe_pages_attend_shared_workspace": ([P, P], I),
+        "qe_pages_drop": ([P, P, P, I, I, I, P], I),
         "qe_pages_resize": ([P, P, P, P, I, P, S, P], I),
         "qe_pages_fork": ([P, P, P, P, I, P, S, P], I),
         "qe_pages_compact": ([P, P, P, P, P, P, S, P], I),

@@ -50,19 +50,8 @@ constexpr int APPEND_DEEP = 3;     // rows that a thread loads at a time (2: 68.
 // Tokens that a block takes at a time, times head_dim: 4 of 128 channels or 8 of 64, so that a thread has one angle at most.
 constexpr int APPEND_CHANNELS = 2 * APPEND_THREADS;
 
-// Which sequence token tok belongs to: how many of q_start[1 ..] are at or below it.  A warp looks at 32 of them at a time.
-__device__ __forceinline__ int pages_find_seq(const ChunksView& c, int tok) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = c.n;
-  while (lo < hi) {
-    const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
-    const int k = __popc(__ballot_sync(~0u, i < hi && c.q_start[i + 1] <= tok));
-    if (step == 1) return lo + k;
-    hi = min(hi, lo + k * step);
-    lo = k > 0 ? lo + (k - 1) * step + 1 : hi;
-  }
-  return lo;
-}
+// which sequence token tok belongs to (by a warp)
+__device__ __forceinline__ int pages_find_seq(const ChunksView& c, int tok) { return pages_count_below(c.q_start + 1, c.n, tok); }
 
 // A block rotates and stores its share of the packed tokens, a few at a time.  The angle of (token, pair) is taken once
 // for all heads: position * turn mod 2^64 is the exact fraction of a turn (64-bit integers wrap at
@@ -343,6 +332,7 @@ __device__ void plan_moves(const PagesView& pg, const TableView& t, const int* a
 }
 
 __device__ __forceinline__ void ref_down(const PagesView& pg, int* refs, int page) {
+  if (page == QE_PAGES_DROPPED) return;   // given back already
   if (page < 0 || page >= pg.P) {
     pages_report(pg, QE_PAGES_ERR_PAGE);
     return;
@@ -438,7 +428,7 @@ __device__ void apply_moves(const PagesView& pg, const TableView& t, int n, cons
         if (j < full) {
           e = from[j];
           if (e >= 0 && e < pg.P) atomicAdd(&t.refs[e], 1);
-          else {
+          else if (e != QE_PAGES_DROPPED) {
             e = -1;
             pages_report(pg, QE_PAGES_ERR_PAGE);
           }
@@ -588,6 +578,31 @@ cudaError_t launch_pages_compact(const PagesView& pg, const TableView& t, int* t
   plan_layout(ws, pg.P, t.rows, 0, &s);
   const cudaError_t e = launch_after(pages_plan_compact_kernel, 1, PLAN_THREADS, st, pg, t, s, n_live);
   return e != cudaSuccess ? e : launch_after(pages_compact_kernel, n_sm * 8, 256, st, pg, t, s, table_out, refs_out);
+}
+
+// ---------------------------------------------------------------------------- drop
+// A warp takes DROP_ENTRIES table entries of a row at a time.  Bound by its launch: what it moves is four bytes for each page of the rows,
+// and twice that for a page that goes.
+constexpr int DROP_ENTRIES = 256;
+__global__ void __launch_bounds__(256) pages_drop_kernel(const PagesView pg, const TableView t, const int* rows, int n, const PagesWindow w) {
+  griddep_wait();
+  const int lane = threadIdx.x & 31, parts = (t.cols + DROP_ENTRIES - 1) / DROP_ENTRIES;
+  const int first = (int)(((long long)w.sinks + pg.S - 1) >> pg.lgS);
+  const long long units = (long long)n * parts;
+  for (long long u = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += (long long)gridDim.x * 8) {
+    const int i = (int)(u / parts), part = (int)(u - (long long)i * parts), row = rows[i];
+    const int len = row_len(pg, t, row, part == 0 && lane == 0);
+    const int end = min((max(len - w.window + 1, 0) >> pg.lgS), (part + 1) * DROP_ENTRIES);
+    if (len == 0) continue;
+    int* entry = t.table + (long long)row * t.stride;
+    for (int j = max(first, part * DROP_ENTRIES) + lane; j < end; j += 32)
+      // (exchanged: another entry of the call may name the row too)
+      if (entry[j] != QE_PAGES_DROPPED) ref_down(pg, t.refs, atomicExch(&entry[j], QE_PAGES_DROPPED));
+  }
+}
+cudaError_t launch_pages_drop(const PagesView& pg, const TableView& t, const int* rows, int n, const PagesWindow& w, int n_sm, cudaStream_t st) {
+  const long long blocks = ((long long)n * ((t.cols + DROP_ENTRIES - 1) / DROP_ENTRIES) + 7) / 8;
+  return launch_after(pages_drop_kernel, (unsigned)(blocks < n_sm * 8 ? blocks : n_sm * 8), 256, st, pg, t, rows, n, w);
 }
 
 // ---------------------------------------------------------------------------- copy, gather

@@ -58,6 +58,16 @@ struct PagesAttendParams {
   float scale;
 };
 
+// what the attention with a window or with shared prefixes has besides
+struct PagesWindow {
+  int window, sinks;          // 1 .. 2^30, 0 .. 2^30
+};
+struct PagesGroups {
+  const int* start;
+  const int* prefix;
+  int n, max_len;
+};
+
 // what a planned resize or fork does to one row (written by the planning kernel)
 struct PagesRowMove {
   int row, src;          // row changed; fork: source row, else -1.  row < 0: nothing
@@ -73,6 +83,9 @@ cudaError_t launch_pages_append(const PagesAppendParams& p, int fp16, int n_sm, 
 cudaError_t launch_pages_attend(const PagesAttendParams& p, int fp16, int device, int n_sm, void* ws, cudaStream_t st);
 size_t pages_attend_bytes(int n_sm, int D);
 bool pages_attend_cuts(const PagesView& pg, const TableView& t);   // whether any row of the table may be cut (and needs workspace)
+cudaError_t launch_pages_attend_window(const PagesAttendParams& p, const PagesWindow& w, int fp16, int device, int n_sm, void* ws, cudaStream_t st);
+cudaError_t launch_pages_attend_shared(const PagesAttendParams& p, const PagesGroups& g, int fp16, int device, int n_sm, void* ws, cudaStream_t st);
+cudaError_t launch_pages_drop(const PagesView& pg, const TableView& t, const int* rows, int n, const PagesWindow& w, int n_sm, cudaStream_t st);
 cudaError_t launch_pages_resize(const PagesView& pg, const TableView& t, const int* rows, const int* new_len, int n, void* ws,
                                 int n_sm, cudaStream_t st);
 cudaError_t launch_pages_fork(const PagesView& pg, const TableView& t, const int* src, const int* dst, int n, void* ws,
@@ -139,6 +152,20 @@ __device__ __forceinline__ void check_starts(const PagesView& pg, const ChunksVi
     bad |= a < 0 || b < a || b > c.total;
   }
   if (bad) pages_report(pg, QE_PAGES_ERR_ROW);
+}
+
+// How many of x[0 .. n) are at or below v, where they do not decrease.  A warp looks at 32 of them at a time.
+__device__ __forceinline__ int pages_count_below(const int* x, int n, int v) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
+    const int k = __popc(__ballot_sync(~0u, i < hi && x[i] <= v));
+    if (step == 1) return lo + k;
+    hi = min(hi, lo + k * step);
+    lo = k > 0 ? lo + (k - 1) * step + 1 : hi;
+  }
+  return lo;
 }
 
 // page of position pos of a row, or -1 (reported) when the table names none

@@ -142,6 +142,61 @@ qe_status check_workspace(const void* ws, size_t bytes, size_t need) {
 
 qe_status launched(cudaError_t e, const char* what) { return e == cudaSuccess ? QE_OK : cuda_fail(e, what); }
 
+// the arguments that every attention has; *some is false where there is nothing to do
+qe_status attend_params(const qe_pages* pages, int layer, const qe_page_table* seqs, const qe_chunks* chunks, const qe_pages_attend_args* a,
+                        qe::PagesAttendParams* o, bool* some) {
+  qe::PagesAttendParams& p = *o;
+  *some = false;
+  QE_TRY(check_pages(pages, &p.pg));
+  QE_TRY(check_layer(pages, layer));
+  QE_TRY(check_table(seqs, false, &p.t));
+  QE_TRY(check_chunks(chunks, &p.c));
+  if (!a) return fail(QE_ERR_INVALID_ARG, "args is null");
+  if (a->n_q_heads < 1 || a->n_q_heads % p.pg.H || a->n_q_heads / p.pg.H > 128)
+    return fail(QE_ERR_INVALID_ARG, "n_q_heads must be a multiple of n_kv_heads, at most 128 per KV head");
+  if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return fail(QE_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (a->max_q_len < 0) return fail(QE_ERR_INVALID_ARG, "max_q_len must be >= 0");
+  if (p.c.n == 0 || p.c.total == 0) return QE_OK;
+  QE_TRY(check_rows("q", a->q, a->q_token_stride, a->q_head_stride, p.c.total, a->n_q_heads, p.pg.D));
+  QE_TRY(check_rows("out", a->out, a->out_token_stride, a->out_head_stride, p.c.total, a->n_q_heads, p.pg.D));
+  if (misaligned(a->lse, 4)) return fail(QE_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+  p.q = static_cast<const uint16_t*>(a->q);
+  p.out = static_cast<uint16_t*>(a->out);
+  p.lse = a->lse;
+  p.qts = a->q_token_stride;
+  p.qhs = a->q_head_stride;
+  p.ots = a->out_token_stride;
+  p.ohs = a->out_head_stride;
+  p.layer = layer;
+  p.Hq = a->n_q_heads;
+  p.causal = a->causal != 0;
+  p.max_q_len = a->max_q_len;
+  p.scale = a->scale;
+  *some = true;
+  return QE_OK;
+}
+
+// need: bytes of workspace for so many SMs; launch: with their number
+template <class Need, class Launch>
+qe_status attend_launch(const char* name, const qe_pages* pages, qe::PagesAttendParams& p, void* workspace, size_t bytes, Need need, Launch launch) {
+  int n_sm = 0;
+  QE_TRY(sm_count(pages->device, &n_sm));
+  if (const size_t n = need(n_sm)) QE_TRY(check_workspace(workspace, bytes, n));
+  p.expire = qe::take_pages_expire();
+  DeviceGuard guard(pages->device);
+  if (guard.err != cudaSuccess) return cuda_fail(guard.err, "cudaSetDevice");
+  return launched(launch(n_sm), name);
+}
+
+size_t attend_need(const qe::PagesAttendParams& p, int n_sm) { return qe::pages_attend_cuts(p.pg, p.t) ? qe::pages_attend_bytes(n_sm, p.pg.D) : 0; }
+
+qe_status check_window(int window, int sinks, qe::PagesWindow* o) {
+  if (window < 1 || sinks < 0) return fail(QE_ERR_INVALID_ARG, "window must be >= 1 and sinks >= 0");
+  constexpr int MOST = 1 << 30;   // (a row holds no more tokens)
+  *o = qe::PagesWindow{window < MOST ? window : MOST, sinks < MOST ? sinks : MOST};
+  return QE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -227,39 +282,80 @@ qe_status qe_pages_attend(const qe_pages* pages, int layer, const qe_page_table*
                           const qe_pages_attend_args* a, void* workspace, size_t bytes, void* stream) {
   qe::NvtxRange nvtx_("qe_pages_attend");
   qe::PagesAttendParams p{};
-  QE_TRY(check_pages(pages, &p.pg));
-  QE_TRY(check_layer(pages, layer));
-  QE_TRY(check_table(seqs, false, &p.t));
-  QE_TRY(check_chunks(chunks, &p.c));
-  if (!a) return fail(QE_ERR_INVALID_ARG, "args is null");
-  if (a->n_q_heads < 1 || a->n_q_heads % p.pg.H || a->n_q_heads / p.pg.H > 128)
-    return fail(QE_ERR_INVALID_ARG, "n_q_heads must be a multiple of n_kv_heads, at most 128 per KV head");
-  if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return fail(QE_ERR_INVALID_ARG, "scale must be positive and finite");
-  if (a->max_q_len < 0) return fail(QE_ERR_INVALID_ARG, "max_q_len must be >= 0");
-  if (p.c.n == 0 || p.c.total == 0) return QE_OK;
-  QE_TRY(check_rows("q", a->q, a->q_token_stride, a->q_head_stride, p.c.total, a->n_q_heads, p.pg.D));
-  QE_TRY(check_rows("out", a->out, a->out_token_stride, a->out_head_stride, p.c.total, a->n_q_heads, p.pg.D));
-  if (misaligned(a->lse, 4)) return fail(QE_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+  bool some;
+  QE_TRY(attend_params(pages, layer, seqs, chunks, a, &p, &some));
+  if (!some) return QE_OK;
+  return attend_launch("qe_pages_attend", pages, p, workspace, bytes, [&](int n_sm) { return attend_need(p, n_sm); }, [&](int n_sm) {
+    return qe::launch_pages_attend(p, pages->dtype == QE_DTYPE_FP16, pages->device, n_sm, workspace, static_cast<cudaStream_t>(stream));
+  });
+}
+
+qe_status qe_pages_attend_window(const qe_pages* pages, int layer, const qe_page_table* seqs, const qe_chunks* chunks,
+                                 const qe_pages_attend_args* a, int window, int sinks, void* workspace, size_t bytes, void* stream) {
+  qe::NvtxRange nvtx_("qe_pages_attend_window");
+  qe::PagesAttendParams p{};
+  qe::PagesWindow w{};
+  bool some;
+  QE_TRY(attend_params(pages, layer, seqs, chunks, a, &p, &some));
+  QE_TRY(check_window(window, sinks, &w));
+  if (!a->causal) return fail(QE_ERR_INVALID_ARG, "a window needs causal attention");
+  if (!some) return QE_OK;
+  return attend_launch("qe_pages_attend_window", pages, p, workspace, bytes, [&](int n_sm) { return attend_need(p, n_sm); }, [&](int n_sm) {
+    return qe::launch_pages_attend_window(p, w, pages->dtype == QE_DTYPE_FP16, pages->device, n_sm, workspace, static_cast<cudaStream_t>(stream));
+  });
+}
+
+qe_status qe_pages_attend_shared_workspace(const qe_pages* pages, size_t* bytes) {
+  qe::PagesView pg{};
+  QE_TRY(check_pages(pages, &pg));
+  if (!bytes) return fail(QE_ERR_INVALID_ARG, "bytes is null");
   int n_sm = 0;
   QE_TRY(sm_count(pages->device, &n_sm));
-  if (qe::pages_attend_cuts(p.pg, p.t)) QE_TRY(check_workspace(workspace, bytes, qe::pages_attend_bytes(n_sm, p.pg.D)));
-  p.q = static_cast<const uint16_t*>(a->q);
-  p.out = static_cast<uint16_t*>(a->out);
-  p.lse = a->lse;
-  p.qts = a->q_token_stride;
-  p.qhs = a->q_head_stride;
-  p.ots = a->out_token_stride;
-  p.ohs = a->out_head_stride;
-  p.layer = layer;
-  p.Hq = a->n_q_heads;
-  p.causal = a->causal != 0;
-  p.max_q_len = a->max_q_len;
-  p.scale = a->scale;
-  p.expire = qe::take_pages_expire();
+  *bytes = qe::pages_attend_bytes(n_sm, pg.D);
+  return QE_OK;
+}
+
+qe_status qe_pages_attend_shared(const qe_pages* pages, int layer, const qe_page_table* seqs, const qe_chunks* chunks,
+                                 const qe_pages_attend_args* a, const qe_groups* groups, void* workspace, size_t bytes, void* stream) {
+  qe::NvtxRange nvtx_("qe_pages_attend_shared");
+  qe::PagesAttendParams p{};
+  bool some;
+  QE_TRY(attend_params(pages, layer, seqs, chunks, a, &p, &some));
+  if (!groups) return fail(QE_ERR_INVALID_ARG, "groups is null");
+  if (groups->n_groups < 0 || groups->n_groups > 65536 || groups->max_group_len < 0)
+    return fail(QE_ERR_INVALID_ARG, "groups: n_groups must be 0 .. 65536 and max_group_len >= 0");
+  if (misaligned(groups->group_start, 4) || misaligned(groups->prefix_len, 4))
+    return fail(QE_ERR_INVALID_ARG, "groups: pointers must be 4-byte aligned");
+  if (!some) return QE_OK;
+  if (groups->n_groups == 0) return fail(QE_ERR_INVALID_ARG, "groups: the call's sequences are in no group");
+  if (!groups->group_start || !groups->prefix_len) return fail(QE_ERR_INVALID_ARG, "groups: null pointer");
+  // (the keys of a tile, a prefix and the own tokens of its sequences, are counted in 32 bits)
+  const int per = 256 * p.pg.H / p.Hq;
+  if (((long long)(p.c.n < per ? p.c.n : per) + 1) * p.t.cols * p.pg.S > 0x7FFFFFFF)
+    return fail(QE_ERR_INVALID_ARG,
+                "page table: too large for shared prefixes: (min(n_seqs, 256 n_kv_heads / n_q_heads) + 1) * max_pages * page_size must be below 2^31");
+  const qe::PagesGroups g{groups->group_start, groups->prefix_len, groups->n_groups, groups->max_group_len};
+  return attend_launch("qe_pages_attend_shared", pages, p, workspace, bytes, [&](int n_sm) { return qe::pages_attend_bytes(n_sm, p.pg.D); }, [&](int n_sm) {
+    return qe::launch_pages_attend_shared(p, g, pages->dtype == QE_DTYPE_FP16, pages->device, n_sm, workspace, static_cast<cudaStream_t>(stream));
+  });
+}
+
+qe_status qe_pages_drop(const qe_pages* pages, const qe_page_table* seqs, const int* rows, int n, int window, int sinks, void* stream) {
+  qe::NvtxRange nvtx_("qe_pages_drop");
+  qe::PagesView pg{};
+  qe::TableView t{};
+  qe::PagesWindow w{};
+  QE_TRY(check_pages(pages, &pg));
+  QE_TRY(check_table(seqs, true, &t));
+  QE_TRY(check_window(window, sinks, &w));
+  if (n < 0 || n > (1 << 24)) return fail(QE_ERR_INVALID_ARG, "n must be 0 .. 2^24");
+  if (n == 0) return QE_OK;
+  if (!rows || misaligned(rows, 4)) return fail(QE_ERR_INVALID_ARG, "rows must be non-null and 4-byte aligned");
   DeviceGuard guard(pages->device);
   if (guard.err != cudaSuccess) return cuda_fail(guard.err, "cudaSetDevice");
-  return launched(qe::launch_pages_attend(p, pages->dtype == QE_DTYPE_FP16, pages->device, n_sm, workspace, static_cast<cudaStream_t>(stream)),
-                  "qe_pages_attend");
+  int n_sm = 0;
+  QE_TRY(sm_count(pages->device, &n_sm));
+  return launched(qe::launch_pages_drop(pg, t, rows, n, w, n_sm, static_cast<cudaStream_t>(stream)), "qe_pages_drop");
 }
 
 qe_status qe_pages_manage_workspace(const qe_pages* pages, const qe_page_table* seqs, int n, size_t* bytes) {

@@ -8,7 +8,11 @@ and reference counts, ``Rope`` the rotary positions of several axes.  A serving 
         q = pool.append(layer, k, v, q_start, seqs, rows=rows, q=q, rope=rope, positions=positions)
         o = pool.attend(layer, q, q_start, seqs, rows=rows, max_q_len=longest)   # (the longest chunk, or 0 if it is not known)
 
-and ``pool.gather(layer, seqs, 0, n)`` gives keys and values in the layout ``QECache.qe_append`` takes: of a bf16 pool, for
+Forks that share a long prefix are attended together by ``attend_shared``.  With a sliding window (``attend(..., window=w,
+sinks=s)``, in every layer that keeps its keys in this table) ``pool.drop(seqs, rows, w, sinks=s)`` after the step gives back
+the pages that no later token sees.
+
+``pool.gather(layer, seqs, 0, n)`` gives keys and values in the layout ``QECache.qe_append`` takes: of a bf16 pool, for
 rows that all have n tokens (shorter ones are filled up with zeros), and for a cache with ``rope_theta`` 0 (``append`` stores rotated keys).
 Nothing here carries a gradient: tensors are read and written by address, whatever autograd would record.
 
@@ -29,6 +33,7 @@ import torch
 from . import QE_ERR_DEVICE, QE_ERR_INVALID_ARG, QEError, load_library
 
 QE_PAGES_ERR_PAGE, QE_PAGES_ERR_ROW, QE_PAGES_ERR_NO_PAGES, QE_PAGES_ERR_TIMEOUT = 1, 2, 4, 8
+QE_PAGES_DROPPED = -2
 
 _P, _I, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
 _I32, _DENSE = torch.int32, torch.contiguous_format
@@ -49,11 +54,12 @@ class _Rope(ctypes.Structure):
     _fields_ = [("rot_dim", _I), ("halves", _I), ("n_axes", _I), ("axis", ctypes.c_byte * 64), ("inv_freq", ctypes.c_double * 64)]
 
 
-# qe_chunks, qe_pages_append_args and qe_pages_attend_args, packed call by call (native sizes and alignment; a ctypes
+# qe_chunks, qe_pages_append_args, qe_pages_attend_args and qe_groups, packed call by call (native sizes and alignment; a ctypes
 # structure costs three times as much to fill)
 _CHUNKS = struct.Struct("@PPii0P")
 _APPEND = struct.Struct("@PPqqqqPPqqqqiPPq0P")
 _ATTEND = struct.Struct("@PPPqqqqiiif0P")
+_GROUPS = struct.Struct("@PPii0P")
 
 try:   # the raw handle without a Stream object around it
     _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -159,13 +165,15 @@ class PagePool:
         if st:
             raise QEError(st, self._lib.qe_last_error(None).decode())
 
-    def _need(self, seqs: PageTable, n: int) -> int:
-        """Bytes of workspace of attend (n < 0) or of managing n entries, with tables of this shape."""
-        key = (seqs._shape, n)
+    def _need(self, seqs: Optional[PageTable], n: int) -> int:
+        """Bytes of workspace of attend (n < 0; of attend_shared without a table) or of managing n entries, with tables of this shape."""
+        key = (seqs._shape if seqs is not None else None, n)
         need = self._bytes.get(key)
         if need is None:
             b = ctypes.c_size_t()
-            if n < 0:
+            if seqs is None:
+                self._check(self._lib.qe_pages_attend_shared_workspace(self._ref, ctypes.byref(b)))
+            elif n < 0:
                 self._check(self._lib.qe_pages_attend_workspace(self._ref, seqs._ref, ctypes.byref(b)))
             else:
                 self._check(self._lib.qe_pages_manage_workspace(self._ref, seqs._ref, n, ctypes.byref(b)))
@@ -261,11 +269,8 @@ class PagePool:
             self._check(st)
         return q_out
 
-    def attend(self, layer: int, q: torch.Tensor, q_start: torch.Tensor, seqs: PageTable, *, rows: Optional[torch.Tensor] = None,
-               scale: Optional[float] = None, causal: bool = True, max_q_len: int = 0, out: Optional[torch.Tensor] = None,
-               return_lse: bool = False):
-        """qe_pages_attend: q [total][n_q_heads][head_dim] over the rows' cached tokens; returns out, or (out, lse
-        [total][n_q_heads] float32) with return_lse.  scale defaults to head_dim ** -0.5."""
+    def _attend(self, q, q_start, seqs, rows, scale, causal, hint, name, out, return_lse):
+        """Checks what every attention takes; (out, lse, page table, chunks, args)."""
         total, hq = q.shape[:2] if q.dim() == 3 else (0, 0)
         qs = self._tokens("q", q, total, hq)
         if out is None:
@@ -275,17 +280,62 @@ class PagePool:
             os = self._tokens("out", out, total, hq)
         lse = torch.empty(total, hq, dtype=torch.float32, device=self.device) if return_lse else None
         ref, c = self._seqs(seqs), self._chunks(q_start, rows, total)
-        if not 0 <= max_q_len < 2 ** 31:
-            raise _bad(f"max_q_len {max_q_len} out of range")
+        if not 0 <= hint < 2 ** 31:
+            raise _bad(f"{name} {hint} out of range")
         a = _ATTEND.pack(q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else 0, qs[0], qs[1], os[0], os[1], hq,
-                         1 if causal else 0, max_q_len, self._scale if scale is None else scale)
+                         1 if causal else 0, hint, self._scale if scale is None else scale)
+        return out, lse, ref, c, a
+
+    def _window(self, window, sinks):
+        if not 1 <= window < 2 ** 31 or not 0 <= sinks < 2 ** 31:
+            raise _bad(f"window {window} or sinks {sinks} out of range")
+
+    def attend(self, layer: int, q: torch.Tensor, q_start: torch.Tensor, seqs: PageTable, *, rows: Optional[torch.Tensor] = None,
+               scale: Optional[float] = None, causal: bool = True, max_q_len: int = 0, out: Optional[torch.Tensor] = None,
+               return_lse: bool = False, window: Optional[int] = None, sinks: int = 0):
+        """qe_pages_attend: q [total][n_q_heads][head_dim] over the rows' cached tokens; returns out, or (out, lse
+        [total][n_q_heads] float32) with return_lse.  scale defaults to head_dim ** -0.5.
+
+        With a window, qe_pages_attend_window: a token sees itself and the window - 1 tokens before it, and the row's first
+        `sinks` tokens; pages that this leaves out may have been dropped."""
+        out, lse, ref, c, a = self._attend(q, q_start, seqs, rows, scale, causal, max_q_len, "max_q_len", out, return_lse)
+        if window is not None:
+            self._window(window, sinks)
+            a = (a, window, sinks)
+            fn = self._lib.qe_pages_attend_window
+        elif sinks:
+            raise _bad("sinks without a window")
+        else:
+            a = (a,)
+            fn = self._lib.qe_pages_attend
         need, stream, layer = self._need(seqs, -1), _raw_stream(self._index), self._layer(layer)
         if need:
             with self._lock:
                 ws = self._scratch(need, stream)
-                st = self._lib.qe_pages_attend(self._ref, layer, ref, c, a, ws.data_ptr(), need, stream)
+                st = fn(self._ref, layer, ref, c, *a, ws.data_ptr(), need, stream)
         else:
-            st = self._lib.qe_pages_attend(self._ref, layer, ref, c, a, None, 0, stream)
+            st = fn(self._ref, layer, ref, c, *a, None, 0, stream)
+        if st:
+            self._check(st)
+        return (out, lse) if return_lse else out
+
+    def attend_shared(self, layer: int, q: torch.Tensor, q_start: torch.Tensor, seqs: PageTable, group_start: torch.Tensor,
+                      prefix_len: torch.Tensor, *, rows: Optional[torch.Tensor] = None, scale: Optional[float] = None, causal: bool = True,
+                      max_group_len: int = 0, out: Optional[torch.Tensor] = None, return_lse: bool = False):
+        """qe_pages_attend_shared: attend for sequences that share prefixes (forks), each read once for its group.
+
+        group_start int32 [n_groups + 1]: group g is the call's sequences group_start[g] .. group_start[g + 1] - 1; prefix_len
+        int32 [n_groups]: their first tokens, in the pages of the group's first sequence.  max_group_len: the most packed tokens
+        of a group, or 0 if it is not known."""
+        out, lse, ref, c, a = self._attend(q, q_start, seqs, rows, scale, causal, max_group_len, "max_group_len", out, return_lse)
+        n = _ints("prefix_len", prefix_len, self._index)
+        if _ints("group_start", group_start, self._index) != n + 1:
+            raise _bad("group_start must have one entry more than prefix_len")
+        g = _GROUPS.pack(group_start.data_ptr(), prefix_len.data_ptr(), n, max_group_len)
+        need, stream, layer = self._need(None, -1), _raw_stream(self._index), self._layer(layer)
+        with self._lock:
+            ws = self._scratch(need, stream)
+            st = self._lib.qe_pages_attend_shared(self._ref, layer, ref, c, a, g, ws.data_ptr(), need, stream)
         if st:
             self._check(st)
         return (out, lse) if return_lse else out
@@ -319,6 +369,15 @@ class PagePool:
     def fork(self, seqs: PageTable, src: torch.Tensor, dst: torch.Tensor):
         """qe_pages_fork: empty row dst[i] becomes a copy of row src[i], sharing its full pages."""
         self._manage(self._lib.qe_pages_fork, seqs, src, dst, ("src", "dst"))
+
+    def drop(self, seqs: PageTable, rows: torch.Tensor, window: int, *, sinks: int = 0):
+        """qe_pages_drop: the rows give back the pages that no later token sees under this window (behind the first `sinks`
+        tokens and before kv_len - window + 1); their table entries become QE_PAGES_DROPPED."""
+        ref, n = self._refs(seqs), _ints("rows", rows, self._index)
+        self._window(window, sinks)
+        st = self._lib.qe_pages_drop(self._ref, ref, rows.data_ptr(), n, window, sinks, _raw_stream(self._index))
+        if st:
+            self._check(st)
 
     def compact(self, seqs: PageTable, *, table_out: Optional[torch.Tensor] = None, refs_out: Optional[torch.Tensor] = None,
                 n_live: Optional[torch.Tensor] = None):
