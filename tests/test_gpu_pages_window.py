@@ -123,6 +123,21 @@ def test_rows_whose_first_block_is_hidden(torch, m, hint, dtype):
         run(torch, [(m, 512 + extra)], 100, 0, hq=2, hkv=1, d=64, ps=16, dtype=dtype, hint=hint, scale=1.0, edit=far, seed=extra)
 
 
+def test_equals_plain_attention_where_the_window_holds_all(torch):
+    """A window as long as the rows gives bit for bit what attention without one does."""
+    import tiered_quantize_evict_gb300 as qe
+    c = Case(torch, [700, 129, 1], hkv=2, d=64, ps=32)
+    pool, seqs = c.objects(qe)
+    for chunks, hint in (([1, 1, 1], 1), ([30, 12, 1], 30), ([200, 129, 1], 0)):
+        starts = c.ints(np.cumsum([0] + chunks))
+        q = c.draw(sum(chunks), 8, 64).to(c.dev)
+        a = pool.attend(0, q, starts, seqs, max_q_len=hint, return_lse=True)
+        b = pool.attend(0, q, starts, seqs, max_q_len=hint, return_lse=True, window=700, sinks=5)
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+    pool.check()
+
+
 def test_visible_pages_that_are_gone_are_reported(torch):
     """A dropped or bad page inside the window counts as zeros and is reported; outside of it nothing is."""
     import tiered_quantize_evict_gb300 as qe

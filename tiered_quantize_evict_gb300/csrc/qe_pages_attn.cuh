@@ -1,6 +1,6 @@
 // qe_pages_attn.cuh -- what the kernels of the chunk attention share: the line of blocks and its cuts, descriptors,
-// tensor-memory and TMA instructions, bounded waits.  The mathematics and the layout are in qe_pages_attn.cu; the kernel for a few query
-// rows is in qe_pages_few.cu.
+// tensor-memory and TMA instructions, bounded waits.  The mathematics and the layout are in qe_pages_halves.cuh; the kernel for a few query
+// rows is in qe_pages_few.cuh; what differs between windows, shared prefixes and neither is in qe_pages_walk.cuh.
 #pragma once
 #include <climits>
 #include <cstring>
@@ -27,9 +27,13 @@ constexpr float PA_UP = FP16 ? 7.f : 0.f;
 template <bool FP16>
 constexpr float PA_DOWN = FP16 ? 0x1p-7f : 1.f;  // 2^-PA_UP
 
+// Which keys the rows see (and what of a kernel is compiled for them): all up to their own; those of a sliding window and the sinks;
+// a prefix that a group of sequences shares, and their own.
+enum PaMode { PA_PLAIN, PA_WINDOW, PA_SHARED };
+
 // what a CTA's piece of the line starts with (read by the join kernel)
 struct PaRec {
-  long long begin;     // place of the tile on the line; -1: no piece
+  long long begin;     // tells the tile (its place on the line, or a number of its own); -1: no piece
   int b;               // block of the tile that the piece starts with
   int tok, ntok;       // the tile's first packed token, and how many
   int kvh;
@@ -49,6 +53,10 @@ struct PaParams {
   int expire;              // qe_debug_inject: 4 k + role, the k-th counted wait of these warps is taken as expired; 0: none
   float scale, scale2;     // of the logits; and times log2(e)
   PaRec* rec;              // [CTAs]; NULL: no tile is cut
+  int items;               // what the line is made of: sequences, or groups of them
+  PagesWindow win;         // window: length, sinks,
+  int sa;                  // and the sinks' whole pieces of pages in tokens
+  PagesGroups gr;          // shared prefixes
   float2* part_ml;         // [CTAs][2][NH][128]: reference, sum
   float* part_o;           // [CTAs][2][NH][D / 4][128][4]
 };
@@ -96,23 +104,53 @@ __device__ __forceinline__ PaSeq pa_seq(const PaParams& p, int i, bool report) {
   r.tiles = (r.s.m + tt - 1) / tt;
   return r;
 }
-// A tile is NH T tokens of a sequence and one KV head.  Its blocks (at least one, so that rows without keys are written too)
+// A tile is NH T tokens of a sequence and one KV head.
+//
+// Under a window the keys that a tile's rows see are the sinks [0, sinks) and [lo, end), lo the first row's window's begin.  The tile
+// counts them without the gap: key v of the tile is key v below sa (the sinks in whole pieces of pages), then v + shift, with shift a multiple
+// of the pieces and sa + shift at or below lo; so sinks and window have their blocks together (1024 keys, 4 sinks, pages of 16, tiles of
+// 64 tokens: 9 blocks, where blocks at multiples of 128 and one for the sinks make 10.5).
+__device__ __forceinline__ int pa_piece(const PaParams& p) { return min(p.pg.S, PA_BN); }   // tokens of a piece of a page
 template <int NH>
+__device__ __forceinline__ int pa_shift(const PaParams& p, const SeqInfo& s, int j) {
+  const int lo = s.len - s.m + j * NH * p.T - p.win.window + 1;
+  return lo >= p.sa ? (lo & -pa_piece(p)) - p.sa : 0;
+}
+// blocks of a tile of so many keys of a window that begins at `lo` (but for whole pieces), with the sinks
+template <int NH>
+__device__ __forceinline__ int pa_window_blocks(const PaParams& p, int lo) {
+  // (where tiles are no multiple of the pieces the window's begin falls anywhere in one: room for the most)
+  const int piece = pa_piece(p), into = NH * p.T % piece == 0 ? lo & (piece - 1) : piece - 1;
+  return (p.sa + into + p.win.window - 1 + NH * p.T + PA_BN - 1) >> 7;
+}
+// Its blocks (at least one, so that rows without keys are written too)
+template <int NH, int MODE>
 __device__ __forceinline__ int pa_blocks(const PaParams& p, const SeqInfo& s, int j) {
   const int end = p.causal ? s.len - s.m + min(s.m, (j + 1) * NH * p.T) : s.len;
+  if constexpr (MODE == PA_WINDOW) {
+    const int shift = pa_shift<NH>(p, s, j);
+    if (shift > 0) return (j + 1) * NH * p.T <= s.m ? pa_window_blocks<NH>(p, s.len - s.m - p.win.window + 1) : (end - shift + PA_BN - 1) >> 7;
+  }
   return max(1, (end + PA_BN - 1) >> 7);
 }
 // length on the line of the tiles before tile j (j < tiles: those are all whole)
-template <int NH>
+template <int NH, int MODE>
 __device__ __forceinline__ long long pa_before(const PaParams& p, const SeqInfo& s, int j) {
   if (!p.causal || j == 0) return (long long)j * (PA_TILE_COST + max(1, (s.len + PA_BN - 1) >> 7));
   const int tt = NH * p.T, off = s.len - s.m;
+  if constexpr (MODE == PA_WINDOW) {
+    const long long far = (long long)p.sa + pa_piece(p) + p.win.window - 1 - off;   // a tile that begins so far behind the first has a shift
+    if (far <= (long long)(j - 1) * tt) {
+      const int some = far <= 0 ? 0 : (int)((unsigned)(far + tt - 1) / (unsigned)tt);
+      return pa_before<NH, PA_PLAIN>(p, s, some) + (long long)(j - some) * (PA_TILE_COST + pa_window_blocks<NH>(p, off - p.win.window + 1));
+    }
+  }
   const int none = off < 0 ? min(j, -off / tt) : 0;   // tiles that see no key
   return (long long)j * PA_TILE_COST + none + floor_sum128(j - none, tt, (long long)off + (long long)(none + 1) * tt + PA_BN - 1);
 }
-template <int NH>
+template <int NH, int MODE>
 __device__ __forceinline__ long long pa_head_length(const PaParams& p, const PaSeq& q) {
-  return q.tiles == 0 ? 0 : pa_before<NH>(p, q.s, q.tiles - 1) + PA_TILE_COST + pa_blocks<NH>(p, q.s, q.tiles - 1);
+  return q.tiles == 0 ? 0 : pa_before<NH, MODE>(p, q.s, q.tiles - 1) + PA_TILE_COST + pa_blocks<NH, MODE>(p, q.s, q.tiles - 1);
 }
 
 // A place on the line: sequence, KV head, tile, block.  The end of the line is (n, 0, 0, 0).
@@ -123,7 +161,7 @@ struct PaPlace {
 };
 
 // A walk from one place to another, tile by tile.
-template <int NH>
+template <int NH, int MODE>
 struct PaCursor {
   int i, h, j, b, nb;   // the place; blocks of the tile
   PaSeq q;
@@ -139,7 +177,7 @@ struct PaCursor {
     eb = pl[1].b;
     q.s = pl[0].s;
     q.tiles = (q.s.m + NH * p.T - 1) / (NH * p.T);
-    nb = pa_blocks<NH>(p, q.s, j);
+    nb = pa_blocks<NH, MODE>(p, q.s, j);
   }
   // blocks left of the tile on this walk; 0: the walk is over
   __device__ __forceinline__ bool last_tile() const { return i == ei && h == eh && j == ej; }
@@ -163,15 +201,23 @@ struct PaCursor {
         } while (q.tiles == 0);
       }
     }
-    nb = pa_blocks<NH>(p, q.s, j);
+    nb = pa_blocks<NH, MODE>(p, q.s, j);
   }
   __device__ __forceinline__ bool second_half(const PaParams& p) const { return NH == 2 && j * 2 * p.T + p.T < q.s.m; }
+  __device__ __forceinline__ int head() const { return h; }
+  __device__ __forceinline__ int tok(const PaParams& p) const { return q.s.q0 + j * NH * p.T; }              // the tile's first packed token
+  __device__ __forceinline__ int tokens(const PaParams& p) const { return min(NH * p.T, q.s.m - j * NH * p.T); }
+  // Key v of the tile in the cache.  shift: of the tile (window)
+  __device__ __forceinline__ int shift(const PaParams& p) const {
+    if constexpr (MODE == PA_WINDOW) return pa_shift<NH>(p, q.s, j);
+    return 0;
+  }
 };
 
 // Every CTA (of NT threads) finds its piece: sums the sequences' lengths on the line, cuts it, finds the places of its two cuts.  Up
 // to 32 sequences are a warp's work: two warps do it, one for each cut, without barriers in between (one token over a short cache, the
 // whole call: 9.7 -> 9.2 us).
-template <int NH, int NT>
+template <int NH, int NT, int MODE>
 __device__ __noinline__ void pa_find(const PaParams& p, PaPlace* pl, long long* s_w) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int W = NT / 32;
@@ -204,7 +250,7 @@ __device__ __noinline__ void pa_find(const PaParams& p, PaPlace* pl, long long* 
     if (i >= p.c.n) return 0ll;
     const PaSeq q = pa_seq<NH>(p, i, report);
     s = q.s;
-    return (head = pa_head_length<NH>(p, q)) * p.pg.H;
+    return (head = pa_head_length<NH, MODE>(p, q)) * p.pg.H;
   };
   // where the two cuts of piece c are on a line; false: there are not so many pieces
   long long cut[2];
@@ -281,7 +327,7 @@ __device__ __noinline__ void pa_find(const PaParams& p, PaPlace* pl, long long* 
     long long before = 0;
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32, cand = lo + lane * step;
-      const long long at = cand < hi ? pa_before<NH>(p, q.s, cand) : LLONG_MAX;
+      const long long at = cand < hi ? pa_before<NH, MODE>(p, q.s, cand) : LLONG_MAX;
       const int top = 31 - __clz(__ballot_sync(~0u, at <= rem));
       before = __shfl_sync(~0u, at, top);
       lo += top * step;
@@ -289,7 +335,7 @@ __device__ __noinline__ void pa_find(const PaParams& p, PaPlace* pl, long long* 
     }
     rem -= before;
     // a cut in what the tile costs besides, or in a short tile, is one before the tile
-    const int b = pa_blocks<NH>(p, q.s, lo) <= PA_WHOLE ? 0 : max(0, (int)rem - PA_TILE_COST);
+    const int b = pa_blocks<NH, MODE>(p, q.s, lo) <= PA_WHOLE ? 0 : max(0, (int)rem - PA_TILE_COST);
     if (lane == 0) {
       pl[warp].h = h;
       pl[warp].j = lo;
@@ -454,10 +500,9 @@ __device__ __forceinline__ float2 pa_unpack(unsigned x) {
 constexpr unsigned long long PA_DESC_K = (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 constexpr unsigned long long PA_DESC_V = (1024ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 
-// Attention of tiles of at most 16 rows (qe_pages_few.cu).  With 17 to 32 rows as 32 columns it took 148 us where the one half of
-// qe_pages_attn.cu takes 134 (8 drafts of 16 sequences of up to 16K tokens), so those stay there.
+// Attention of tiles of at most 16 rows (qe_pages_few.cuh).  With 17 to 32 rows as 32 columns it took 148 us where the one half of
+// qe_pages_halves.cuh takes 134 (8 drafts of 16 sequences of up to 16K tokens), so those stay there.
 constexpr int PAGES_FEW_ROWS = 16;
-cudaError_t launch_pages_few(const PaParams& p, const CUtensorMap* maps, int fp16, int device, cudaStream_t st);
 cudaError_t launch_pages_join(const PaParams& p, int nh, int fp16, cudaStream_t st);
 
 }  // namespace qe

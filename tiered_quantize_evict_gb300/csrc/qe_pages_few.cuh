@@ -1,9 +1,9 @@
-// qe_pages_few.cu -- attention over the cached pages for tiles of at most 16 query rows (decode steps, a few drafts).
+// qe_pages_few.cuh -- attention over the cached pages for tiles of at most 16 query rows (decode steps, a few drafts).
 //
 // Bound by reading the cache, so everything else has to fit under it: the products are taken the other way round, keys (then
 // channels) as the 128 rows of the tensor cores and the few query rows as N = 16 columns:
 //   S^T = K Q^T (128 keys x N),   O^T += V^T P^T (head_dim channels x 2 N, keys inner),
-// with the formulas and the split of the line of qe_pages_attn.cu.  A block costs the tensor cores about 600 cycles instead of 1536,
+// with the formulas and the split of the line of qe_pages_halves.cuh.  A block costs the tensor cores about 600 cycles instead of 1536,
 // and a thread 16 exponentials instead of 64 whatever the rows (decode step of 16 sequences of up to 32K tokens: 302 -> 287 us with
 // 128 channels, 236 -> 171 us with 64).
 //  * P^T is written to shared memory in two parts per probability, rounded and remainder, as 2 N columns (about 17 significant bits
@@ -14,10 +14,9 @@
 //    warps otherwise).
 // CTA: warps 0-3 softmax, 4 TMA of keys and values, 5 tensor-core issue, 6 TMA of the queries, 7 tensor memory.
 // mbarriers: kfull / kempty per slot, qfull / qempty per query buffer, s[i] (S i complete), p[i] (P i written; one arrival per
-// softmax warp), o[i] (the P V of an even or odd block complete, as with NH = 1 there).  Waits are bounded as in qe_pages_attn.cu.
-#include <atomic>
-
-#include "qe_pages_attn.cuh"
+// softmax warp), o[i] (the P V of an even or odd block complete, as with NH = 1 there).  Waits are bounded as in qe_pages_halves.cuh.
+#pragma once
+#include "qe_pages_walk.cuh"
 
 namespace qe {
 
@@ -72,20 +71,22 @@ __device__ __forceinline__ bool pf_or(bool v) {
   return r != 0;
 }
 
-template <int D, bool FP16>
+template <int D, bool FP16, int MODE>
 __global__ void __launch_bounds__(PF_THREADS, 1)
     pages_few_kernel(const __grid_constant__ PaParams p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                      const __grid_constant__ CUtensorMap mv) {
   using Sh = PfShape<D>;
+  using Cursor = typename PaWalk<1, MODE>::Cursor;
   constexpr int NS = Sh::SLOTS, N = Sh::N;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) unsigned long long b_kfull[NS], b_kempty[NS], b_qfull[2], b_qempty[2], b_s[2], b_p[2], b_o[2], b_end;
   __shared__ unsigned s_tmem;
   __shared__ int s_abort;
-  __shared__ PaPlace s_place[2];
+  __shared__ typename PaWalk<1, MODE>::Place s_place[2];
   __shared__ long long s_w[PF_THREADS / 32];
   __shared__ __align__(16) float s_red[N][4];      // a column's value of each softmax warp
   __shared__ float s_inv[N];
+  __shared__ PaValid<MODE, NS> s_valid;
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0), aux = warp - 4;   // aux: TMA, tensor cores, queries, tensor memory
@@ -120,40 +121,37 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   pa_fence_before();
   griddep_wait();
   griddep_launch_dependents();   // (what follows may then rely on all that ran before this launch)
-  pa_find<1, PF_THREADS>(p, s_place, s_w);   // ends with a barrier
+  const bool work = PaWalk<1, MODE>::template find<PF_THREADS>(p, s_place, s_w);   // ends with a barrier
   pa_fence_after();
   const unsigned tm = s_tmem;
-  const bool work = s_place[0].i < p.c.n && (s_place[0].i != s_place[1].i || s_place[0].h != s_place[1].h || s_place[0].j != s_place[1].j ||
-                                             s_place[0].b != s_place[1].b);
 
   if (work && aux == 0) {
     // ============================== keys and values
-    PaCursor<1> cur;
+    Cursor cur;
     cur.set(p, s_place);
     const int rows = min(p.pg.S, PA_BN);               // tokens of a piece: a page, or a block's part of one
     const int np = PA_BN / rows;
     const int piece = lane % np, cb = lane / np;       // lane -> (page of the block, column block)
     const bool mine = cb < Sh::CB;
-    // the table's entry for this lane's piece (INT_MIN behind the sequence's end), loaded a block before it is looked at
-    auto entry = [&]() {
-      const int key = cur.b * PA_BN + piece * rows;
-      return key < cur.q.s.len ? p.t.table[(long long)cur.q.s.row * p.t.stride + (key >> p.pg.lgS)] : INT_MIN;
-    };
+    // this lane's piece, its entry loaded a block before it is looked at
+    typename PaWalk<1, MODE>::Keys keys;
     int slot = 0, ph = 1, issued = 0, left = cur.count();
-    int next = entry(), till = PaWait::counted(p, PaWait::KEYS);
+    PaPiece next = keys.at(p, cur, cur.b * PA_BN + piece * rows);
+    int till = PaWait::counted(p, PaWait::KEYS);
     bool ok = true;
 #pragma unroll 1
     while (left > 0 && ok) {
-      const int tk = (cur.b * PA_BN) & (p.pg.S - 1), h = cur.h;
-      const bool there = next >= 0 && next < p.pg.P;
-      const int now = there ? next : p.pg.P;             // out of the pool: the copy fills zeros
-      if (!there && next != INT_MIN) pages_report(p.pg, QE_PAGES_ERR_PAGE);
+      const int tk = next.tok, h = cur.h;
+      const bool there = next.entry >= 0 && next.entry < p.pg.P;
+      const int now = there ? next.entry : p.pg.P;       // out of the pool: the copy fills zeros
+      if (!there && next.entry != INT_MIN) pages_report(p.pg, QE_PAGES_ERR_PAGE);
+      const int valid = there ? next.valid : 255;
       ++cur.b;
       if (--left == 0) {
         cur.next_tile(p);
         left = cur.count();
       }
-      if (left > 0) next = entry();
+      if (left > 0) next = keys.at(p, cur, cur.b * PA_BN + piece * rows);
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
         ok = ok && wait.count(till, smem_u32(&b_kempty[slot]), ph);
@@ -162,6 +160,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           break;
         }
         const unsigned full = smem_u32(&b_kfull[slot]);
+        if constexpr (MODE == PA_SHARED) {   // (told by the values' arrival)
+          if (kv && lane < 8) s_valid.set(slot, lane, lane < np ? valid : 255);
+          __syncwarp();
+        }
         if (lane == 0) mbar_expect_tx(full, Sh::TILE);
         __syncwarp();
         if (mine) pa_tma4(sm_kv + slot * Sh::TILE + cb * 16384 + piece * rows * 128, kv ? &mv : &mk, cb * 64, tk, h, now, full);
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     constexpr unsigned FMT = FP16 ? 0u : (1u << 7) | (1u << 10);
     constexpr unsigned ID_S = (1u << 4) | FMT | (((unsigned)N >> 3) << 17) | ((128u >> 4) << 24);
     constexpr unsigned ID_O = (1u << 4) | FMT | (1u << 15) | (1u << 16) | ((2u * N >> 3) << 17) | (((unsigned)D >> 4) << 24);
-    PaCursor<1> cur;
+    Cursor cur;
     cur.set(p, s_place);
     // The ring is consumed in its order (K 0, V 0, K 1, ...), but S runs a block ahead: K n is used before V n - 1.
     int slot = 0, ph = 0, pp = 0, qp = 0, tile = 0, left = 0;   // (bit i of pp, qp: the parity of p[i], qfull[i])
@@ -248,33 +250,46 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     __syncwarp();
     wait.drain(smem_u32(&b_end), 0);
   } else if (work && aux == 2) {
-    // ============================== queries
-    if (lane == 0) {
-      PaCursor<1> cur;
-      cur.set(p, s_place);
-      PaFill fill[2];
-      int tile = 0, blocks = 0, till = PaWait::counted(p, PaWait::QUERIES);   // (blocks: of the tiles before)
-#pragma unroll 1
-      for (; cur.count() > 0; cur.next_tile(p)) {
-        const int qb = tile & 1;
-        if (!wait.count(till, smem_u32(&b_qempty[qb]), fill[qb].empty(), blocks)) break;
-        const unsigned full = smem_u32(&b_qfull[qb]);
-        mbar_expect_tx(full, p.T * p.G * 128 * Sh::CB);
-        for (int cb = 0; cb < Sh::CB; ++cb)
-          pa_tma3(sm_q + qb * Sh::Q_BUF + cb * Sh::Q_CB, &mq, cb * 64, cur.h * p.G, cur.q.s.q0 + cur.j * p.T, full);
-        ++fill[qb].sent;
-        ++tile;
-        blocks += cur.count();
-      }
+    // ============================== queries (one lane; the walk over groups takes the warp)
+    Cursor cur;
+    cur.set(p, s_place);
+    PaFill fill[2];
+    int tile = 0, blocks = 0, till = PaWait::counted(p, PaWait::QUERIES);   // (blocks: of the tiles before)
+    bool ok = true;
+    auto send = [&]() {
+      const int qb = tile & 1;
+      ok = wait.count(till, smem_u32(&b_qempty[qb]), fill[qb].empty(), blocks);
+      if (!ok) return;
+      const unsigned full = smem_u32(&b_qfull[qb]);
+      mbar_expect_tx(full, p.T * p.G * 128 * Sh::CB);
+      for (int cb = 0; cb < Sh::CB; ++cb)
+        pa_tma3(sm_q + qb * Sh::Q_BUF + cb * Sh::Q_CB, &mq, cb * 64, cur.head() * p.G, cur.tok(p), full);
+      ++fill[qb].sent;
+      ++tile;
+      blocks += cur.count();
+    };
+    auto drain = [&]() {
       for (int qb = 0; qb < 2; ++qb)
         if (fill[qb].sent > 0) wait.drain(smem_u32(&b_qfull[qb]), fill[qb].landed());
+    };
+    if constexpr (MODE == PA_SHARED) {
+#pragma unroll 1
+      for (; cur.count() > 0; cur.next_tile(p)) {
+        if (lane == 0) send();
+        if (!__shfl_sync(~0u, ok, 0)) break;
+      }
+      if (lane == 0) drain();
+    } else if (lane == 0) {
+#pragma unroll 1
+      for (; ok && cur.count() > 0; cur.next_tile(p)) send();
+      drain();
     }
   } else if (work && aux < 0) {
     // ============================== softmax: a key of every block, all rows
     const int kl = tid;
     const unsigned lane_off = (unsigned)(warp * 32) << 16;
     const unsigned prow = sm_p + kl * 128, x7 = kl & 7;   // this key's probabilities, in chunks of 16 bytes swizzled by the key
-    PaCursor<1> cur;
+    Cursor cur;
     cur.set(p, s_place);
     int sp = 0, n = 0;   // (bit i of sp: the parity of s[i])
     auto larger = [](float a, float b) { return fmaxf(a, b); };
@@ -282,8 +297,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     // A wait that fails (the CTA is leaving) lets the loops run out without waiting, so that the warps' barriers stay in step.
 #pragma unroll 1
     for (int cnt; (cnt = cur.count()) > 0; cur.next_tile(p)) {
-      const int off = cur.q.s.len - cur.q.s.m + cur.j * p.T;        // the tile's first token sees the keys [0, off]
-      const int every = p.causal ? off + 1 : cur.q.s.len;           // keys that all rows see
+      const PaFewSight<N, MODE> sight(p, cur);
+      unsigned unset = 0;                                           // rows that have seen no key: they have no reference yet
       constexpr float UP = PA_UP<FP16>;
       float base[N], sum[N];                                        // UP - reference (log2 units), and this key's part of the sum
 #pragma unroll
@@ -298,17 +313,13 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         unsigned s[N];
         pa_ld16(tm + (n & 1) * N + lane_off, s);
         pa_wait_ld<N>(s);
-        if (__builtin_expect((cur.b + k + 1) * PA_BN > every, 0)) {
-          // rows from `from` on see this key
-          const int from = key >= cur.q.s.len ? N : (p.causal ? min(max(key - off, 0), N) * p.G : 0);
-#pragma unroll
-          for (int c = 0; c < N; ++c)
-            if (c < from) s[c] = 0xFF800000u;   // -inf, whatever lies there
-          if ((cur.b + k + 1) * PA_BN > cur.q.s.len) {
-            // the values behind the sequence's end may be anything: zeros, so that 0 x NaN does not reach the sum
+        if (__builtin_expect(sight.partly((cur.b + k) * PA_BN), 0)) {
+          sight.mask(p, key, s);
+          if (sight.strange((cur.b + k) * PA_BN)) {
+            // the values that nobody sees may be anything: zeros, so that 0 x NaN does not reach the sum
             const int place = 2 * n + 1, slot = place % NS;
             wait(smem_u32(&b_kfull[slot]), (place / NS) & 1);
-            if (key >= cur.q.s.len) {
+            if (MODE == PA_SHARED ? s_valid.none(slot, kl, p) : sight.none(key)) {
               const unsigned row = sm_kv + slot * Sh::TILE + kl * 128;
 #pragma unroll 1
               for (int cb = 0; cb < Sh::CB; ++cb)
@@ -323,6 +334,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         if (k > 0) {
 #pragma unroll
           for (int c = 0; c < N; ++c) over |= fmaf(__uint_as_float(s[c]), p.scale2, base[c]) > PA_LAZY + UP;
+          if (MODE != PA_PLAIN && unset) {   // (the first logit that such a row sees is its reference, however far below zero)
+#pragma unroll
+            for (int c = 0; c < N; ++c) over |= (unset >> c & 1) && s[c] != 0xFF800000u;
+          }
         }
         if (__builtin_expect(k == 0 || pf_or(over), 0)) {
           float m[N], f[N];
@@ -337,8 +352,15 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             const float top = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)) * p.scale2;
             // (a row that sees none of these keys keeps its reference; of a first block, any)
             const float nb = top == -INFINITY ? (k == 0 ? UP : base[c]) : UP - top;
-            const float use = k == 0 ? nb : fminf(base[c], nb);
+            float use = k == 0 ? nb : fminf(base[c], nb);
             f[c] = k == 0 ? 1.f : ex2(use - base[c]);
+            if constexpr (MODE != PA_PLAIN) {
+              if (unset >> c & 1) {   // (its sums are zero)
+                use = nb;
+                f[c] = 1.f;
+              }
+              unset = top == -INFINITY ? (k == 0 ? unset | 1u << c : unset) : unset & ~(1u << c);
+            }
             base[c] = use;
             sum[c] *= f[c];
           }
@@ -398,7 +420,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       s_red[col][warp] = sum[0];
       pf_sync();
       const bool whole = cnt == cur.nb;
-      const int ntok = min(p.T, cur.q.s.m - cur.j * p.T), rows = ntok * p.G;
+      const int ntok = cur.tokens(p), rows = ntok * p.G;
       const long long part = (long long)blockIdx.x * 2 + (cur.b == 0 ? 1 : 0);
       if (kl < rows) {   // a thread per row
         const int row = kl;
@@ -413,7 +435,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           p.part_ml[part * 128 + row] = make_float2(all == 0.f ? -INFINITY : ref, all);
         } else if (p.lse) {
           const int t = row / p.G;
-          p.lse[(long long)(cur.q.s.q0 + cur.j * p.T + t) * p.Hq + cur.h * p.G + (row - t * p.G)] =
+          p.lse[(long long)(cur.tok(p) + t) * p.Hq + cur.head() * p.G + (row - t * p.G)] =
               all == 0.f ? -INFINITY : (ref + UP + log2f(all * PA_DOWN<FP16>)) * 0.69314718055994531f;
         }
       }
@@ -429,7 +451,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       pa_ld16(tm + Sh::TM_O + N + lane_off, l);
       pa_wait_ld<N>(o);
       pa_wait_ld<N>(l);
-      uint16_t* dst = p.out + (long long)(cur.q.s.q0 + cur.j * p.T) * p.ots + (long long)cur.h * p.G * p.ohs + chan;
+      uint16_t* dst = p.out + (long long)cur.tok(p) * p.ots + (long long)cur.head() * p.G * p.ohs + chan;
       float* po = p.part_o + (part * (D / 4) + chan / 4) * 512 + chan % 4;
       int g = 0;
 #pragma unroll
@@ -453,33 +475,6 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     pa_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(Sh::TM_COLS) : "memory");
   }
-}
-
-template <int D, bool FP16>
-static cudaError_t few_t(const PaParams& p, const CUtensorMap* maps, int device, cudaStream_t st) {
-  static std::atomic<unsigned long long> ready{0};   // devices whose copy of the kernel has its attribute
-  if (device >= 64 || !(ready.load() >> device & 1)) {
-    const cudaError_t e = cudaFuncSetAttribute(pages_few_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfShape<D>::SMEM);
-    if (e != cudaSuccess) return e;
-    if (device < 64) ready.fetch_or(1ull << device);
-  }
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.ctas);
-  cfg.blockDim = dim3(PF_THREADS);
-  cfg.dynamicSmemBytes = PfShape<D>::SMEM;
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, pages_few_kernel<D, FP16>, p, maps[0], maps[1], maps[2]);
-  return e != cudaSuccess || !p.rec ? e : launch_pages_join(p, 1, FP16, st);   // (no rec: no tile is cut)
-}
-
-cudaError_t launch_pages_few(const PaParams& p, const CUtensorMap* maps, int fp16, int device, cudaStream_t st) {
-  if (p.pg.D == 128) return fp16 ? few_t<128, true>(p, maps, device, st) : few_t<128, false>(p, maps, device, st);
-  return fp16 ? few_t<64, true>(p, maps, device, st) : few_t<64, false>(p, maps, device, st);
 }
 
 }  // namespace qe
