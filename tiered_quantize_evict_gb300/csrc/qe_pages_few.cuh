@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   pa_fence_before();
   griddep_wait();
   griddep_launch_dependents();   // (what follows may then rely on all that ran before this launch)
-  const bool work = PaWalk<1, MODE>::template find<PF_THREADS>(p, s_place, s_w);   // ends with a barrier
+  const bool work = PaWalk<1, MODE>::template find<PF_THREADS>(p, s_place, s_w, reinterpret_cast<int*>(smem_raw + 1024 + 2 * Sh::Q_BUF));   // ends with a barrier
   pa_fence_after();
   const unsigned tm = s_tmem;
 

@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
   pa_fence_before();
   griddep_wait();
   griddep_launch_dependents();   // (what follows may then rely on all that ran before this launch)
-  const bool work = PaWalk<NH, MODE>::template find<PA_THREADS<NH>>(p, s_place, s_w);   // ends with a barrier
+  const bool work = PaWalk<NH, MODE>::template find<PA_THREADS<NH>>(p, s_place, s_w, reinterpret_cast<int*>(smem_raw) + 256);   // ends with a barrier
   pa_fence_after();
   const unsigned tm = s_tmem;
 
@@ -470,7 +470,21 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
           }
-          if (any_live) {
+          if (MODE == PA_SHARED && any_live && sight.nothing(k * PA_BN, ch * 64)) {
+            // nothing of the block is for these rows (both warps of a row say so): probabilities of zero
+            unsigned z[16] = {};
+            pa_st16(t_s + ch * 32, z);
+            pa_st16(t_s + ch * 32 + 16, z);
+            if (NH == 1) {
+              pa_st16(t_s + 64 + ch * 32, z);
+              pa_st16(t_s + 64 + ch * 32 + 16, z);
+            }
+            pa_wait_st();
+            pa_fence_before();
+            __syncwarp();
+            if (lane == 0)
+              for (int c = 0; c < PARTS - 1; ++c) pa_arrive(smem_u32(&b_p[sb][c]));
+          } else if (any_live) {
             unsigned s[64];
             pa_ld32(t_s + ch * 64, s);
             pa_ld32(t_s + ch * 64 + 32, s + 32);
@@ -601,7 +615,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
               unsigned o[32];
               pa_ld32(t_o + c, o);
               pa_wait_ld<32>(o);
-              if (live)
+              if (live && (MODE != PA_SHARED || sum != 0.f))   // (the join leaves out a part without a sum)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)       // four channels of 32 rows side by side
                   *reinterpret_cast<uint4*>(po + (c / 4 + e) * 512) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);

@@ -14,20 +14,29 @@ namespace qe {
 
 constexpr int PA_TILE_KEYS = PA_TILE_COST * PA_BN;
 
+// Where groups and sequences are looked up: in the call's arrays (row and len NULL), or in a copy of what they come to.
+struct PaSource {
+  const int *start, *prefix, *q_start, *row, *len;
+  __device__ __forceinline__ int row_of(const PaParams& p, int s) const { return row ? row[s] : (p.c.rows ? p.c.rows[s] : s); }
+  __device__ __forceinline__ int len_of(const PaParams& p, int s, int r) const { return len ? len[s] : row_len(p.pg, p.t, r, false); }
+};
+__device__ __forceinline__ PaSource pa_arrays(const PaParams& p) { return PaSource{p.gr.start, p.gr.prefix, p.c.q_start, nullptr, nullptr}; }
+
 // A group: its sequences [s0, s1), packed tokens [q0, q1), tokens of the prefix (whole pages) and the row that has them.
 struct PaGroup {
   int s0, s1, q0, q1, prefix, row;
   __device__ __forceinline__ bool empty() const { return q1 <= q0; }
 };
-__device__ __forceinline__ PaGroup pa_group(const PaParams& p, int g) {
+__device__ __forceinline__ PaGroup pa_group(const PaParams& p, const PaSource& from, int g) {
   PaGroup r;
-  r.s0 = min(max(p.gr.start[g], 0), p.c.n);
-  r.s1 = min(max(p.gr.start[g + 1], r.s0), p.c.n);
-  const int want = p.gr.prefix[g];
-  r.q0 = min(max(p.c.q_start[r.s0], 0), p.c.total);
-  r.q1 = min(max(p.c.q_start[r.s1], r.q0), p.c.total);
-  r.row = r.s0 < r.s1 ? (p.c.rows ? p.c.rows[r.s0] : r.s0) : -1;
-  r.prefix = min(max(want, 0), row_len(p.pg, p.t, r.row, false)) & -p.pg.S;
+  r.s0 = min(max(from.start[g], 0), p.c.n);
+  r.s1 = min(max(from.start[g + 1], r.s0), p.c.n);
+  const int want = from.prefix[g];
+  r.q0 = min(max(from.q_start[r.s0], 0), p.c.total);
+  r.q1 = min(max(from.q_start[r.s1], r.q0), p.c.total);
+  const bool some = r.s0 < r.s1;
+  r.row = some ? from.row_of(p, r.s0) : -1;
+  r.prefix = min(max(want, 0), some ? from.len_of(p, r.s0, r.row) : 0) & -p.pg.S;
   return r;
 }
 
@@ -39,11 +48,11 @@ struct PaMember {
     return max(0, (p.causal ? len - m + min(m, end - a) : len) - g.prefix);
   }
 };
-__device__ __forceinline__ PaMember pa_member(const PaParams& p, const PaGroup& g, int s) {
+__device__ __forceinline__ PaMember pa_member(const PaParams& p, const PaSource& from, const PaGroup& g, int s) {
   PaMember r;
-  const int a = p.c.q_start[s], b = p.c.q_start[s + 1];
-  r.row = p.c.rows ? p.c.rows[s] : s;
-  r.len = row_len(p.pg, p.t, r.row, false);
+  const int a = from.q_start[s], b = from.q_start[s + 1];
+  r.row = from.row_of(p, s);
+  r.len = from.len_of(p, s, r.row);
   r.a = min(max(a, g.q0), g.q1);
   r.m = min(max(b, r.a), g.q1) - r.a;
   return r;
@@ -55,12 +64,12 @@ struct PaBatch {
   PaMember s;
   int at, end;         // own keys of the tile [at, end), in whole pieces; empty where the sequence has no tokens in the tile
   bool more;           // sequences behind may have some
-  __device__ __forceinline__ void load(const PaParams& p, const PaGroup& g, int base, int t0, int t1, int before) {
+  __device__ __forceinline__ void load(const PaParams& p, const PaSource& from, const PaGroup& g, int base, int t0, int t1, int before) {
     const int lane = threadIdx.x & 31, i = base + lane, piece = pa_piece(p);
     s = PaMember{t1, 0, -1, 0};
     int own = 0;
     if (i < g.s1) {
-      s = pa_member(p, g, i);
+      s = pa_member(p, from, g, i);
       if (max(s.a, t0) < min(s.a + s.m, t1)) own = (s.own(p, g, t1) + piece - 1) & -piece;
     }
     int y = own;
@@ -86,6 +95,8 @@ struct PaBatch {
 
 struct PaSharedPlace {
   int h, g, j, b;      // KV head (that of the end of the line: their number), group, tile of the group, block
+  PaGroup gr;          // what a walk from here on starts with
+  int first, t0, t1, nb;
   int i;               // (while it is being found) sequence,
   long long rem;       // and how far behind its start on a head's line
   __device__ __forceinline__ bool before(const PaSharedPlace& o) const {
@@ -101,19 +112,19 @@ struct PaSharedCursor {
   PaGroup gr;
   int first;            // sequence of the tile's first token
   int t0, t1;           // the tile's packed tokens
-  __device__ __forceinline__ void tile(const PaParams& p) {
+  __device__ __forceinline__ void tile(const PaParams& p, const PaSource& from) {
     t0 = gr.q0 + j * NH * p.T;
     t1 = min(gr.q1, t0 + NH * p.T);
-    first = gr.s0 + pages_count_below(p.c.q_start + gr.s0 + 1, gr.s1 - gr.s0, t0);
-    nb = max(1, (keys(p, gr.s1) + PA_BN - 1) >> 7);
+    first = gr.s0 + pages_count_below(from.q_start + gr.s0 + 1, gr.s1 - gr.s0, t0);
+    nb = max(1, (keys(p, from, gr.s1) + PA_BN - 1) >> 7);
   }
   // keys of the tile before those of sequence `until`
-  __device__ __forceinline__ int keys(const PaParams& p, int until) const {
+  __device__ __forceinline__ int keys(const PaParams& p, const PaSource& from, int until) const {
     PaBatch x;
     int at = gr.prefix;
 #pragma unroll 1
     for (int base = first; base < until; base += 32) {
-      x.load(p, gr, base, t0, t1, at);
+      x.load(p, from, gr, base, t0, t1, at);
       if (until - base < 32) return __shfl_sync(~0u, x.at, until - base);
       at = x.total();
       if (!x.more) break;
@@ -129,8 +140,11 @@ struct PaSharedCursor {
     eg = pl[1].g;
     ej = pl[1].j;
     eb = pl[1].b;
-    gr = pa_group(p, g);
-    tile(p);
+    gr = pl[0].gr;
+    first = pl[0].first;
+    t0 = pl[0].t0;
+    t1 = pl[0].t1;
+    nb = pl[0].nb;
   }
   __device__ __forceinline__ bool last_tile() const { return h == eh && g == eg && j == ej; }
   __device__ __forceinline__ int count() const { return last_tile() ? eb - b : nb - b; }
@@ -169,9 +183,9 @@ struct PaSharedCursor {
           }
         }
       }
-      gr = pa_group(p, g);
+      gr = pa_group(p, pa_arrays(p), g);
     }
-    tile(p);
+    tile(p, pa_arrays(p));
   }
   __device__ __forceinline__ bool second_half(const PaParams& p) const { return NH == 2 && t0 + p.T < t1; }
   __device__ __forceinline__ int head() const { return h; }
@@ -186,7 +200,7 @@ struct PaSharedCursor {
     int at = gr.prefix;
 #pragma unroll 1
     for (int base = first; base < gr.s1; base += 32) {
-      x.load(p, gr, base, t0, t1, at);
+      x.load(p, pa_arrays(p), gr, base, t0, t1, at);
       const int n = PaBatch::first_above(x.s.a + x.s.m, t), from = min(n, 31);
       const int a = __shfl_sync(~0u, x.s.a, from), m = __shfl_sync(~0u, x.s.m, from), len = __shfl_sync(~0u, x.s.len, from), k = __shfl_sync(~0u, x.at, from);
       if (n < 32 && t >= a && t < a + m) {
@@ -224,7 +238,7 @@ struct PaSharedKeys {
         g = c.g;
         j = c.j;
         base = c.first;
-        x.load(p, c.gr, base, c.t0, c.t1, c.gr.prefix);
+        x.load(p, pa_arrays(p), c.gr, base, c.t0, c.t1, c.gr.prefix);
       }
       while (true) {
         const int n = PaBatch::first_above(x.end, v), from = min(n, 31);
@@ -237,7 +251,7 @@ struct PaSharedKeys {
         if (!x.more || !__any_sync(~0u, key < 0)) break;
         const int at = x.total();
         base += 32;
-        x.load(p, c.gr, base, c.t0, c.t1, at);
+        x.load(p, pa_arrays(p), c.gr, base, c.t0, c.t1, at);
       }
     }
     if (key >= 0 && key < len) {
@@ -249,9 +263,12 @@ struct PaSharedKeys {
   }
 };
 
-// Every CTA finds its piece, as pa_find does.
+// Every CTA finds its piece, as pa_find does.  `space` is shared memory for PA_FIND_INTS(NT) numbers: where there is a thread for each
+// sequence and group, what the arrays hold is read once, side by side, and looked up there (a call over one group of 64 sequences: the
+// piece is known after 4.5 us instead of 9).
+constexpr int PA_FIND_INTS(int nt) { return 5 * nt + 2; }
 template <int NH, int NT>
-__device__ __noinline__ void pa_find_shared(const PaParams& p, PaSharedPlace* pl, long long* s_w) {
+__device__ __noinline__ void pa_find_shared(const PaParams& p, PaSharedPlace* pl, long long* s_w, int* space) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tt = NH * p.T, piece = pa_piece(p);
   constexpr int W = NT / 32;
   const int c = blockIdx.x;
@@ -275,11 +292,32 @@ __device__ __noinline__ void pa_find_shared(const PaParams& p, PaSharedPlace* pl
     __syncthreads();
     return before + y - x;
   };
+  PaSource from = pa_arrays(p);
+  const bool held = p.c.n <= NT && p.gr.n <= NT;
+  if (held) {
+    int *start = space, *prefix = start + NT + 1, *q_start = prefix + NT, *row = q_start + NT + 1, *len = row + NT;
+    if (tid < p.gr.n) {
+      start[tid + 1] = from.start[tid + 1];
+      prefix[tid] = from.prefix[tid];
+    }
+    if (tid < p.c.n) {
+      q_start[tid + 1] = from.q_start[tid + 1];
+      const int r = from.row_of(p, tid);
+      row[tid] = r;
+      len[tid] = row_len(p.pg, p.t, r, false);
+    }
+    if (tid == NT - 1) {
+      start[0] = from.start[0];
+      q_start[0] = from.q_start[0];
+    }
+    __syncthreads();
+    from = PaSource{start, prefix, q_start, row, len};
+  }
   auto group_of = [&](int i) {   // the last that does not begin behind sequence i
     int lo = 0, hi = p.gr.n;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (p.gr.start[mid] <= i) lo = mid;
+      if (from.start[mid] <= i) lo = mid;
       else hi = mid;
     }
     return lo;
@@ -313,13 +351,13 @@ __device__ __noinline__ void pa_find_shared(const PaParams& p, PaSharedPlace* pl
   auto length = [&](int i, bool report) {
     if (i >= p.c.n) return 0ll;
     const int gi = group_of(i);
-    const PaGroup g = pa_group(p, gi);
+    const PaGroup g = pa_group(p, from, gi);
     if (report) {
       const SeqInfo s = seq_info(p.pg, p.t, p.c, i, true);
       if (s.m > 0 && g.prefix > 0 && g.prefix > (p.causal ? s.len - s.m : s.len)) pages_report(p.pg, QE_PAGES_ERR_ROW);
     }
     if (i < g.s0 || i >= g.s1) return 0ll;   // (of no group)
-    const PaMember s = pa_member(p, g, i);
+    const PaMember s = pa_member(p, from, g, i);
     if (s.m == 0) return 0ll;
     const Part r = on_line(g, s);
     if (r.tiles == 0) return r.part;
@@ -336,7 +374,7 @@ __device__ __noinline__ void pa_find_shared(const PaParams& p, PaSharedPlace* pl
       if (bad) pages_report(p.pg, QE_PAGES_ERR_ROW);
     }
   }
-  if (tid < 2) pl[tid] = PaSharedPlace{p.pg.H, 0, 0, 0, -1, 0};
+  if (tid < 2) pl[tid].h = p.pg.H, pl[tid].g = pl[tid].j = pl[tid].b = 0, pl[tid].i = -1;
   // one pass where there is a thread for each sequence, else two
   long long line, x = length(tid, c == 0), pre = scan(x, line);
 #pragma unroll 1
@@ -348,14 +386,14 @@ __device__ __noinline__ void pa_find_shared(const PaParams& p, PaSharedPlace* pl
   const long long all = line * p.pg.H, most = all / (PA_LEAST * PA_BN);
   const int pieces = most < 1 ? 1 : (most > gridDim.x ? (int)gridDim.x : (int)most);
   if (c < pieces && all > 0) {
-    const long long each = all / pieces;
+    const long long each = div_ll(all, pieces);
     const int over = (int)(all - each * pieces);
     long long cut[2];
     int head[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const long long to = each * (c + k) + (long long)over * (c + k) / pieces;
-      head[k] = (int)(to / line);
+      const long long to = each * (c + k) + over * (c + k) / pieces;
+      head[k] = (int)div_ll(to, line);
       cut[k] = to - head[k] * line;
     }
     long long at = 0;
@@ -384,8 +422,8 @@ __device__ __noinline__ void pa_find_shared(const PaParams& p, PaSharedPlace* pl
     long long rem = pl[warp].rem;
     PaSharedCursor<NH> cur;
     cur.g = group_of(i);
-    cur.gr = pa_group(p, cur.g);
-    const Part r = on_line(cur.gr, pa_member(p, cur.gr, i));
+    cur.gr = pa_group(p, from, cur.g);
+    const Part r = on_line(cur.gr, pa_member(p, from, cur.gr, i));
     const bool in_part = rem < r.part;
     if (in_part) {
       cur.j = r.j - 1;
@@ -404,8 +442,8 @@ __device__ __noinline__ void pa_find_shared(const PaParams& p, PaSharedPlace* pl
       cur.j = r.j + lo;
       rem -= before + PA_TILE_KEYS;
     }
-    cur.tile(p);
-    if (in_part) rem += cur.keys(p, i);
+    cur.tile(p, from);
+    if (in_part) rem += cur.keys(p, from, i);
     // A cut in what the tile costs besides, or in a short tile, is one before the tile; one behind its blocks is before the next.  (Cuts
     // are 256 keys apart or more, which are at least 170 of a tile's and so another block: no two pieces start at the same block inside of
     // a tile, and a part that the join looks for has been written.)
@@ -422,10 +460,16 @@ __device__ __noinline__ void pa_find_shared(const PaParams& p, PaSharedPlace* pl
       pl[warp].g = end ? 0 : cur.g;
       pl[warp].j = end ? 0 : cur.j;
       pl[warp].b = b;
+      pl[warp].gr = cur.gr;
+      pl[warp].first = cur.first;
+      pl[warp].t0 = cur.t0;
+      pl[warp].t1 = cur.t1;
+      pl[warp].nb = cur.nb;
       if (warp == 0)
         p.rec[c] = end ? PaRec{-1, 0, 0, 0, 0, 0} : PaRec{(long long)cur.h * p.c.total + cur.t0, b, cur.t0, cur.t1 - cur.t0, cur.h, pieces};
     }
   }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (copies go where `space` is)
   __syncthreads();
 }
 

@@ -22,7 +22,7 @@ struct PaWalk {
   using Keys = PaRowKeys<NH, MODE>;
   // finds the CTA's piece of the line; false where it has none
   template <int NT>
-  static __device__ __forceinline__ bool find(const PaParams& p, Place* pl, long long* s_w) {
+  static __device__ __forceinline__ bool find(const PaParams& p, Place* pl, long long* s_w, int*) {
     pa_find<NH, NT, MODE>(p, pl, s_w);
     // (two cuts that fall into the same place leave an empty piece)
     return pl[0].i < p.c.n && (pl[0].i != pl[1].i || pl[0].h != pl[1].h || pl[0].j != pl[1].j || pl[0].b != pl[1].b);
@@ -34,8 +34,8 @@ struct PaWalk<NH, PA_SHARED> {
   using Place = PaSharedPlace;
   using Keys = PaSharedKeys<NH>;
   template <int NT>
-  static __device__ __forceinline__ bool find(const PaParams& p, Place* pl, long long* s_w) {
-    pa_find_shared<NH, NT>(p, pl, s_w);
+  static __device__ __forceinline__ bool find(const PaParams& p, Place* pl, long long* s_w, int* space) {
+    pa_find_shared<NH, NT>(p, pl, s_w, space);
     return pl[0].before(pl[1]);
   }
 };
@@ -61,6 +61,7 @@ struct PaValid<PA_SHARED, SLOTS> {
 template <int NH, int MODE>
 struct PaSight {
   int vis, low, open, all_vis, all_low, end, gap;   // end: values from here on are nobody's; gap: as are those of [open, gap)
+  int mine0, mine1;                                 // shared: the warp's rows see own keys of [mine0, mine1), counted from the block's first
   __device__ __forceinline__ PaSight(const PaParams& p, const typename PaWalk<NH, MODE>::Cursor& c, int t, bool live, bool any_live, int from) {
     constexpr int FAR = 1 << 30;
     open = low = gap = all_low = -FAR;
@@ -74,6 +75,9 @@ struct PaSight {
           vis = hi - from;
           low = lo - from;
         }
+        const int block = c.b * PA_BN;
+        mine0 = __reduce_min_sync(~0u, live ? lo - block : FAR);
+        mine1 = __reduce_max_sync(~0u, live ? hi - block : -FAR);
       }
       end = open;   // (own keys: PaValid)
     } else {
@@ -95,6 +99,10 @@ struct PaSight {
   __device__ __forceinline__ bool partly(int at) const {
     if constexpr (MODE == PA_SHARED) return at + 64 > open;
     return at + 64 > all_vis || (MODE == PA_WINDOW && at < all_low && at + 64 > open);
+  }
+  // whether no row of the warp sees any key of the block from `at` on (`back`: how far this thread's half of it is behind its first key)
+  __device__ __forceinline__ bool nothing(int at, int back) const {
+    return MODE == PA_SHARED && at >= open + back && (at + PA_BN <= mine0 || at >= mine1);
   }
   // -inf in the place of the logits that the row does not see, whatever lies there
   __device__ __forceinline__ void mask(int at, unsigned (&s)[64]) const {
