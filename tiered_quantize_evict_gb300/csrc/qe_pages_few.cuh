@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     // this lane's piece, its entry loaded a block before it is looked at
     typename PaWalk<1, MODE>::Keys keys;
     int slot = 0, ph = 1, issued = 0, left = cur.count();
-    PaPiece next = keys.at(p, cur, cur.b * PA_BN + piece * rows);
+    PaPiece next = keys.at(p, cur, cur.b, piece * rows);
     int till = PaWait::counted(p, PaWait::KEYS);
     bool ok = true;
 #pragma unroll 1
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         cur.next_tile(p);
         left = cur.count();
       }
-      if (left > 0) next = keys.at(p, cur, cur.b * PA_BN + piece * rows);
+      if (left > 0) next = keys.at(p, cur, cur.b, piece * rows);
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
         ok = ok && wait.count(till, smem_u32(&b_kempty[slot]), ph);

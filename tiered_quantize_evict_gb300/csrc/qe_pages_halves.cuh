@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
       // this lane's piece, its entry loaded a block before it is looked at
       typename PaWalk<NH, MODE>::Keys keys;
       int slot = 0, ph = 1, issued = 0, left = cur.count();
-      PaPiece next = keys.at(p, cur, cur.b * PA_BN + piece * rows);
+      PaPiece next = keys.at(p, cur, cur.b, piece * rows);
       int till = PaWait::counted(p, PaWait::KEYS);
       bool ok = true;
 #pragma unroll 1
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
           cur.next_tile(p);
           left = cur.count();
         }
-        if (left > 0) next = keys.at(p, cur, cur.b * PA_BN + piece * rows);
+        if (left > 0) next = keys.at(p, cur, cur.b, piece * rows);
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           ok = ok && wait.count(till, smem_u32(&b_kempty[slot]), ph);
@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
       // The ring is consumed in its order: K 0, then V n - 1 and K n in turn.
       int slot = 0, ph = 0, pp = 0, qp = 0, tile = 0, left = 0;   // (bit i of pp, qp: the parity of p[i], qfull[i])
       int till = PaWait::counted(p, PaWait::PRODUCTS);
+      int at = 0, all = 0, done = 0;   // (shared: the block; how many of the tile's are for this half, and how many of them were before)
       bool was_first = false, was_last = false, was_mine = false, mine = false, ok = true, more = true;
       auto step = [&]() {
         if (++slot == NS) {
@@ -273,14 +274,25 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
       };
 #pragma unroll 1
       for (int n = 0; more; ++n) {
-        const bool first = left == 0;
+        bool first = left == 0;
         if (first) {
           if (n > 0) cur.next_tile(p);
           left = cur.count();
           more = left > 0;      // one more round for the last P V
           mine = h == 0 || cur.second_half(p);
+          if constexpr (MODE == PA_SHARED && NH == 2) {
+            at = cur.b;
+            all = more && mine ? cur.count_for(h) : 0;
+            done = 0;
+          }
         }
-        const bool last = left == 1;
+        bool last = left == 1;
+        if constexpr (MODE == PA_SHARED && NH == 2) {   // of the blocks that are for this half
+          mine = more && all > 0 && cur.is_for(h, at++);
+          first = mine && done == 0;
+          done += mine;
+          last = mine && done == all;
+        }
         const int vslot = slot;
         if constexpr (NH == 2) {
           // what has to be there: values, keys and queries, long before the probabilities
@@ -386,6 +398,8 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
         const int halves = cur.second_half(p) ? 2 : 1;
 #pragma unroll 1
         for (int h = 0; h < halves; ++h) {
+          if constexpr (MODE == PA_SHARED && NH == 2)
+            if (cur.count_for(h) == 0) continue;
           const int qb = NH == 2 ? h : tile & 1;
           ok = wait.count(till, smem_u32(&b_qempty[qb]), fill[qb].empty(), blocks);
           if (!ok) break;
@@ -445,21 +459,36 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
         const int t = half * p.T + rt;                    // token of the tile
         const bool live = rt < p.T && t < cur.tokens(p);
         const bool any_live = __any_sync(~0u, live);
-        const PaSight<NH, MODE> sight(p, cur, t, live, any_live, cur.b * PA_BN + ch * 64);   // from this thread's half of the first block on
+        const bool whole = cnt == cur.nb;
+        const long long part = ((long long)blockIdx.x * 2 + (cur.b == 0 ? 1 : 0)) * NH + half;
+        if constexpr (MODE == PA_SHARED && NH == 2)
+          if (cur.count_for(half) == 0) {   // (whole tiles have blocks for both)
+            if (live && ch == 0) p.part_ml[part * 128 + r] = make_float2(-INFINITY, 0.f);
+            n += cnt;
+            continue;
+          }
+        // from this thread's half of the first block on (shared: of the stream)
+        const PaSight<NH, MODE> sight(p, cur, half, t, live, any_live, (MODE == PA_SHARED ? 0 : cur.b * PA_BN) + ch * 64);
+        bool begun = false;
         float ref = -INFINITY, sum = 0.f;
 #pragma unroll 1
         for (int k = 0; k < cnt; ++k, ++n) {
+          int at = k * PA_BN;
+          if constexpr (MODE == PA_SHARED)
+            if (const int z = cur.block(cur.b + k, at); NH == 2 && cur.b + k >= cur.np && z != half) continue;
+          const bool begin = MODE == PA_SHARED ? !begun : k == 0;
+          begun = true;
           const int sb = NH == 2 ? half : n & 1;
           wait(smem_u32(&b_s[sb]), sp >> sb & 1, NH == 2 ? n : 0);   // (half 1 may have sat out tiles before)
           sp ^= 1 << sb;
           __syncwarp();
           pa_fence_after();
           const unsigned t_s = tm + sb * 128 + lane_off;
-          if (__builtin_expect(sight.strange(k * PA_BN) && ch == 0, 0)) {
+          if (__builtin_expect(sight.strange(at) && ch == 0, 0)) {
             // the values that nobody sees may be anything: zeros, so that 0 x NaN does not reach the sum
             const int place = 2 * n + 1, slot = place % NS;
             wait(smem_u32(&b_kfull[slot]), (place / NS) & 1);
-            if (MODE == PA_SHARED ? s_valid.none(slot, r, p) : sight.none(k * PA_BN + r)) {
+            if (MODE == PA_SHARED ? s_valid.none(slot, r, p) : sight.none(at + r)) {
               const unsigned row = sm_kv + slot * Sh::TILE + r * 128;
 #pragma unroll 1
               for (int cb = 0; cb < Sh::CB; ++cb)
@@ -470,7 +499,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
           }
-          if (MODE == PA_SHARED && any_live && sight.nothing(k * PA_BN, ch * 64)) {
+          if (MODE == PA_SHARED && any_live && sight.nothing(at, ch * 64)) {
             // nothing of the block is for these rows (both warps of a row say so): probabilities of zero
             unsigned z[16] = {};
             pa_st16(t_s + ch * 32, z);
@@ -489,7 +518,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
             pa_ld32(t_s + ch * 64, s);
             pa_ld32(t_s + ch * 64 + 32, s + 32);
             pa_wait_ld<64>(s);
-            if (__builtin_expect(sight.partly(k * PA_BN), 0)) sight.mask(k * PA_BN, s);
+            if (__builtin_expect(sight.partly(at), 0)) sight.mask(at, s);
             float mx[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) mx[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 4]));
@@ -499,11 +528,11 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
               for (int e = 0; e < 4; ++e)
                 mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(s[c + e])), __uint_as_float(s[c + 4 + e]));
             float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            if (__builtin_expect(k == 0 || pa_pair_or(pair, live && (m - ref) * p.scale2 > PA_LAZY), 0)) {
+            if (__builtin_expect(begin || pa_pair_or(pair, live && (m - ref) * p.scale2 > PA_LAZY), 0)) {
               m = together(fmaxf(m, ref), [](float a, float b) { return fmaxf(a, b); });
               const float f = m == -INFINITY ? 1.f : ex2((ref - m) * p.scale2);
               ref = m;
-              if (k > 0) {
+              if (!begin) {
                 sum *= f;
                 if constexpr (NH == 1) {   // the P V before this block's may still be running
                   wait(smem_u32(&b_o[(n - 1) & 1]), (n - 1) >> 1 & 1);
@@ -577,11 +606,9 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
         pa_fence_after();
         if (any_live) {
           sum = together(sum, [](float a, float b) { return a + b; });
-          const bool whole = cnt == cur.nb;
           const int tok = cur.tok(p) + t;
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
           const int head = cur.head() * p.G + rg;
-          const long long part = ((long long)blockIdx.x * 2 + (cur.b == 0 ? 1 : 0)) * NH + half;
           if (whole) {
             // four lanes write a row's 128 (64) bytes side by side, eight rows a store: with a row per lane a store touches 32
             // lines, and what follows queues behind it (prompts 132 -> 129 us)

@@ -4,6 +4,10 @@
 // the tile's sequences has of its own (up to what its last token in the tile sees, in whole pieces of pages), one after the other:
 // short ends of several sequences fill a block together.  A row sees the prefix and a range of the rest.
 //
+// With two halves the keys are two streams: the prefix and what the first half's sequences have, and what the second half's have.  The
+// blocks behind the prefix come from both in turn, and each is for its half alone: the other half's softmax and products are at the
+// block before and the one behind meanwhile (a block that one half is at and the other waits for took 2.0 us, where reading it takes 1.4).
+//
 // The line is, for each KV head, the groups' tiles in order.  It is measured in keys, sequence by sequence: what a tile costs besides its
 // blocks and the prefix count where the tile begins, own keys where they are.  (Only the cuts go by this measure, and every CTA takes it alike; a
 // walk counts the tiles' own blocks.)
@@ -58,11 +62,11 @@ __device__ __forceinline__ PaMember pa_member(const PaParams& p, const PaSource&
   return r;
 }
 
-// The members of a tile's 32 sequences from `base` on, one to a lane, with the place of their own keys in the tile (before: the keys
-// that come before them).
+// 32 sequences from `base` on, one to a lane, with the place of their own keys in the stream of the packed tokens [t0, t1) (before: the
+// keys that come before them).
 struct PaBatch {
   PaMember s;
-  int at, end;         // own keys of the tile [at, end), in whole pieces; empty where the sequence has no tokens in the tile
+  int at, end;         // own keys of the stream [at, end), in whole pieces; empty where the sequence has none of the tokens
   bool more;           // sequences behind may have some
   __device__ __forceinline__ void load(const PaParams& p, const PaSource& from, const PaGroup& g, int base, int t0, int t1, int before) {
     const int lane = threadIdx.x & 31, i = base + lane, piece = pa_piece(p);
@@ -93,10 +97,22 @@ struct PaBatch {
   }
 };
 
+// a stream's sequences begin at `first`, its keys behind `before` others, and it ends with packed token t1's
+struct PaStream {
+  int first, t0, t1, before;
+};
+
+// A tile's keys: what a walk and the place that it starts at have in common.
+struct PaSharedTile {
+  PaGroup gr;
+  int first, mid;       // sequences of the tile's first token, and of its second half's
+  int t0, t1;           // the tile's packed tokens
+  int np, na, nz;       // blocks with keys of the prefix; those and the rest of the first stream; the second stream's
+};
+
 struct PaSharedPlace {
   int h, g, j, b;      // KV head (that of the end of the line: their number), group, tile of the group, block
-  PaGroup gr;          // what a walk from here on starts with
-  int first, t0, t1, nb;
+  PaSharedTile tile;   // what a walk from here on starts with
   int i;               // (while it is being found) sequence,
   long long rem;       // and how far behind its start on a head's line
   __device__ __forceinline__ bool before(const PaSharedPlace& o) const {
@@ -106,31 +122,61 @@ struct PaSharedPlace {
 
 // A walk from one place to another, tile by tile, by a whole warp.
 template <int NH>
-struct PaSharedCursor {
+struct PaSharedCursor : PaSharedTile {
   int h, g, j, b, nb;   // the place; blocks of the tile
   int eh, eg, ej, eb;   // where the walk ends
-  PaGroup gr;
-  int first;            // sequence of the tile's first token
-  int t0, t1;           // the tile's packed tokens
+  __device__ __forceinline__ PaStream stream(const PaParams& p, int z) const {
+    if (NH == 1) return PaStream{first, t0, t1, gr.prefix};
+    return z ? PaStream{mid, t0 + p.T, t1, np * PA_BN} : PaStream{first, t0, min(t1, t0 + p.T), gr.prefix};
+  }
   __device__ __forceinline__ void tile(const PaParams& p, const PaSource& from) {
     t0 = gr.q0 + j * NH * p.T;
     t1 = min(gr.q1, t0 + NH * p.T);
-    first = gr.s0 + pages_count_below(from.q_start + gr.s0 + 1, gr.s1 - gr.s0, t0);
-    nb = max(1, (keys(p, from, gr.s1) + PA_BN - 1) >> 7);
+    np = (gr.prefix + PA_BN - 1) >> 7;
+    nz = 0;
+    first = mid = gr.s0 + pages_count_below(from.q_start + gr.s0 + 1, gr.s1 - gr.s0, t0);
+    // (every half has a block, so that rows without keys are written too)
+    na = max(1, (keys(p, from, gr.s1, stream(p, 0)) + PA_BN - 1) >> 7);
+    if (second_half(p)) {
+      mid = gr.s0 + pages_count_below(from.q_start + gr.s0 + 1, gr.s1 - gr.s0, t0 + p.T);
+      nz = max(np == 0 ? 1 : 0, ((keys(p, from, gr.s1, stream(p, 1)) + PA_BN - 1) >> 7) - np);
+    }
+    nb = na + nz;
   }
-  // keys of the tile before those of sequence `until`
-  __device__ __forceinline__ int keys(const PaParams& p, const PaSource& from, int until) const {
+  // keys of a stream before those of sequence `until`
+  __device__ __forceinline__ int keys(const PaParams& p, const PaSource& from, int until, const PaStream& z) const {
     PaBatch x;
-    int at = gr.prefix;
+    int at = z.before;
 #pragma unroll 1
-    for (int base = first; base < until; base += 32) {
-      x.load(p, from, gr, base, t0, t1, at);
+    for (int base = z.first; base < until; base += 32) {
+      x.load(p, from, gr, base, z.t0, z.t1, at);
       if (until - base < 32) return __shfl_sync(~0u, x.at, until - base);
       at = x.total();
       if (!x.more) break;
     }
     return at;
   }
+  // block i of the tile: its stream and first key there (prefix blocks are the first stream's, and of both halves)
+  __device__ __forceinline__ int block(int i, int& at) const {
+    if (NH == 1 || i < np) {
+      at = i * PA_BN;
+      return 0;
+    }
+    const int x = i - np, a = na - np, both = min(a, nz), z = x < 2 * both ? x & 1 : a < nz;
+    at = (np + (x < 2 * both ? x >> 1 : x - both)) * PA_BN;
+    return z;
+  }
+  __device__ __forceinline__ bool is_for(int half, int i) const {
+    int at;
+    return NH == 1 || i < np || block(i, at) == half;
+  }
+  // how many of the blocks before block i are for a half
+  __device__ __forceinline__ int blocks_for(int half, int i) const {
+    if (NH == 1 || i <= np) return i;
+    const int x = i - np, a = na - np, both = min(a, nz);
+    return np + (x < 2 * both ? (x + 1 - half) >> 1 : both + ((a < nz) == half ? x - 2 * both : 0));
+  }
+  __device__ __forceinline__ int count_for(int half) const { return blocks_for(half, b + count()) - blocks_for(half, b); }
   __device__ __forceinline__ void set(const PaParams& p, const PaSharedPlace* pl) {
     h = pl[0].h;
     g = pl[0].g;
@@ -140,11 +186,8 @@ struct PaSharedCursor {
     eg = pl[1].g;
     ej = pl[1].j;
     eb = pl[1].b;
-    gr = pl[0].gr;
-    first = pl[0].first;
-    t0 = pl[0].t0;
-    t1 = pl[0].t1;
-    nb = pl[0].nb;
+    static_cast<PaSharedTile&>(*this) = pl[0].tile;
+    nb = na + nz;
   }
   __device__ __forceinline__ bool last_tile() const { return h == eh && g == eg && j == ej; }
   __device__ __forceinline__ int count() const { return last_tile() ? eb - b : nb - b; }
@@ -193,14 +236,14 @@ struct PaSharedCursor {
   __device__ __forceinline__ int tokens(const PaParams&) const { return t1 - t0; }
   __device__ __forceinline__ int shift(const PaParams&) const { return 0; }
 
-  // the range [lo, hi) of the tile's keys behind the prefix that packed token t (of this lane) sees
-  __device__ __forceinline__ void range(const PaParams& p, int t, int& lo, int& hi) const {
-    lo = hi = gr.prefix;
+  // the range [lo, hi) of a stream's keys behind the prefix that its packed token t (of this lane) sees
+  __device__ __forceinline__ void range(const PaParams& p, int half, int t, int& lo, int& hi) const {
+    const PaStream z = stream(p, half);
     PaBatch x;
-    int at = gr.prefix;
+    int at = lo = hi = z.before;
 #pragma unroll 1
-    for (int base = first; base < gr.s1; base += 32) {
-      x.load(p, pa_arrays(p), gr, base, t0, t1, at);
+    for (int base = z.first; base < gr.s1; base += 32) {
+      x.load(p, pa_arrays(p), gr, base, z.t0, z.t1, at);
       const int n = PaBatch::first_above(x.s.a + x.s.m, t), from = min(n, 31);
       const int a = __shfl_sync(~0u, x.s.a, from), m = __shfl_sync(~0u, x.s.m, from), len = __shfl_sync(~0u, x.s.len, from), k = __shfl_sync(~0u, x.at, from);
       if (n < 32 && t >= a && t < a + m) {
@@ -220,14 +263,17 @@ struct PaPiece {
 };
 template <int NH>
 struct PaSharedKeys {
-  PaBatch x;
-  int base, h, g, j;    // the batch's first sequence; of which tile
-  __device__ __forceinline__ PaSharedKeys() : base(0), h(-1), g(-1), j(-1) {}
-  // key v of the tile (a piece's first, of this lane; v does not decrease from call to call within a tile)
-  __device__ __forceinline__ PaPiece at(const PaParams& p, const PaSharedCursor<NH>& c, int v) {
+  PaBatch x, y;         // the batch of the stream of the last call, and the other stream's
+  int xb, yb;           // their first sequences
+  int z, h, g, j;       // which stream x is of; of which tile (h < 0: none yet)
+  __device__ __forceinline__ PaSharedKeys() : z(0), h(-1) {}
+  // the piece of block i that begins with its key `off` (of this lane); i does not decrease from call to call within a tile
+  __device__ __forceinline__ PaPiece at(const PaParams& p, const PaSharedCursor<NH>& c, int i, int off) {
     PaPiece r{INT_MIN, 0, 255};
-    int key = -1, row = -1, len = 0;
-    if (v < c.gr.prefix) {
+    int key = -1, row = -1, len = 0, v;
+    const int zi = c.block(i, v);
+    v += off;
+    if (i < c.np && v < c.gr.prefix) {
       key = v;
       row = c.gr.row;
       len = INT_MAX;
@@ -237,8 +283,21 @@ struct PaSharedKeys {
         h = c.h;
         g = c.g;
         j = c.j;
-        base = c.first;
-        x.load(p, pa_arrays(p), c.gr, base, c.t0, c.t1, c.gr.prefix);
+        xb = yb = -1;
+      }
+      if (NH == 2 && zi != z) {
+        z = zi;
+        const PaBatch t = x;
+        x = y;
+        y = t;
+        const int tb = xb;
+        xb = yb;
+        yb = tb;
+      }
+      const PaStream s = c.stream(p, z);
+      if (xb < 0) {
+        xb = s.first;
+        x.load(p, pa_arrays(p), c.gr, xb, s.t0, s.t1, s.before);
       }
       while (true) {
         const int n = PaBatch::first_above(x.end, v), from = min(n, 31);
@@ -250,8 +309,8 @@ struct PaSharedKeys {
         }
         if (!x.more || !__any_sync(~0u, key < 0)) break;
         const int at = x.total();
-        base += 32;
-        x.load(p, pa_arrays(p), c.gr, base, c.t0, c.t1, at);
+        xb += 32;
+        x.load(p, pa_arrays(p), c.gr, xb, s.t0, s.t1, at);
       }
     }
     if (key >= 0 && key < len) {
@@ -443,7 +502,7 @@ __device__ __noinline__ void pa_find_shared(const PaParams& p, PaSharedPlace* pl
       rem -= before + PA_TILE_KEYS;
     }
     cur.tile(p, from);
-    if (in_part) rem += cur.keys(p, from, i);
+    if (in_part) rem += cur.keys(p, from, i, PaStream{cur.first, cur.t0, cur.t1, cur.gr.prefix});
     // A cut in what the tile costs besides, or in a short tile, is one before the tile; one behind its blocks is before the next.  (Cuts
     // are 256 keys apart or more, which are at least 170 of a tile's and so another block: no two pieces start at the same block inside of
     // a tile, and a part that the join looks for has been written.)
@@ -460,11 +519,7 @@ __device__ __noinline__ void pa_find_shared(const PaParams& p, PaSharedPlace* pl
       pl[warp].g = end ? 0 : cur.g;
       pl[warp].j = end ? 0 : cur.j;
       pl[warp].b = b;
-      pl[warp].gr = cur.gr;
-      pl[warp].first = cur.first;
-      pl[warp].t0 = cur.t0;
-      pl[warp].t1 = cur.t1;
-      pl[warp].nb = cur.nb;
+      pl[warp].tile = cur;
       if (warp == 0)
         p.rec[c] = end ? PaRec{-1, 0, 0, 0, 0, 0} : PaRec{(long long)cur.h * p.c.total + cur.t0, b, cur.t0, cur.t1 - cur.t0, cur.h, pieces};
     }

@@ -8,9 +8,9 @@ namespace qe {
 // Where the keys of a row's tiles lie: a place for each, or one after the gap that a window leaves.
 template <int NH, int MODE>
 struct PaRowKeys {
-  // key v of the tile (a piece's first, of this lane)
-  __device__ __forceinline__ PaPiece at(const PaParams& p, const PaCursor<NH, MODE>& c, int v) const {
-    const int key = MODE == PA_WINDOW && v >= p.sa ? v + c.shift(p) : v;
+  // the piece of block i that begins with its key `off` (of this lane)
+  __device__ __forceinline__ PaPiece at(const PaParams& p, const PaCursor<NH, MODE>& c, int i, int off) const {
+    const int v = i * PA_BN + off, key = MODE == PA_WINDOW && v >= p.sa ? v + c.shift(p) : v;
     return PaPiece{key < c.q.s.len ? p.t.table[(long long)c.q.s.row * p.t.stride + (key >> p.pg.lgS)] : INT_MIN, key & (p.pg.S - 1), 255};
   }
 };
@@ -61,8 +61,8 @@ struct PaValid<PA_SHARED, SLOTS> {
 template <int NH, int MODE>
 struct PaSight {
   int vis, low, open, all_vis, all_low, end, gap;   // end: values from here on are nobody's; gap: as are those of [open, gap)
-  int mine0, mine1;                                 // shared: the warp's rows see own keys of [mine0, mine1), counted from the block's first
-  __device__ __forceinline__ PaSight(const PaParams& p, const typename PaWalk<NH, MODE>::Cursor& c, int t, bool live, bool any_live, int from) {
+  int mine0, mine1;                                 // shared: the warp's rows see own keys of [mine0, mine1) of their stream
+  __device__ __forceinline__ PaSight(const PaParams& p, const typename PaWalk<NH, MODE>::Cursor& c, int half, int t, bool live, bool any_live, int from) {
     constexpr int FAR = 1 << 30;
     open = low = gap = all_low = -FAR;
     if constexpr (MODE == PA_SHARED) {
@@ -70,14 +70,13 @@ struct PaSight {
       vis = FAR;
       if (any_live) {
         int lo, hi;
-        c.range(p, c.t0 + t, lo, hi);
+        c.range(p, half, c.t0 + t, lo, hi);
         if (live) {
           vis = hi - from;
           low = lo - from;
         }
-        const int block = c.b * PA_BN;
-        mine0 = __reduce_min_sync(~0u, live ? lo - block : FAR);
-        mine1 = __reduce_max_sync(~0u, live ? hi - block : -FAR);
+        mine0 = __reduce_min_sync(~0u, live ? lo : FAR);
+        mine1 = __reduce_max_sync(~0u, live ? hi : -FAR);
       }
       end = open;   // (own keys: PaValid)
     } else {
@@ -135,7 +134,7 @@ struct PaFewSight {
       every = len = c.gr.prefix;
       const int t = threadIdx.x & 31;
       int a, b;
-      c.range(p, c.t0 + t, a, b);
+      c.range(p, 0, c.t0 + t, a, b);
       const int have = c.tokens(p);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
