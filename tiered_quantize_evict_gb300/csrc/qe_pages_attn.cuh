@@ -49,6 +49,9 @@ struct PaParams {
   long long ots, ohs;
   int Hq, G, T, causal;
   int q_rows;              // rows of a query buffer
+  // Copies of keys and values.  Wide: a piece of a page with all its channels, and the heads of all pages as one axis of `all` places,
+  // head h of page i at place i of_page + h of_head.  Where that axis would be too long (odd strides): 8 tokens x 64 channels each.
+  int wide, of_page, of_head, all;
   int ctas;                // CTAs of the attention kernel: one per SM
   int expire;              // qe_debug_inject: 4 k + role, the k-th counted wait of these warps is taken as expired; 0: none
   float scale, scale2;     // of the logits; and times log2(e)
@@ -375,10 +378,10 @@ __device__ __forceinline__ void pa_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void pa_arrive(unsigned bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void pa_tma4(unsigned dst, const CUtensorMap* map, int x, int y, int z, int w, unsigned bar) {
+__device__ __forceinline__ void pa_tma5(unsigned dst, const CUtensorMap* map, int y, int z, int w, int v, unsigned bar) {   // x = 0
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void pa_tma3(unsigned dst, const CUtensorMap* map, int x, int y, int z, unsigned bar) {
@@ -495,10 +498,19 @@ __device__ __forceinline__ float2 pa_unpack(unsigned x) {
   return make_float2(bf16lo_to_f32(x), bf16hi_to_f32(x));
 }
 
-// shared-memory descriptors: 128-byte swizzle, 8-row groups 1024 bytes apart.  K-major operands (Q, K); and V with
-// channels as the rows of the operand (MN-major: 64 channels to a column block, blocks 128 tokens x 128 bytes apart).
-constexpr unsigned long long PA_DESC_K = (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-constexpr unsigned long long PA_DESC_V = (1024ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+// A slot of keys or values: groups of 8 tokens, in a group 64 channels after 64 channels (CB column blocks), 1024 bytes each (128-byte
+// swizzle).  So one copy brings all channels of a piece of a page: a copy costs some 100 cycles whatever its size, and with two for a
+// page of 16 tokens the copies were what bounded a block (32 of them 3100 cycles, 2048 new tokens over 32K 746 us; with pages of 64 tokens 630).
+constexpr int PA_CELL = 1024;
+// Shared-memory descriptors.  K-major operands: Q (groups of 8 rows side by side) and K; V with channels as the rows of the operand
+// (MN-major; the second stride is that of the column blocks), and the probabilities of qe_pages_few.cuh.
+constexpr unsigned long long PA_DESC = (1ull << 46) | (2ull << 61);
+constexpr unsigned long long PA_DESC_Q = PA_DESC | (1ull << 16) | (64ull << 32);
+template <int CB>
+constexpr unsigned long long PA_DESC_K = PA_DESC | (1ull << 16) | (64ull * CB << 32);
+template <int CB>
+constexpr unsigned long long PA_DESC_V = PA_DESC | (64ull << 16) | (64ull * CB << 32);
+constexpr unsigned long long PA_DESC_P = PA_DESC | (1024ull << 16) | (64ull << 32);
 
 // Attention of tiles of at most 16 rows (qe_pages_few.cuh).  With 17 to 32 rows as 32 columns it took 148 us where the one half of
 // qe_pages_halves.cuh takes 134 (8 drafts of 16 sequences of up to 16K tokens), so those stay there.

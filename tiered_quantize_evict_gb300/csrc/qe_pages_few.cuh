@@ -129,21 +129,17 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     // ============================== keys and values
     Cursor cur;
     cur.set(p, s_place);
-    const int rows = min(p.pg.S, PA_BN);               // tokens of a piece: a page, or a block's part of one
-    const int np = PA_BN / rows;
-    const int piece = lane % np, cb = lane / np;       // lane -> (page of the block, column block)
-    const bool mine = cb < Sh::CB;
+    const PaCopy<Sh::CB> copy(p);
     // this lane's piece, its entry loaded a block before it is looked at
     typename PaWalk<1, MODE>::Keys keys;
     int slot = 0, ph = 1, issued = 0, left = cur.count();
-    PaPiece next = keys.at(p, cur, cur.b, piece * rows);
+    PaPiece next = keys.at(p, cur, cur.b, copy.piece * copy.rows);
     int till = PaWait::counted(p, PaWait::KEYS);
     bool ok = true;
 #pragma unroll 1
     while (left > 0 && ok) {
-      const int tk = next.tok, h = cur.h;
+      const int tk = next.tok, h = cur.h, now = next.entry;
       const bool there = next.entry >= 0 && next.entry < p.pg.P;
-      const int now = there ? next.entry : p.pg.P;       // out of the pool: the copy fills zeros
       if (!there && next.entry != INT_MIN) pages_report(p.pg, QE_PAGES_ERR_PAGE);
       const int valid = there ? next.valid : 255;
       ++cur.b;
@@ -151,7 +147,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         cur.next_tile(p);
         left = cur.count();
       }
-      if (left > 0) next = keys.at(p, cur, cur.b, piece * rows);
+      if (left > 0) next = keys.at(p, cur, cur.b, copy.piece * copy.rows);
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
         ok = ok && wait.count(till, smem_u32(&b_kempty[slot]), ph);
@@ -161,12 +157,12 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         }
         const unsigned full = smem_u32(&b_kfull[slot]);
         if constexpr (MODE == PA_SHARED) {   // (told by the values' arrival)
-          if (kv && lane < 8) s_valid.set(slot, lane, lane < np ? valid : 255);
+          if (kv && lane < copy.pieces) s_valid.set(slot, lane, valid);
           __syncwarp();
         }
         if (lane == 0) mbar_expect_tx(full, Sh::TILE);
         __syncwarp();
-        if (mine) pa_tma4(sm_kv + slot * Sh::TILE + cb * 16384 + piece * rows * 128, kv ? &mv : &mk, cb * 64, tk, h, now, full);
+        if (copy.mine) copy.send(p, kv ? &mv : &mk, sm_kv + slot * Sh::TILE, there, now, h, tk, full);
         ++issued;
         if (++slot == NS) {
           slot = 0;
@@ -213,10 +209,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         if (!__all_sync(~0u, ok)) break;
         pa_fence_after();
         if (pa_elect()) {   // S n = K Q^T
-          const unsigned long long a = PA_DESC_K | ((sm_kv + kslot * Sh::TILE) >> 4), b = PA_DESC_K | ((sm_q + qb * Sh::Q_BUF) >> 4);
+          const unsigned long long a = PA_DESC_K<Sh::CB> | ((sm_kv + kslot * Sh::TILE) >> 4), b = PA_DESC_Q | ((sm_q + qb * Sh::Q_BUF) >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            pa_mma_ss(tm + (n & 1) * N, a + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), b + (((k >> 2) * Sh::Q_CB + (k & 3) * 32) >> 4), ID_S,
+            pa_mma_ss(tm + (n & 1) * N, a + (((k >> 2) * PA_CELL + (k & 3) * 32) >> 4), b + (((k >> 2) * Sh::Q_CB + (k & 3) * 32) >> 4), ID_S,
                       k > 0);
           pa_commit(smem_u32(&b_s[n & 1]));
           pa_commit(smem_u32(&b_kempty[kslot]));
@@ -233,9 +229,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         if (!__all_sync(~0u, ok)) break;
         pa_fence_after();
         if (pa_elect()) {   // O += V^T P^T
-          const unsigned long long a = PA_DESC_V | ((sm_kv + slot * Sh::TILE) >> 4), b = PA_DESC_V | ((sm_p + pb * 64) >> 4);
+          const unsigned long long a = PA_DESC_V<Sh::CB> | ((sm_kv + slot * Sh::TILE) >> 4), b = PA_DESC_P | ((sm_p + pb * 64) >> 4);
 #pragma unroll
-          for (int k = 0; k < PA_BN / 16; ++k) pa_mma_ss(tm + Sh::TM_O, a + k * 128, b + k * 128, ID_O, !was_first || k > 0);
+          for (int k = 0; k < PA_BN / 16; ++k) pa_mma_ss(tm + Sh::TM_O, a + k * 128 * Sh::CB, b + k * 128, ID_O, !was_first || k > 0);
           pa_commit(smem_u32(&b_kempty[slot]));
           pa_commit(smem_u32(&b_o[pb]));
         }
@@ -320,12 +316,12 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             const int place = 2 * n + 1, slot = place % NS;
             wait(smem_u32(&b_kfull[slot]), (place / NS) & 1);
             if (MODE == PA_SHARED ? s_valid.none(slot, kl, p) : sight.none(key)) {
-              const unsigned row = sm_kv + slot * Sh::TILE + kl * 128;
+              const unsigned row = sm_kv + slot * Sh::TILE + pa_slot_row<Sh::CB>(kl);
 #pragma unroll 1
               for (int cb = 0; cb < Sh::CB; ++cb)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row + cb * 16384 + e * 16), "r"(0) : "memory");
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row + cb * PA_CELL + e * 16), "r"(0) : "memory");
             }
             __syncwarp();
           }

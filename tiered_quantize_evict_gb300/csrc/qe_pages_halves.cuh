@@ -180,21 +180,17 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
       // ============================== keys and values
       Cursor cur;
       cur.set(p, s_place);
-      const int rows = min(p.pg.S, PA_BN);               // tokens of a piece: a page, or a block's part of one
-      const int np = PA_BN / rows;
-      const int piece = lane % np, cb = lane / np;       // lane -> (page of the block, column block)
-      const bool mine = cb < Sh::CB;
+      const PaCopy<Sh::CB> copy(p);
       // this lane's piece, its entry loaded a block before it is looked at
       typename PaWalk<NH, MODE>::Keys keys;
       int slot = 0, ph = 1, issued = 0, left = cur.count();
-      PaPiece next = keys.at(p, cur, cur.b, piece * rows);
+      PaPiece next = keys.at(p, cur, cur.b, copy.piece * copy.rows);
       int till = PaWait::counted(p, PaWait::KEYS);
       bool ok = true;
 #pragma unroll 1
       while (left > 0 && ok) {
-        const int tk = next.tok, h = cur.h;
+        const int tk = next.tok, h = cur.h, now = next.entry;
         const bool there = next.entry >= 0 && next.entry < p.pg.P;
-        const int now = there ? next.entry : p.pg.P;       // out of the pool: the copy fills zeros
         if (!there && next.entry != INT_MIN) pages_report(p.pg, QE_PAGES_ERR_PAGE);
         const int valid = there ? next.valid : 255;
         ++cur.b;
@@ -202,7 +198,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
           cur.next_tile(p);
           left = cur.count();
         }
-        if (left > 0) next = keys.at(p, cur, cur.b, piece * rows);
+        if (left > 0) next = keys.at(p, cur, cur.b, copy.piece * copy.rows);
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           ok = ok && wait.count(till, smem_u32(&b_kempty[slot]), ph);
@@ -212,12 +208,12 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
           }
           const unsigned full = smem_u32(&b_kfull[slot]);
           if constexpr (MODE == PA_SHARED) {   // (told by the values' arrival)
-            if (kv && lane < 8) s_valid.set(slot, lane, lane < np ? valid : 255);
+            if (kv && lane < copy.pieces) s_valid.set(slot, lane, valid);
             __syncwarp();
           }
           if (lane == 0) mbar_expect_tx(full, Sh::TILE);
           __syncwarp();
-          if (mine) pa_tma4(sm_kv + slot * Sh::TILE + cb * 16384 + piece * rows * 128, kv ? &mv : &mk, cb * 64, tk, h, now, full);
+          if (copy.mine) copy.send(p, kv ? &mv : &mk, sm_kv + slot * Sh::TILE, there, now, h, tk, full);
           ++issued;
           if (++slot == NS) {
             slot = 0;
@@ -249,10 +245,10 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
       };
       const unsigned t_o = tm + Sh::TM_O + h * D;
       auto qk = [&](int qb, int sb, int kslot, bool q_done) {   // S sb = Q qb K^T (by one lane)
-        const unsigned long long a = PA_DESC_K | ((sm_q + qb * q_buf) >> 4), b = PA_DESC_K | ((sm_kv + kslot * Sh::TILE) >> 4);
+        const unsigned long long a = PA_DESC_Q | ((sm_q + qb * q_buf) >> 4), b = PA_DESC_K<Sh::CB> | ((sm_kv + kslot * Sh::TILE) >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const unsigned o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4, oq = ((k >> 2) * q_cb + (k & 3) * 32) >> 4;
+          const unsigned o = ((k >> 2) * PA_CELL + (k & 3) * 32) >> 4, oq = ((k >> 2) * q_cb + (k & 3) * 32) >> 4;
           if (NH == 2 && k == D / 16 - 2) pa_arrive(smem_u32(&b_turn[h ^ 1]));   // (its first product is issued by when these are done)
           pa_mma_ss(tm + sb * 128, a + oq, b + o, ID_S, k > 0);
         }
@@ -262,14 +258,14 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
       };
       // O += P sb V over one part of each 64 keys (by one lane)
       auto pv = [&](int part, int sb, int vslot, bool acc) {
-        const unsigned long long b = PA_DESC_V | ((sm_kv + vslot * Sh::TILE) >> 4);
+        const unsigned long long b = PA_DESC_V<Sh::CB> | ((sm_kv + vslot * Sh::TILE) >> 4);
         constexpr int KS = 4 / PARTS;   // steps of 16 keys of a part of 64
 #pragma unroll
         for (int rest = 0; rest < (NH == 1 ? 2 : 1); ++rest)   // (with the remainders of P)
 #pragma unroll
           for (int i = 0; i < 2 * KS; ++i) {
             const int k = i / KS * 4 + part * KS + i % KS;
-            pa_mma_ts(t_o, tm + sb * 128 + rest * 64 + k * 8, b + k * 128, ID_O, acc || rest > 0 || i > 0);
+            pa_mma_ts(t_o, tm + sb * 128 + rest * 64 + k * 8, b + k * 128 * Sh::CB, ID_O, acc || rest > 0 || i > 0);
           }
       };
 #pragma unroll 1
@@ -489,12 +485,12 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
             const int place = 2 * n + 1, slot = place % NS;
             wait(smem_u32(&b_kfull[slot]), (place / NS) & 1);
             if (MODE == PA_SHARED ? s_valid.none(slot, r, p) : sight.none(at + r)) {
-              const unsigned row = sm_kv + slot * Sh::TILE + r * 128;
+              const unsigned row = sm_kv + slot * Sh::TILE + pa_slot_row<Sh::CB>(r);
 #pragma unroll 1
               for (int cb = 0; cb < Sh::CB; ++cb)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row + cb * 16384 + e * 16), "r"(0) : "memory");
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(row + cb * PA_CELL + e * 16), "r"(0) : "memory");
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();

@@ -1,6 +1,7 @@
 // qe_pages_launch.cuh -- the launch of an attention over the cached pages, of one mode (PaMode).
 #pragma once
 #include <atomic>
+#include <numeric>
 
 #include "qe_pages_few.cuh"
 #include "qe_pages_halves.cuh"
@@ -104,7 +105,7 @@ static cudaError_t launch_pages_mode(const PagesAttendParams& a, const PagesWind
 
   CUtensorMap maps[3];
   const CUtensorMapDataType ty = fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   // (a driver call: a thread that has made none of the runtime's has no context yet, which cudaSetDevice gives it)
   auto encode = [&](CUtensorMap* map, int rank, uint16_t* base, const cuuint64_t* dim, const cuuint64_t* str, const cuuint32_t* box) {
     auto call = [&] {
@@ -122,11 +123,21 @@ static cudaError_t launch_pages_mode(const PagesAttendParams& a, const PagesWind
     const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.T};
     if (!encode(&maps[0], 3, const_cast<uint16_t*>(a.q), dim, str, box)) return cudaErrorInvalidValue;
   }
+  // keys and values (PaParams); `unit`: the heads' places are so many elements apart
+  const long long unit = g.hs && g.ps ? std::gcd(g.hs, g.ps) : (g.hs ? g.hs : (g.ps ? g.ps : g.D));
+  const long long places = (g.P - 1) * (g.ps / unit) + (g.H - 1) * (g.hs / unit) + 1;
+  p.wide = places <= INT_MAX;
+  p.of_page = (int)(g.ps / unit);
+  p.of_head = (int)(g.hs / unit);
+  p.all = (int)places;
   for (int i = 0; i < 2; ++i) {
-    const cuuint64_t dim[4] = {(cuuint64_t)g.D, (cuuint64_t)g.S, (cuuint64_t)g.H, (cuuint64_t)g.P};
-    const cuuint64_t str[3] = {bytes(g.ts), bytes(g.hs), bytes(g.ps)};
-    const cuuint32_t box[4] = {64, (cuuint32_t)(g.S < 128 ? g.S : 128), 1, 1};
-    if (!encode(&maps[1 + i], 4, (i ? g.v : g.k) + a.layer * g.ls, dim, str, box)) return cudaErrorInvalidValue;
+    uint16_t* base = (i ? g.v : g.k) + a.layer * g.ls;
+    const cuuint32_t cb = (cuuint32_t)(g.D / 64), rows = (cuuint32_t)(g.S < PA_BN ? g.S : PA_BN);
+    const cuuint64_t wide_dim[5] = {64, 8, cb, (cuuint64_t)(g.S / 8), (cuuint64_t)places}, wide_str[4] = {bytes(g.ts), 128, bytes(8 * g.ts), bytes(unit)};
+    const cuuint32_t wide_box[5] = {64, 8, cb, rows / 8, 1};
+    const cuuint64_t dim[5] = {64, cb, (cuuint64_t)g.S, (cuuint64_t)g.H, (cuuint64_t)g.P}, str[4] = {128, bytes(g.ts), bytes(g.hs), bytes(g.ps)};
+    const cuuint32_t box[5] = {64, 1, 8, 1, 1};
+    if (!(p.wide ? encode(&maps[1 + i], 5, base, wide_dim, wide_str, wide_box) : encode(&maps[1 + i], 5, base, dim, str, box))) return cudaErrorInvalidValue;
   }
   if (one && p.T * p.G <= PAGES_FEW_ROWS) {
     if (g.D == 128) return fp16 ? few_t<128, true, MODE>(p, maps, device, st) : few_t<128, false, MODE>(p, maps, device, st);

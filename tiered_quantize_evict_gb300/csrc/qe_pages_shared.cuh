@@ -316,7 +316,7 @@ struct PaSharedKeys {
     if (key >= 0 && key < len) {
       r.entry = p.t.table[(long long)row * p.t.stride + (key >> p.pg.lgS)];
       r.tok = key & (p.pg.S - 1);
-      if (len - key < pa_piece(p)) r.valid = len - key;
+      if (len - key < (p.wide ? pa_piece(p) : 8)) r.valid = len - key;
     }
     return r;
   }

@@ -40,6 +40,33 @@ struct PaWalk<NH, PA_SHARED> {
   }
 };
 
+// What a warp's lane copies of each block: a piece of a page, in a wide copy all its channels, else 64 of them.
+template <int CB>
+struct PaCopy {
+  int rows, piece, cb;     // tokens; which of the block's pieces, and column block
+  int pieces;              // of a block
+  bool mine;
+  __device__ __forceinline__ PaCopy(const PaParams& p) {
+    const int lane = threadIdx.x & 31;
+    rows = p.wide ? min(p.pg.S, PA_BN) : 8;
+    pieces = PA_BN / rows;
+    piece = lane % pieces;
+    cb = lane / pieces;
+    mine = cb < (p.wide ? 1 : CB);
+  }
+  // entry: the page, or any other number for zeros
+  __device__ __forceinline__ void send(const PaParams& p, const CUtensorMap* map, unsigned slot, bool there, int page, int head, int tok, unsigned bar) const {
+    const unsigned to = slot + piece * rows * 128 * CB + cb * PA_CELL;
+    if (p.wide) pa_tma5(to, map, 0, 0, tok >> 3, there ? page * p.of_page + head * p.of_head : p.all, bar);   // (out of the pool: zeros)
+    else pa_tma5(to, map, cb, tok, head, there ? page : p.pg.P, bar);
+  }
+};
+// a token's row in a slot, in bytes; its channels from 64 on are PA_CELL further
+template <int CB>
+__device__ __forceinline__ unsigned pa_slot_row(int r) {
+  return (r >> 3) * (CB * PA_CELL) + (r & 7) * 128;
+}
+
 // How many rows of each of a slot's pieces hold values (shared prefixes: pieces of many sequences end where they like).
 template <int MODE, int SLOTS>
 struct PaValid {
@@ -47,11 +74,11 @@ struct PaValid {
 };
 template <int SLOTS>
 struct PaValid<PA_SHARED, SLOTS> {
-  uint8_t rows[SLOTS][8];
+  uint8_t rows[SLOTS][16];
   __device__ __forceinline__ void set(int slot, int piece, int n) { rows[slot][piece] = (uint8_t)n; }
   __device__ __forceinline__ bool none(int slot, int r, const PaParams& p) const {
-    const int n = pa_piece(p);
-    return (r & (n - 1)) >= rows[slot][r / n];
+    const int lg = p.wide ? min(p.pg.lgS, 7) : 3;
+    return (r & ((1 << lg) - 1)) >= rows[slot][r >> lg];
   }
 };
 
