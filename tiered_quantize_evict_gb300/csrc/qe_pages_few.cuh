@@ -466,6 +466,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       pf_sync();   // O and the sums are read whole before the next tile's
     }
   }
+  if constexpr (MODE == PA_SHARED)
+    if (blockIdx.x == 0 && aux == 2) pa_check_shared(p);
   __syncthreads();
   if (aux == 3) {
     pa_fence_after();

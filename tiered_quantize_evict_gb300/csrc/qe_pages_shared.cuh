@@ -8,15 +8,11 @@
 // blocks behind the prefix come from both in turn, and each is for its half alone: the other half's softmax and products are at the
 // block before and the one behind meanwhile (a block that one half is at and the other waits for took 2.0 us, where reading it takes 1.4).
 //
-// The line is, for each KV head, the groups' tiles in order.  It is measured in keys, sequence by sequence: what a tile costs besides its
-// blocks and the prefix count where the tile begins, own keys where they are.  (Only the cuts go by this measure, and every CTA takes it alike; a
-// walk counts the tiles' own blocks.)
+// The line is, for each KV head, the groups' tiles in order, each as long as its blocks and what it costs besides.
 #pragma once
 #include "qe_pages_attn.cuh"
 
 namespace qe {
-
-constexpr int PA_TILE_KEYS = PA_TILE_COST * PA_BN;
 
 // Where groups and sequences are looked up: in the call's arrays (row and len NULL), or in a copy of what they come to.
 struct PaSource {
@@ -113,8 +109,6 @@ struct PaSharedTile {
 struct PaSharedPlace {
   int h, g, j, b;      // KV head (that of the end of the line: their number), group, tile of the group, block
   PaSharedTile tile;   // what a walk from here on starts with
-  int i;               // (while it is being found) sequence,
-  long long rem;       // and how far behind its start on a head's line
   __device__ __forceinline__ bool before(const PaSharedPlace& o) const {
     return h != o.h ? h < o.h : (g != o.g ? g < o.g : (j != o.j ? j < o.j : b < o.b));
   }
@@ -322,39 +316,59 @@ struct PaSharedKeys {
   }
 };
 
-// Every CTA finds its piece, as pa_find does.  `space` is shared memory for PA_FIND_INTS(NT) numbers: where there is a thread for each
-// sequence and group, what the arrays hold is read once, side by side, and looked up there (a call over one group of 64 sequences: the
-// piece is known after 4.5 us instead of 9).
-constexpr int PA_FIND_INTS(int nt) { return 5 * nt + 2; }
+// Reports what a call got wrong, by a warp of the first CTA that has nothing else to do.
+static __device__ __noinline__ void pa_check_shared(const PaParams& p) {
+  const int lane = threadIdx.x & 31;
+  for (int k = lane; k < p.gr.n; k += 32) {
+    const int a = p.gr.start[k], b = p.gr.start[k + 1], want = p.gr.prefix[k];
+    bool bad = a < 0 || b < a || b > p.c.n || (k == 0 && a != 0) || (k == p.gr.n - 1 && b != p.c.n);
+    if (!bad && a < b) bad = want < 0 || want > row_len(p.pg, p.t, p.c.rows ? p.c.rows[a] : a, false);
+    if (bad) pages_report(p.pg, QE_PAGES_ERR_ROW);
+  }
+  for (int i = lane; i < p.c.n; i += 32) {
+    const SeqInfo s = seq_info(p.pg, p.t, p.c, i, true);
+    int lo = 0, hi = p.gr.n;         // the last group that does not begin behind the sequence
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.gr.start[mid] <= i) lo = mid;
+      else hi = mid;
+    }
+    const int whole = max(p.gr.prefix[lo], 0) & -p.pg.S;
+    if (s.m > 0 && whole > 0 && whole > (p.causal ? s.len - s.m : s.len)) pages_report(p.pg, QE_PAGES_ERR_ROW);
+  }
+}
+
+// Every CTA finds its piece, as pa_find does: the groups' numbers of tiles, then the tiles, a warp for each, then the two cuts among
+// them.  `space` is shared memory for pa_find_ints(NT) numbers.  Where there is a thread for each sequence and group, what the arrays hold
+// is read once, side by side, and looked up there.  (Bound by fetching its instructions, once in a launch, and by latency: the same with a
+// line of sequences, whose tiles then had to be found, took 10 us for one group of 64.)
+constexpr int PA_TILE_INTS = 2 + sizeof(PaSharedTile) / sizeof(int);   // group, tile of the group, the tile
+constexpr int pa_find_ints(int nt) { return 6 * nt + 3 + nt * PA_TILE_INTS; }
+// a tile counts as so many blocks at most (a row of 2^27 tokens), so that a block's tiles are added up in 32 bits
+constexpr int PA_MOST_BLOCKS = 1 << 20;
 template <int NH, int NT>
-__device__ __noinline__ void pa_find_shared(const PaParams& p, PaSharedPlace* pl, long long* s_w, int* space) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tt = NH * p.T, piece = pa_piece(p);
+__device__ __noinline__ void pa_find_shared(const PaParams& p, PaSharedPlace* pl, int* s_w, int* space) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tt = NH * p.T, c = blockIdx.x;
   constexpr int W = NT / 32;
-  const int c = blockIdx.x;
-  auto scan = [&](long long x, long long& total) {
-    long long y = x;
+  int *start = space, *prefix = start + NT + 1, *q_start = prefix + NT, *row = q_start + NT + 1, *len = row + NT, *s_first = len + NT,
+      *s_tile = s_first + NT + 1;
+  auto scan = [&](int x, int& total) {   // sum of the threads' before this one
+    int y = x;
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) {
-      const long long z = __shfl_up_sync(~0u, y, k);
+      const int z = __shfl_up_sync(~0u, y, k);
       if (lane >= k) y += z;
     }
     if (lane == 31) s_w[warp] = y;
     __syncthreads();
-    long long before = 0, all = 0;
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      const long long z = s_w[k];
-      if (k < warp) before += z;
-      all += z;
-    }
-    total = all;
+    int v = lane < W ? s_w[lane] : 0;
+    const int before = __reduce_add_sync(~0u, lane < warp ? v : 0);
+    total = __reduce_add_sync(~0u, v);
     __syncthreads();
     return before + y - x;
   };
   PaSource from = pa_arrays(p);
-  const bool held = p.c.n <= NT && p.gr.n <= NT;
-  if (held) {
-    int *start = space, *prefix = start + NT + 1, *q_start = prefix + NT, *row = q_start + NT + 1, *len = row + NT;
+  if (p.c.n <= NT && p.gr.n <= NT) {
     if (tid < p.gr.n) {
       start[tid + 1] = from.start[tid + 1];
       prefix[tid] = from.prefix[tid];
@@ -369,161 +383,90 @@ __device__ __noinline__ void pa_find_shared(const PaParams& p, PaSharedPlace* pl
       start[0] = from.start[0];
       q_start[0] = from.q_start[0];
     }
-    __syncthreads();
     from = PaSource{start, prefix, q_start, row, len};
   }
-  auto group_of = [&](int i) {   // the last that does not begin behind sequence i
-    int lo = 0, hi = p.gr.n;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (from.start[mid] <= i) lo = mid;
-      else hi = mid;
-    }
-    return lo;
-  };
-  // A sequence on a head's line: what it has in a tile that began before (part), then the tiles that begin in it
-  struct Part {
-    PaGroup g;
-    PaMember s;
-    int own, j, c0, tiles;       // own keys before the chunk's (and half a piece); the tile it begins in; its tokens in a tile that began before; tiles that begin in it
-    long long part;
-  };
-  auto on_line = [&](const PaGroup& g, const PaMember& s) {
-    Part r;
-    r.g = g;
-    r.s = s;
-    r.own = max(0, (p.causal ? s.len - s.m : s.len) - g.prefix) + piece / 2;
-    const int o = s.a - g.q0;
-    r.j = o / tt;
-    const int into = o - r.j * tt;
-    r.c0 = into > 0 ? min(s.m, tt - into) : 0;
-    r.part = r.c0 > 0 ? r.own + (p.causal ? r.c0 : 0) : 0;
-    r.tiles = (s.m - r.c0 + tt - 1) / tt;
-    r.j += into > 0;
-    return r;
-  };
-  auto tiles_before = [&](const Part& r, int k) {   // of the tiles that begin in the sequence
-    long long x = (long long)k * (PA_TILE_KEYS + r.g.prefix + r.own);
-    if (p.causal) x += (long long)k * r.c0 + (long long)k * (k + 1) / 2 * tt;
-    return x;
-  };
-  auto length = [&](int i, bool report) {
-    if (i >= p.c.n) return 0ll;
-    const int gi = group_of(i);
-    const PaGroup g = pa_group(p, from, gi);
-    if (report) {
-      const SeqInfo s = seq_info(p.pg, p.t, p.c, i, true);
-      if (s.m > 0 && g.prefix > 0 && g.prefix > (p.causal ? s.len - s.m : s.len)) pages_report(p.pg, QE_PAGES_ERR_ROW);
-    }
-    if (i < g.s0 || i >= g.s1) return 0ll;   // (of no group)
-    const PaMember s = pa_member(p, from, g, i);
-    if (s.m == 0) return 0ll;
-    const Part r = on_line(g, s);
-    if (r.tiles == 0) return r.part;
-    return r.part + tiles_before(r, r.tiles - 1) + PA_TILE_KEYS + g.prefix + r.own + (p.causal ? s.m : 0);
-  };
-  if (c == 0) {
-    for (int k = tid; k < p.gr.n; k += NT) {
-      const int a = p.gr.start[k], b = p.gr.start[k + 1];
-      bool bad = a < 0 || b < a || b > p.c.n || (k == 0 && a != 0) || (k == p.gr.n - 1 && b != p.c.n);
-      if (!bad && a < b) {
-        const int want = p.gr.prefix[k];
-        bad = want < 0 || want > row_len(p.pg, p.t, p.c.rows ? p.c.rows[a] : a, false);
-      }
-      if (bad) pages_report(p.pg, QE_PAGES_ERR_ROW);
-    }
-  }
-  if (tid < 2) pl[tid].h = p.pg.H, pl[tid].g = pl[tid].j = pl[tid].b = 0, pl[tid].i = -1;
-  // one pass where there is a thread for each sequence, else two
-  long long line, x = length(tid, c == 0), pre = scan(x, line);
+  if (tid < 2) pl[tid].h = p.pg.H, pl[tid].g = pl[tid].j = pl[tid].b = 0;
+  __syncthreads();
+  long long line = 0;
+  int pieces = 0, head[2] = {p.pg.H, p.pg.H};
+  long long cut[2] = {0, 0};
+  // one pass over the tiles where each has a thread; else the line is measured in a first
 #pragma unroll 1
-  for (int base = NT; base < p.c.n; base += NT) {
-    long long tot;
-    scan(length(base + tid, c == 0), tot);
-    line += tot;
-  }
-  const long long all = line * p.pg.H, most = all / (PA_LEAST * PA_BN);
-  const int pieces = most < 1 ? 1 : (most > gridDim.x ? (int)gridDim.x : (int)most);
-  if (c < pieces && all > 0) {
-    const long long each = div_ll(all, pieces);
-    const int over = (int)(all - each * pieces);
-    long long cut[2];
-    int head[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const long long to = each * (c + k) + over * (c + k) / pieces;
-      head[k] = (int)div_ll(to, line);
-      cut[k] = to - head[k] * line;
-    }
+  for (int pass = 0; pass < 2; ++pass) {
     long long at = 0;
 #pragma unroll 1
-    for (int base = 0; base < p.c.n; base += NT) {
-      if (p.c.n > NT) {
-        long long tot;
-        x = length(base + tid, false);
-        pre = at + scan(x, tot);
-        at += tot;
+    for (int gb = 0; gb < p.gr.n; gb += NT) {
+      int tiles = 0, all_tiles;
+      if (gb + tid < p.gr.n) {
+        const PaGroup g = pa_group(p, from, gb + tid);
+        tiles = (g.q1 - g.q0 + tt - 1) / tt;
       }
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (head[k] < p.pg.H && cut[k] >= pre && cut[k] < pre + x) {
-          pl[k].h = head[k];
-          pl[k].i = base + tid;
-          pl[k].rem = cut[k] - pre;
+      const int mine = scan(tiles, all_tiles);
+      s_first[tid + 1] = mine + tiles;
+      if (tid == 0) s_first[0] = 0;
+      __syncthreads();
+#pragma unroll 1
+      for (int xb = 0; xb < all_tiles; xb += NT) {
+#pragma unroll 1
+        for (int x = xb + warp; x < min(all_tiles, xb + NT); x += W) {
+          const int k = pages_count_below(s_first + 1, NT, x);
+          PaSharedCursor<NH> cur;
+          cur.j = x - s_first[k];
+          cur.gr = pa_group(p, from, gb + k);
+          cur.tile(p, from);
+          if (lane == 0) {
+            int* to = s_tile + (x - xb) * PA_TILE_INTS;
+            to[0] = gb + k;
+            to[1] = cur.j;
+            *reinterpret_cast<PaSharedTile*>(to + 2) = cur;
+          }
         }
-    }
-  } else if (tid == 0) {
-    p.rec[c] = PaRec{-1, 0, 0, 0, 0, 0};
-  }
-  __syncthreads();
-  if (warp < 2 && pl[warp].i >= 0) {
-    const int i = pl[warp].i;
-    long long rem = pl[warp].rem;
-    PaSharedCursor<NH> cur;
-    cur.g = group_of(i);
-    cur.gr = pa_group(p, from, cur.g);
-    const Part r = on_line(cur.gr, pa_member(p, from, cur.gr, i));
-    const bool in_part = rem < r.part;
-    if (in_part) {
-      cur.j = r.j - 1;
-    } else {
-      rem -= r.part;
-      int lo = 0, hi = r.tiles;   // the last tile that begins at or before rem: 32 places a round
-      long long before = 0;
-      while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32, cand = lo + lane * step;
-        const long long at = cand < hi ? tiles_before(r, cand) : LLONG_MAX;
-        const int top = 31 - __clz(__ballot_sync(~0u, at <= rem));
-        before = __shfl_sync(~0u, at, top);
-        lo += top * step;
-        hi = min(hi, lo + step);
+        __syncthreads();
+        const int* info = s_tile + tid * PA_TILE_INTS;
+        const PaSharedTile* t = reinterpret_cast<const PaSharedTile*>(info + 2);
+        const int nb = xb + tid < all_tiles ? min(t->na + t->nz, PA_MOST_BLOCKS) : 0;
+        int sum;
+        const int len = nb > 0 ? PA_TILE_COST + nb : 0, before = scan(len, sum);
+        const bool once = p.gr.n <= NT && all_tiles <= NT;
+        if (pass == 0 && once) line = sum;
+        if ((pass == 0 && once) || (pass == 1 && pieces == 0)) {   // the line is known: the cuts
+          const long long all = line * p.pg.H, most = all / PA_LEAST;
+          pieces = most < 1 ? 1 : (most > gridDim.x ? (int)gridDim.x : (int)most);
+          if (c < pieces && all > 0) {
+            const long long each = div_ll(all, pieces);
+            const int over = (int)(all - each * pieces);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const long long to = each * (c + k) + over * (c + k) / pieces;
+              head[k] = (int)div_ll(to, line);
+              cut[k] = to - head[k] * line;
+            }
+          }
+        }
+        if (once || pass == 1) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (head[k] < p.pg.H && cut[k] >= at + before && cut[k] < at + before + len) {
+              // a cut in what the tile costs besides, or in a short tile, is one before the tile
+              const int rem = (int)(cut[k] - at) - before - PA_TILE_COST, b = nb <= PA_WHOLE ? 0 : max(0, rem);
+              pl[k].h = head[k];
+              pl[k].g = info[0];
+              pl[k].j = info[1];
+              pl[k].b = b;
+              pl[k].tile = *t;
+              if (k == 0) p.rec[c] = PaRec{(long long)head[0] * p.c.total + t->t0, b, t->t0, t->t1 - t->t0, head[0], pieces};
+            }
+        }
+        at += sum;
+        if (once) pass = 2;
+        __syncthreads();   // (s_tile is read)
       }
-      cur.j = r.j + lo;
-      rem -= before + PA_TILE_KEYS;
+      if (all_tiles == 0 && p.gr.n <= NT) pass = 2;
     }
-    cur.tile(p, from);
-    if (in_part) rem += cur.keys(p, from, i, PaStream{cur.first, cur.t0, cur.t1, cur.gr.prefix});
-    // A cut in what the tile costs besides, or in a short tile, is one before the tile; one behind its blocks is before the next.  (Cuts
-    // are 256 keys apart or more, which are at least 170 of a tile's and so another block: no two pieces start at the same block inside of
-    // a tile, and a part that the join looks for has been written.)
-    int b = cur.nb <= PA_WHOLE || rem <= 0 ? 0 : (int)(rem >> 7);
-    cur.h = pl[warp].h;
-    cur.eh = -1;
-    if (b >= cur.nb) {
-      cur.next_tile(p);
-      b = 0;
-    }
-    const bool end = cur.h >= p.pg.H;
-    if (lane == 0) {
-      pl[warp].h = cur.h;
-      pl[warp].g = end ? 0 : cur.g;
-      pl[warp].j = end ? 0 : cur.j;
-      pl[warp].b = b;
-      pl[warp].tile = cur;
-      if (warp == 0)
-        p.rec[c] = end ? PaRec{-1, 0, 0, 0, 0, 0} : PaRec{(long long)cur.h * p.c.total + cur.t0, b, cur.t0, cur.t1 - cur.t0, cur.h, pieces};
-    }
+    line = pass == 0 ? at : line;
+    if (pass == 0 && line == 0) break;
   }
+  if (tid == 0 && (line == 0 || c >= pieces)) p.rec[c] = PaRec{-1, 0, 0, 0, 0, 0};
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (copies go where `space` is)
   __syncthreads();
 }

@@ -35,7 +35,7 @@ struct PaWalk<NH, PA_SHARED> {
   using Keys = PaSharedKeys<NH>;
   template <int NT>
   static __device__ __forceinline__ bool find(const PaParams& p, Place* pl, long long* s_w, int* space) {
-    pa_find_shared<NH, NT>(p, pl, s_w, space);
+    pa_find_shared<NH, NT>(p, pl, reinterpret_cast<int*>(s_w), space);
     return pl[0].before(pl[1]);
   }
 };
