@@ -123,7 +123,7 @@ __device__ __forceinline__ int pa_shift(const PaParams& p, const SeqInfo& s, int
 template <int NH>
 __device__ __forceinline__ int pa_window_blocks(const PaParams& p, int lo) {
   // (where tiles are no multiple of the pieces the window's begin falls anywhere in one: room for the most)
-  const int piece = pa_piece(p), into = NH * p.T % piece == 0 ? lo & (piece - 1) : piece - 1;
+  const int piece = pa_piece(p), into = (NH * p.T & (piece - 1)) == 0 ? lo & (piece - 1) : piece - 1;
   return (p.sa + into + p.win.window - 1 + NH * p.T + PA_BN - 1) >> 7;
 }
 // Its blocks (at least one, so that rows without keys are written too)

@@ -47,11 +47,11 @@ struct PaCopy {
   int pieces;              // of a block
   bool mine;
   __device__ __forceinline__ PaCopy(const PaParams& p) {
-    const int lane = threadIdx.x & 31;
-    rows = p.wide ? min(p.pg.S, PA_BN) : 8;
-    pieces = PA_BN / rows;
-    piece = lane % pieces;
-    cb = lane / pieces;
+    const int lane = threadIdx.x & 31, lg = p.wide ? min(p.pg.lgS, 7) : 3;
+    rows = 1 << lg;
+    pieces = PA_BN >> lg;
+    piece = lane & (pieces - 1);
+    cb = lane >> (7 - lg);
     mine = cb < (p.wide ? 1 : CB);
   }
   // entry: the page, or any other number for zeros
