@@ -88,6 +88,16 @@ def test_more_sequences_than_threads(torch):
     run(torch, groups, hq=2, hkv=1, d=64, ps=16, hint=8)
 
 
+def test_more_groups_and_tiles_than_threads(torch):
+    """Groups of a sequence or two, more than a block has threads; one group of more tiles than that."""
+    rng = np.random.default_rng(6)
+    groups = [(16 * int(p), [(1, int(x)) for x in rng.integers(1, 30, k)]) for p, k in zip(rng.integers(0, 3, 1500), rng.integers(0, 3, 1500))]
+    run(torch, groups, hq=1, hkv=1, d=64, ps=16)
+    run(torch, groups, hq=2, hkv=1, d=64, ps=16, hint=2)
+    run(torch, [(48, [(1, 3)] * 1400)], hq=2, hkv=1, d=64, ps=16, hint=2)
+    run(torch, [(32, [(1, 2)] * 1400)], hq=128, hkv=1, d=64, ps=16, lse=False)
+
+
 @pytest.mark.parametrize("m", [1, 2, 5, 16, 33, 100, 300])
 @pytest.mark.parametrize("hint", [0, 4])
 def test_chunks_of_forks(torch, m, hint):

@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   pa_fence_before();
   griddep_wait();
   griddep_launch_dependents();   // (what follows may then rely on all that ran before this launch)
+  static_assert(2 * Sh::Q_BUF + 4 * pa_find_ints(PF_THREADS) <= Sh::ALL, "the cuts' space is behind the query buffers");
   const bool work = PaWalk<1, MODE>::template find<PF_THREADS>(p, s_place, s_w, reinterpret_cast<int*>(smem_raw + 1024 + 2 * Sh::Q_BUF));   // ends with a barrier
   pa_fence_after();
   const unsigned tm = s_tmem;

@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
   pa_fence_before();
   griddep_wait();
   griddep_launch_dependents();   // (what follows may then rely on all that ran before this launch)
+  static_assert(1024 + 4 * pa_find_ints(PA_THREADS<NH>) <= Sh::ALL, "the cuts' space is in the ring");
   const bool work = PaWalk<NH, MODE>::template find<PA_THREADS<NH>>(p, s_place, s_w, reinterpret_cast<int*>(smem_raw) + 256);   // ends with a barrier
   pa_fence_after();
   const unsigned tm = s_tmem;
