@@ -9,6 +9,8 @@
 //  * P^T is written to shared memory in two parts per probability, rounded and remainder, as 2 N columns (about 17 significant bits
 //    for bf16); the output adds the two columns of a row.  A key's 2 N columns are 64 bytes; the P of odd blocks is the other half
 //    of the same 128-byte rows.
+//  * R: rows that a tile can have (4, 8 or 16); the softmax leaves the other columns out: whatever lies there
+//    as probabilities goes into columns of O that nobody reads (256 sequences of a token, 4 heads to a group, under a window of 512: 123 -> 100 us).
 //  * A softmax thread has one key and all rows: references and running sums are per column, in registers; a column's maximum
 //    is taken across the 128 threads only for a tile's first block and when a logit passes its reference by 2^8 (a vote over the four
 //    warps otherwise).
@@ -35,8 +37,8 @@ struct PfShape {
   static constexpr int TM_O = 2 * N, TM_COLS = 4 * N;             // tensor memory: S 0, S 1 (N columns each), O (2 N)
 };
 
-// Reduces v[0 .. 16) over the warp's lanes; returns the column whose result v[0] then is (lanes 2 i and 2 i + 1 both have column i).
-// Each step halves the columns a lane keeps: 16 exchanges instead of 80.
+// Reduces v[0 .. N) over the warp's lanes; returns the column whose result v[0] then is (of 16, lanes 2 i and 2 i + 1 both have column i).
+// Each step halves the columns a lane keeps: for 16, 16 exchanges instead of 80.
 template <int N, class Op>
 __device__ __forceinline__ int pf_reduce(float (&v)[N], Op op) {
   const int lane = threadIdx.x & 31;
@@ -88,7 +90,26 @@ __device__ __forceinline__ bool pf_or(bool v) {
   return r != 0;
 }
 
-template <int D, bool FP16, int MODE>
+// R columns of this thread's tensor-memory lane, and back
+template <int R>
+__device__ __forceinline__ void pf_ld(unsigned t, unsigned* r) {
+  if constexpr (R == 16) pa_ld16(t, r);
+  else if constexpr (R == 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(t)
+                 : "memory");
+  else
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(t) : "memory");
+}
+template <int R>
+__device__ __forceinline__ void pf_st(unsigned t, const unsigned* r) {
+  if constexpr (R == 16) pa_st16(t, r);
+  else if constexpr (R == 8) pa_st8(t, r);
+  else asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+
+template <int D, int R, bool FP16, int MODE>
 __global__ void __launch_bounds__(PF_THREADS, 1)
     pages_few_kernel(const __grid_constant__ PaParams p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                      const __grid_constant__ CUtensorMap mv) {
@@ -101,8 +122,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   __shared__ int s_abort;
   __shared__ typename PaWalk<1, MODE>::Place s_place[2];
   __shared__ long long s_w[PF_THREADS / 32];
-  __shared__ __align__(16) float s_red[N][4];      // a column's value of each softmax warp
-  __shared__ float s_inv[N];
+  __shared__ __align__(16) float s_red[R][4];      // a column's value of each softmax warp
+  __shared__ float s_inv[R];
   __shared__ PaValid<MODE, NS> s_valid;
 
   const int tid = threadIdx.x, lane = tid & 31;
@@ -311,12 +332,12 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     // A wait that fails (the CTA is leaving) lets the loops run out without waiting, so that the warps' barriers stay in step.
 #pragma unroll 1
     for (int cnt; (cnt = cur.count()) > 0; cur.next_tile(p)) {
-      const PaFewSight<N, MODE> sight(p, cur);
+      const PaFewSight<R, MODE> sight(p, cur);
       unsigned unset = 0;                                           // rows that have seen no key: they have no reference yet
       constexpr float UP = PA_UP<FP16>;
-      float base[N], sum[N];                                        // UP - reference (log2 units), and this key's part of the sum
+      float base[R], sum[R];                                        // UP - reference (log2 units), and this key's part of the sum
 #pragma unroll
-      for (int c = 0; c < N; ++c) sum[c] = 0.f;
+      for (int c = 0; c < R; ++c) sum[c] = 0.f;
 #pragma unroll 1
       for (int k = 0; k < cnt; ++k, ++n) {
         const int key = (cur.b + k) * PA_BN + kl;
@@ -324,9 +345,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         sp ^= 1 << (n & 1);
         __syncwarp();
         pa_fence_after();
-        unsigned s[N];
-        pa_ld16(tm + (n & 1) * N + lane_off, s);
-        pa_wait_ld<N>(s);
+        unsigned s[R];
+        pf_ld<R>(tm + (n & 1) * N + lane_off, s);
+        pa_wait_ld<R>(s);
         if (__builtin_expect(sight.partly((cur.b + k) * PA_BN), 0)) {
           sight.mask(p, key, s);
           if (sight.strange((cur.b + k) * PA_BN)) {
@@ -340,21 +361,21 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         bool over = false;
         if (k > 0) {
 #pragma unroll
-          for (int c = 0; c < N; ++c) over |= fmaf(__uint_as_float(s[c]), p.scale2, base[c]) > PA_LAZY + UP;
+          for (int c = 0; c < R; ++c) over |= fmaf(__uint_as_float(s[c]), p.scale2, base[c]) > PA_LAZY + UP;
           if (MODE != PA_PLAIN && unset) {   // (the first logit that such a row sees is its reference, however far below zero)
 #pragma unroll
-            for (int c = 0; c < N; ++c) over |= (unset >> c & 1) && s[c] != 0xFF800000u;
+            for (int c = 0; c < R; ++c) over |= (unset >> c & 1) && s[c] != 0xFF800000u;
           }
         }
         if (__builtin_expect(k == 0 || pf_or(over), 0)) {
-          float m[N], f[N];
+          float m[R], f[R];
 #pragma unroll
-          for (int c = 0; c < N; ++c) m[c] = __uint_as_float(s[c]);
-          const int col = pf_reduce<N>(m, larger);
+          for (int c = 0; c < R; ++c) m[c] = __uint_as_float(s[c]);
+          const int col = pf_reduce<R>(m, larger);
           s_red[col][warp] = m[0];
           pf_sync();
 #pragma unroll
-          for (int c = 0; c < N; ++c) {
+          for (int c = 0; c < R; ++c) {
             const float4 w = *reinterpret_cast<const float4*>(s_red[c]);
             const float top = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)) * p.scale2;
             // (a row that sees none of these keys keeps its reference; of a first block, any)
@@ -377,13 +398,13 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             pa_fence_after();
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
-              unsigned o[N];
+              unsigned o[R];
               const unsigned at = tm + Sh::TM_O + part * N + lane_off;
-              pa_ld16(at, o);
-              pa_wait_ld<N>(o);
+              pf_ld<R>(at, o);
+              pa_wait_ld<R>(o);
 #pragma unroll
-              for (int c = 0; c < N; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f[c]);
-              pa_st16(at, o);
+              for (int c = 0; c < R; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f[c]);
+              pf_st<R>(at, o);
             }
             pa_wait_st();
           }
@@ -393,10 +414,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         const int pb = n & 1;
         const unsigned long long sc2 = f2_pack(p.scale2, p.scale2);
 #pragma unroll
-        for (int c = 0; c < N; c += 8) {
-          unsigned hi[4], lo[4];
+        for (int c = 0; c < R; c += 8) {
+          unsigned hi[4] = {}, lo[4] = {};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < (R < 8 ? R / 2 : 4); ++i) {
             const int a = c + 2 * i;
             const unsigned long long x =
                 f2_fma((unsigned long long)s[a] | ((unsigned long long)s[a + 1] << 32), sc2, f2_pack(base[a], base[a + 1]));
@@ -423,7 +444,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       }
 
       // ------------------------------ the tile's end in this piece
-      const int col = pf_reduce<N>(sum, plus);
+      const int col = pf_reduce<R>(sum, plus);
       s_red[col][warp] = sum[0];
       pf_sync();
       const bool whole = cnt == cur.nb;
@@ -433,7 +454,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         const int row = kl;
         float ref = 0.f;   // (of the sums: UP below the reference)
 #pragma unroll
-        for (int c = 0; c < N; ++c)
+        for (int c = 0; c < R; ++c)
           if (c == kl) ref = -base[c];
         const float4 w = *reinterpret_cast<const float4*>(s_red[row]);
         const float all = w.x + w.y + w.z + w.w;
@@ -453,16 +474,16 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       // a thread has a channel: lane of O (64 channels: sixteen to a warp)
       const int chan = D == 128 ? kl : warp * 16 + lane;
       const bool have = D == 128 || lane < 16;
-      unsigned o[N], l[N];
-      pa_ld16(tm + Sh::TM_O + lane_off, o);
-      pa_ld16(tm + Sh::TM_O + N + lane_off, l);
-      pa_wait_ld<N>(o);
-      pa_wait_ld<N>(l);
+      unsigned o[R], l[R];
+      pf_ld<R>(tm + Sh::TM_O + lane_off, o);
+      pf_ld<R>(tm + Sh::TM_O + N + lane_off, l);
+      pa_wait_ld<R>(o);
+      pa_wait_ld<R>(l);
       uint16_t* dst = p.out + (long long)cur.tok(p) * p.ots + (long long)cur.head() * p.G * p.ohs + chan;
       float* po = p.part_o + (part * (D / 4) + chan / 4) * 512 + chan % 4;
       int g = 0;
 #pragma unroll
-      for (int c = 0; c < N; ++c)
+      for (int c = 0; c < R; ++c)
         if (c < rows) {
           const float x = __uint_as_float(o[c]) + __uint_as_float(l[c]);
           if (have && whole) *dst = (uint16_t)pa_pack<FP16>(x * s_inv[c], 0.f);

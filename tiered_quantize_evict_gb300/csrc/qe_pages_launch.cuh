@@ -2,6 +2,7 @@
 #pragma once
 #include <atomic>
 #include <numeric>
+#include <type_traits>
 
 #include "qe_pages_few.cuh"
 #include "qe_pages_halves.cuh"
@@ -34,11 +35,11 @@ static cudaError_t halves_t(const PaParams& p, const CUtensorMap* maps, int devi
   return e != cudaSuccess || !p.rec ? e : launch_pages_join(p, NH, FP16, st);   // (no rec: no tile is cut)
 }
 
-template <int D, bool FP16, int MODE>
+template <int D, int R, bool FP16, int MODE>
 static cudaError_t few_t(const PaParams& p, const CUtensorMap* maps, int device, cudaStream_t st) {
   static std::atomic<unsigned long long> ready{0};   // devices whose copy of the kernel has its attribute
   if (device >= 64 || !(ready.load() >> device & 1)) {
-    const cudaError_t e = cudaFuncSetAttribute(pages_few_kernel<D, FP16, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfShape<D>::SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(pages_few_kernel<D, R, FP16, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfShape<D>::SMEM);
     if (e != cudaSuccess) return e;
     if (device < 64) ready.fetch_or(1ull << device);
   }
@@ -52,7 +53,7 @@ static cudaError_t few_t(const PaParams& p, const CUtensorMap* maps, int device,
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, pages_few_kernel<D, FP16, MODE>, p, maps[0], maps[1], maps[2]);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, pages_few_kernel<D, R, FP16, MODE>, p, maps[0], maps[1], maps[2]);
   return e != cudaSuccess || !p.rec ? e : launch_pages_join(p, 1, FP16, st);   // (no rec: no tile is cut)
 }
 
@@ -140,8 +141,15 @@ static cudaError_t launch_pages_mode(const PagesAttendParams& a, const PagesWind
     if (!(p.wide ? encode(&maps[1 + i], 5, base, wide_dim, wide_str, wide_box) : encode(&maps[1 + i], 5, base, dim, str, box))) return cudaErrorInvalidValue;
   }
   if (one && p.T * p.G <= PAGES_FEW_ROWS) {
-    if (g.D == 128) return fp16 ? few_t<128, true, MODE>(p, maps, device, st) : few_t<128, false, MODE>(p, maps, device, st);
-    return fp16 ? few_t<64, true, MODE>(p, maps, device, st) : few_t<64, false, MODE>(p, maps, device, st);
+    // (columns that the softmax takes: those of a decode step with 4 heads to a group need not pay for 16)
+    auto few = [&](auto r) {
+      constexpr int R = decltype(r)::value;
+      if (g.D == 128) return fp16 ? few_t<128, R, true, MODE>(p, maps, device, st) : few_t<128, R, false, MODE>(p, maps, device, st);
+      return fp16 ? few_t<64, R, true, MODE>(p, maps, device, st) : few_t<64, R, false, MODE>(p, maps, device, st);
+    };
+    const int rows = p.T * p.G;
+    if (rows <= 4) return few(std::integral_constant<int, 4>{});
+    return rows <= 8 ? few(std::integral_constant<int, 8>{}) : few(std::integral_constant<int, 16>{});
   }
   if (g.D == 128) {
     if (one) return fp16 ? halves_t<128, 1, true, MODE>(p, maps, device, st) : halves_t<128, 1, false, MODE>(p, maps, device, st);
