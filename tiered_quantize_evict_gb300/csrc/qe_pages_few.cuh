@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   __shared__ __align__(8) unsigned long long b_kfull[NS], b_kempty[NS], b_qfull[2], b_qempty[2], b_s[2], b_p[2], b_o[2], b_end;
   __shared__ unsigned s_tmem;
   __shared__ int s_abort;
-  __shared__ typename PaWalk<1, MODE>::Place s_place[2];
+  __shared__ typename PaWalk<1, MODE>::Place s_place[PaWalk<1, MODE>::PLACES];
   __shared__ long long s_w[PF_THREADS / 32];
   __shared__ __align__(16) float s_red[R][4];      // a column's value of each softmax warp
   __shared__ float s_inv[R];

@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
   __shared__ __align__(8) unsigned long long b_kfull[Sh::MOST], b_kempty[Sh::MOST], b_qfull[2], b_qempty[2], b_s[2], b_p[2][PARTS], b_o[2], b_turn[2], b_end;
   __shared__ unsigned s_tmem;
   __shared__ int s_abort;
-  __shared__ typename PaWalk<NH, MODE>::Place s_place[2];
+  __shared__ typename PaWalk<NH, MODE>::Place s_place[PaWalk<NH, MODE>::PLACES];
   __shared__ long long s_w[PA_THREADS<NH> / 32];
   __shared__ float s_x[NH][128];      // what the two threads of a row tell each other
   __shared__ PaValid<MODE, Sh::MOST> s_valid;

@@ -106,8 +106,14 @@ struct PaSharedTile {
   int np, na, nz;       // blocks with keys of the prefix; those and the rest of the first stream; the second stream's
 };
 
+// Places in shared memory: where the CTA's walk starts, where it ends, and with one half the tiles behind the first, as far as they are
+// kept: what a warp would have to gather of the arrays again, between two tiles (64 groups of 8 sequences 148.7 -> 143.3 us; the softmax of
+// two halves has no registers for it: 64 sequences 70 -> 88).
+constexpr int PA_KEPT = 3;
+template <int NH>
+constexpr int PA_PLACES = NH == 1 ? 3 + PA_KEPT : 2;
 struct PaSharedPlace {
-  int h, g, j, b;      // KV head (that of the end of the line: their number), group, tile of the group, block
+  int h, g, j, b;      // KV head (that of the end of the line: their number; of a tile that is not kept: -1), group, tile of the group, block
   PaSharedTile tile;   // what a walk from here on starts with
   __device__ __forceinline__ bool before(const PaSharedPlace& o) const {
     return h != o.h ? h < o.h : (g != o.g ? g < o.g : (j != o.j ? j < o.j : b < o.b));
@@ -119,6 +125,7 @@ template <int NH>
 struct PaSharedCursor : PaSharedTile {
   int h, g, j, b, nb;   // the place; blocks of the tile
   int eh, eg, ej, eb;   // where the walk ends
+  const PaSharedPlace* kept;
   __device__ __forceinline__ PaStream stream(const PaParams& p, int z) const {
     if (NH == 1) return PaStream{first, t0, t1, gr.prefix};
     return z ? PaStream{mid, t0 + p.T, t1, np * PA_BN} : PaStream{first, t0, min(t1, t0 + p.T), gr.prefix};
@@ -180,6 +187,7 @@ struct PaSharedCursor : PaSharedTile {
     eg = pl[1].g;
     ej = pl[1].j;
     eb = pl[1].b;
+    kept = pl + 2;
     static_cast<PaSharedTile&>(*this) = pl[0].tile;
     nb = na + nz;
   }
@@ -191,6 +199,18 @@ struct PaSharedCursor : PaSharedTile {
       return;
     }
     b = 0;
+    if (NH == 1 && kept) {
+      if (kept->h >= 0) {
+        h = kept->h;
+        g = kept->g;
+        j = kept->j;
+        static_cast<PaSharedTile&>(*this) = kept->tile;
+        nb = na + nz;
+        ++kept;
+        return;
+      }
+      kept = nullptr;
+    }
     ++j;
     if ((long long)gr.q0 + (long long)j * NH * p.T >= gr.q1) {
       j = 0;
@@ -386,6 +406,7 @@ __device__ __noinline__ void pa_find_shared(const PaParams& p, PaSharedPlace* pl
     from = PaSource{start, prefix, q_start, row, len};
   }
   if (tid < 2) pl[tid].h = p.pg.H, pl[tid].g = pl[tid].j = pl[tid].b = 0;
+  if (NH == 1 && tid == 0) pl[2].h = pl[2 + PA_KEPT].h = -1;
   __syncthreads();
   long long line = 0;
   int pieces = 0, head[2] = {p.pg.H, p.pg.H};
@@ -454,12 +475,20 @@ __device__ __noinline__ void pa_find_shared(const PaParams& p, PaSharedPlace* pl
               pl[k].j = info[1];
               pl[k].b = b;
               pl[k].tile = *t;
+              if (NH == 1 && k == 0) s_w[0] = tid;
               if (k == 0) p.rec[c] = PaRec{(long long)head[0] * p.c.total + t->t0, b, t->t0, t->t1 - t->t0, head[0], pieces};
             }
         }
         at += sum;
-        if (once) pass = 2;
         __syncthreads();   // (s_tile is read)
+        if (NH == 1 && once && head[0] < p.pg.H && tid < PA_KEPT * PA_TILE_INTS) {   // the tiles behind the first, behind the last the next head's
+          const int e = tid / PA_TILE_INTS, i = tid - e * PA_TILE_INTS, x = s_w[0] + 1 + e, up = x / all_tiles;
+          const int h = head[0] + up < p.pg.H ? head[0] + up : -1, v = s_tile[(x - up * all_tiles) * PA_TILE_INTS + i];
+          if (i == 0) pl[2 + e].h = h, pl[2 + e].g = v;
+          else if (i == 1) pl[2 + e].j = v;
+          else reinterpret_cast<int*>(&pl[2 + e].tile)[i - 2] = v;
+        }
+        if (once) pass = 2;
       }
       if (all_tiles == 0 && p.gr.n <= NT) pass = 2;
     }

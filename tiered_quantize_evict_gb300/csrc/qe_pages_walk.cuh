@@ -19,6 +19,7 @@ template <int NH, int MODE>
 struct PaWalk {
   using Cursor = PaCursor<NH, MODE>;
   using Place = PaPlace;
+  static constexpr int PLACES = 2;
   using Keys = PaRowKeys<NH, MODE>;
   // finds the CTA's piece of the line; false where it has none
   template <int NT>
@@ -32,6 +33,7 @@ template <int NH>
 struct PaWalk<NH, PA_SHARED> {
   using Cursor = PaSharedCursor<NH>;
   using Place = PaSharedPlace;
+  static constexpr int PLACES = PA_PLACES<NH>;
   using Keys = PaSharedKeys<NH>;
   template <int NT>
   static __device__ __forceinline__ bool find(const PaParams& p, Place* pl, long long* s_w, int* space) {
