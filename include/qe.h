@@ -618,6 +618,7 @@ typedef struct {
  * kv_len - m of each of the group's chunks of m tokens (causal = 0: kv_len) and at most the first sequence's kv_len; one that is not, or a
  * group_start that decreases or leaves [0, n_seqs], sets QE_PAGES_ERR_ROW (a prefix is cut to the first sequence's length; a
  * chunk that begins inside its prefix sees all of it; sequences of no group are left alone).  args->max_q_len is not looked at.
+ * Inputs are finite: a value that is not may reach all tokens of its group, those of the other sequences too.
  * Sizes that can be served: (S + 1) max_pages page_size below 2^31, with S = min(n_seqs, 256 n_kv_heads / n_q_heads). */
 qe_status qe_pages_attend_shared(const qe_pages* pages, int layer, const qe_page_table* seqs, const qe_chunks* chunks,
                                  const qe_pages_attend_args* args, const qe_groups* groups, void* workspace, size_t bytes, void* stream);
@@ -627,7 +628,8 @@ qe_status qe_pages_attend_shared_workspace(const qe_pages* pages, size_t* bytes)
 /* Give back the pages that a window has left: of each of n rows, those whose tokens are all behind the first `sinks` and all
  * before kv_len - window + 1, which no later token sees.  Their entries become QE_PAGES_DROPPED; lengths and positions stay as
  * they are.  Rows grow, are forked, cut, freed and compacted as before (a row that is cut back to inside of a dropped page is
- * reported where that page is needed: tokens taken back widen the window, so drop with a window that much larger).  A row may
+ * reported where that page is needed: tokens taken back widen the window, so drop with a window that much larger).  Attention that
+ * sees a dropped page, or gathering one, takes its keys as zeros and reports it, as any page that is not there.  A row may
  * be named twice.  Pages given back are free from the next call on. */
 qe_status qe_pages_drop(const qe_pages* pages, const qe_page_table* seqs, const int* rows, int n, int window, int sinks, void* stream);
 

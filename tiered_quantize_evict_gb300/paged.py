@@ -326,7 +326,7 @@ class PagePool:
 
         group_start int32 [n_groups + 1]: group g is the call's sequences group_start[g] .. group_start[g + 1] - 1; prefix_len
         int32 [n_groups]: their first tokens, in the pages of the group's first sequence.  max_group_len: the most packed tokens
-        of a group, or 0 if it is not known."""
+        of a group, or 0 if it is not known.  Values that are not finite may reach the whole group."""
         out, lse, ref, c, a = self._attend(q, q_start, seqs, rows, scale, causal, max_group_len, "max_group_len", out, return_lse)
         n = _ints("prefix_len", prefix_len, self._index)
         if _ints("group_start", group_start, self._index) != n + 1:
