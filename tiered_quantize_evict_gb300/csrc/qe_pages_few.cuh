@@ -14,7 +14,7 @@
 //  * A softmax thread has one key and all rows: references and running sums are per column, in registers; a column's maximum
 //    is taken across the 128 threads only for a tile's first block and when a logit passes its reference by 2^8 (a vote over the four
 //    warps otherwise).
-// CTA: warps 0-3 softmax, 4 TMA of keys and values, 5 tensor-core issue, 6 TMA of the queries, 7 tensor memory.
+// CTA: warps 0-3 softmax, 4 TMA of keys and values, 5 tensor-core issue, 6 TMA of the queries, 7 tensor memory (and TMA of values).
 // mbarriers: kfull / kempty per slot, qfull / qempty per query buffer, s[i] (S i complete), p[i] (P i written; one arrival per
 // softmax warp), o[i] (the P V of an even or odd block complete, as with NH = 1 there).  Waits are bounded as in qe_pages_halves.cuh.
 #pragma once
@@ -32,7 +32,11 @@ struct PfShape {
   static constexpr int Q_CB = N * 128, Q_BUF = CB * Q_CB;          // a query buffer's column block, and the buffer
   static constexpr int P_BUF = 128 * 128;                         // 128 keys, two times 2 N columns
   static constexpr int ALL = 7 * 32768;
-  static constexpr int SLOTS = (ALL - 2 * Q_BUF - P_BUF) / TILE;
+  static constexpr int SLOTS = (ALL - 2 * Q_BUF - P_BUF) / (2 * TILE) * 2;
+  // Keys and values sent by a warp each: what a lane's copies cost, some 100 cycles each, and what it looks up is what bounds 64 channels
+  // (decode step with pages of 16, 32, 64 tokens 218, 172, 151 us with one warp, 152, 148, 146 with two).  With 128 channels memory bounds,
+  // and one warp sends them in the order they are used (16 sequences of up to 32K tokens 275 us with one, 282 with two).
+  static constexpr bool SPLIT = D == 64;
   static constexpr int SMEM = ALL + 1024;
   static constexpr int TM_O = 2 * N, TM_COLS = 4 * N;             // tensor memory: S 0, S 1 (N columns each), O (2 N)
 };
@@ -116,6 +120,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   using Sh = PfShape<D>;
   using Cursor = typename PaWalk<1, MODE>::Cursor;
   constexpr int NS = Sh::SLOTS, N = Sh::N;
+  constexpr bool SPLIT = Sh::SPLIT;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) unsigned long long b_kfull[NS], b_kempty[NS], b_qfull[2], b_qempty[2], b_s[2], b_p[2], b_o[2], b_end;
   __shared__ unsigned s_tmem;
@@ -164,14 +169,17 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   pa_fence_after();
   const unsigned tm = s_tmem;
 
-  if (work && aux == 0) {
-    // ============================== keys and values
+  if (work && (aux == 0 || (SPLIT && aux == 3))) {
+    // ============================== keys and values, or one of them
+    const int kv0 = SPLIT && aux == 3;
+    constexpr int STEP = SPLIT ? 2 : 1;
+    static_assert(!SPLIT || NS % 2 == 0, "keys and values have slots of their own");
     Cursor cur;
     cur.set(p, s_place);
     const PaCopy<Sh::CB> copy(p);
     // this lane's piece, its entry loaded a block before it is looked at
     typename PaWalk<1, MODE>::Keys keys;
-    int slot = 0, ph = 1, issued = 0, left = cur.count();
+    int slot = kv0, ph = 1, issued = 0, left = cur.count();
     PaPiece next = keys.at(p, cur, cur.b, copy.piece * copy.rows);
     int till = PaWait::counted(p, PaWait::KEYS);
     bool ok = true;
@@ -188,7 +196,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       }
       if (left > 0) next = keys.at(p, cur, cur.b, copy.piece * copy.rows);
 #pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv) {
+      for (int kv = kv0; kv < (SPLIT ? kv0 + 1 : 2); ++kv) {
         ok = ok && wait.count(till, smem_u32(&b_kempty[slot]), ph);
         if (!__all_sync(~0u, ok)) {
           ok = false;
@@ -203,14 +211,17 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         __syncwarp();
         if (copy.mine) copy.send(p, kv ? &mv : &mk, sm_kv + slot * Sh::TILE, there, now, h, tk, full);
         ++issued;
-        if (++slot == NS) {
-          slot = 0;
+        if ((slot += STEP) >= NS) {
+          slot -= NS;
           ph ^= 1;
         }
       }
     }
     if (lane == 0)   // the copies land before the CTA leaves (early, it may be, and for another warp's wait)
-      for (int i = max(0, issued - NS); i < issued; ++i) wait.drain(smem_u32(&b_kfull[i % NS]), (i / NS) & 1);
+      for (int i = max(0, issued - NS / STEP); i < issued; ++i) {
+        const int place = STEP * i + kv0;
+        wait.drain(smem_u32(&b_kfull[place % NS]), (place / NS) & 1);
+      }
   } else if (work && aux == 1) {
     // ============================== tensor cores (the whole warp walks the loop, one lane issues)
     constexpr unsigned FMT = FP16 ? 0u : (1u << 7) | (1u << 10);
