@@ -46,6 +46,10 @@ namespace qe {
 template <int NH>
 constexpr int PA_PARTS = NH == 2 ? 4 : 2;
 
+// Keys and values sent by a warp each: with 64 channels, where what copies cost bounds small pages (PfShape), if one of the 4 warps
+// is free for it (a fifth would leave the softmax of two halves 80 registers).
+template <int D, int NH>
+constexpr bool PA_SPLIT = D == 64 && NH == 1;
 // threads: 8 softmax warps per half, 4 more warps
 template <int NH>
 constexpr int PA_THREADS = 256 * NH + 128;
@@ -59,7 +63,8 @@ struct PaShape {
   static constexpr int SMEM = ALL + 1024;
   // Slots beside two query buffers of `rows` rows (64 where a tile has no more, else 128; the products of rows behind read what
   // lies there and are not used): bound by memory, the ring's depth is what counts.
-  static constexpr int slots(int rows) { return (ALL - 2 * CB * rows * 128) / TILE; }
+  // (with 64 channels an even number, for keys and values with slots of their own)
+  static constexpr int slots(int rows) { return (ALL - 2 * CB * rows * 128) / (TILE * (3 - CB)) * (3 - CB); }
   static constexpr int TM_O = 256;               // tensor memory: S0 at column 0, S1 at 128, O0 here, O1 at + D
 };
 
@@ -177,14 +182,17 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
 
   if (aux >= 0) {
     if (NH == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (work && aux == 0) {
-      // ============================== keys and values
+    constexpr bool SPLIT = PA_SPLIT<D, NH>;
+    if (work && (aux == 0 || (SPLIT && aux == 2))) {
+      // ============================== keys and values, or one of them
+      const int kv0 = SPLIT && aux != 0;
+      constexpr int STEP = SPLIT ? 2 : 1;
       Cursor cur;
       cur.set(p, s_place);
       const PaCopy<Sh::CB> copy(p);
       // this lane's piece, its entry loaded a block before it is looked at
       typename PaWalk<NH, MODE>::Keys keys;
-      int slot = 0, ph = 1, issued = 0, left = cur.count();
+      int slot = kv0, ph = 1, issued = 0, left = cur.count();
       PaPiece next = keys.at(p, cur, cur.b, copy.piece * copy.rows);
       int till = PaWait::counted(p, PaWait::KEYS);
       bool ok = true;
@@ -201,7 +209,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
         }
         if (left > 0) next = keys.at(p, cur, cur.b, copy.piece * copy.rows);
 #pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
+        for (int kv = kv0; kv < (SPLIT ? kv0 + 1 : 2); ++kv) {
           ok = ok && wait.count(till, smem_u32(&b_kempty[slot]), ph);
           if (!__all_sync(~0u, ok)) {
             ok = false;
@@ -216,14 +224,17 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
           __syncwarp();
           if (copy.mine) copy.send(p, kv ? &mv : &mk, sm_kv + slot * Sh::TILE, there, now, h, tk, full);
           ++issued;
-          if (++slot == NS) {
-            slot = 0;
+          if ((slot += STEP) >= NS) {
+            slot -= NS;
             ph ^= 1;
           }
         }
       }
       if (lane == 0)   // the copies land before the CTA leaves (early, it may be, and for another warp's wait)
-        for (int i = max(0, issued - NS); i < issued; ++i) wait.drain(smem_u32(&b_kfull[i % NS]), (i / NS) & 1);
+        for (int i = max(0, issued - NS / STEP); i < issued; ++i) {
+          const int place = STEP * i + kv0;
+          wait.drain(smem_u32(&b_kfull[place % NS]), (place / NS) & 1);
+        }
     } else if (work && aux - 1 < NH) {
       // ============================== tensor cores: a warp per half, so that the waits and the issue of one half pass while
       // the products of the other run.  The whole warp walks the loop (addresses and descriptors stay uniform), one lane issues.
