@@ -25,7 +25,6 @@ __device__ __forceinline__ PaSource pa_arrays(const PaParams& p) { return PaSour
 // A group: its sequences [s0, s1), packed tokens [q0, q1), tokens of the prefix (whole pages) and the row that has them.
 struct PaGroup {
   int s0, s1, q0, q1, prefix, row;
-  __device__ __forceinline__ bool empty() const { return q1 <= q0; }
 };
 __device__ __forceinline__ PaGroup pa_group(const PaParams& p, const PaSource& from, int g) {
   PaGroup r;
@@ -430,10 +429,11 @@ __device__ __noinline__ void pa_find_shared(const PaParams& p, PaSharedPlace* pl
       for (int xb = 0; xb < all_tiles; xb += NT) {
 #pragma unroll 1
         for (int x = xb + warp; x < min(all_tiles, xb + NT); x += W) {
-          const int k = pages_count_below(s_first + 1, NT, x);
+          // (bounded: groups that overlap, which is an error, could have more tiles than 32 bits count)
+          const int k = min(pages_count_below(s_first + 1, NT, x), min(NT, p.gr.n - gb) - 1);
           PaSharedCursor<NH> cur;
-          cur.j = x - s_first[k];
           cur.gr = pa_group(p, from, gb + k);
+          cur.j = min(max(x - s_first[k], 0), max(cur.gr.q1 - cur.gr.q0 - 1, 0) / tt);
           cur.tile(p, from);
           if (lane == 0) {
             int* to = s_tile + (x - xb) * PA_TILE_INTS;
