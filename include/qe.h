@@ -614,10 +614,12 @@ typedef struct {
 } qe_groups;
 
 /* qe_pages_attend for sequences that share prefixes: a prefix is read once for the queries of its whole group.  The same
- * results (up to the order of sums) as qe_pages_attend on tables that repeat the prefix's pages.  Every prefix is at most
+ * results as qe_pages_attend on tables that repeat the prefix's pages, up to the order of sums and to the bits of a probability when it
+ * meets the values: at least as many as there with the same args->max_q_len (the longest chunk; results are right for any), and that is
+ * twice the pool type's where max_q_len is known (not 0) and n_q_heads / n_kv_heads times it is 128 at most.  Every prefix is at most
  * kv_len - m of each of the group's chunks of m tokens (causal = 0: kv_len) and at most the first sequence's kv_len; one that is not, or a
  * group_start that decreases or leaves [0, n_seqs], sets QE_PAGES_ERR_ROW (a prefix is cut to the first sequence's length; a
- * chunk that begins inside its prefix sees all of it; sequences of no group are left alone).  args->max_q_len is not looked at.
+ * chunk that begins inside its prefix sees all of it; sequences of no group are left alone).
  * Inputs are finite: a value that is not may reach all tokens of its group, those of the other sequences too.
  * Sizes that can be served: (S + 1) max_pages page_size below 2^31, with S = min(n_seqs, 256 n_kv_heads / n_q_heads). */
 qe_status qe_pages_attend_shared(const qe_pages* pages, int layer, const qe_page_table* seqs, const qe_chunks* chunks,

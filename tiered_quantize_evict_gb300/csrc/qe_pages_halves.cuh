@@ -27,6 +27,8 @@
 //    2^-32 of the reference's weight where that is more (P is taken 2^7 times as large, or it would be 2^-25); the sum is of the
 //    unrounded ones.  With NH = 1, where the tensor cores wait for memory anyway, what the rounding leaves is kept as
 //    a second operand and multiplied too: error against 64 bits 1.45 -> 1.0 times that of the result's own rounding.
+//    REST: with two halves of shared prefixes too, where the caller says that the chunks are short (a block of both halves is then 3072
+//    cycles of products, not 2048, and takes 2.0 us where reading it takes 1.4: 64 sequences behind a 32K prefix 69 -> 79 us, error 2.2e-3 -> 1.7e-3).
 // mbarriers.  Every wait is bounded, by 0.2 s and 10 us for each block that it may sit out; one that expires sets QE_PAGES_ERR_TIMEOUT
 // and an abort flag that ends all loops, and the CTA leaves after what it issued has landed: each warp that issues waits for its own
 // last, whether it or another warp gave up.
@@ -127,7 +129,7 @@ __device__ __forceinline__ void pa_quad_transpose(unsigned* u) {
 }
 // ---------------------------------------------------------------------------- the kernel
 
-template <int D, int NH, bool FP16, int MODE>
+template <int D, int NH, bool FP16, int MODE, bool REST>
 __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
     pages_attend_kernel(const __grid_constant__ PaParams p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                         const __grid_constant__ CUtensorMap mv) {
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
         const unsigned long long b = PA_DESC_V<Sh::CB> | ((sm_kv + vslot * Sh::TILE) >> 4);
         constexpr int KS = 4 / PARTS;   // steps of 16 keys of a part of 64
 #pragma unroll
-        for (int rest = 0; rest < (NH == 1 ? 2 : 1); ++rest)   // (with the remainders of P)
+        for (int rest = 0; rest < (REST ? 2 : 1); ++rest)   // (with the remainders of P)
 #pragma unroll
           for (int i = 0; i < 2 * KS; ++i) {
             const int k = i / KS * 4 + part * KS + i % KS;
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
             unsigned z[16] = {};
             pa_st16(t_s + ch * 32, z);
             pa_st16(t_s + ch * 32 + 16, z);
-            if (NH == 1) {
+            if (REST) {
               pa_st16(t_s + 64 + ch * 32, z);
               pa_st16(t_s + 64 + ch * 32 + 16, z);
             }
@@ -577,7 +579,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
                 const float e0 = ex2(f2_lo(x)), e1 = ex2(f2_hi(x));
                 acc[e & 1] = f2_add(acc[e & 1], f2_pack(e0, e1));
                 pk[e] = pa_pack<FP16>(e0, e1);
-                if (NH == 1) {
+                if (REST) {
                   const float2 r = pa_unpack<FP16>(pk[e]);
                   const unsigned long long d = f2_sub(f2_pack(e0, e1), f2_pack(r.x, r.y));
                   rest[e] = pa_pack<FP16>(f2_lo(d), f2_hi(d));
@@ -588,6 +590,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
                 pa_st16(t_s + 64 + ch * 32 + c * N, rest);
               } else {
                 pa_st8(t_s + ch * 32 + c * N, pk);
+                if (REST) pa_st8(t_s + 64 + ch * 32 + c * N, rest);
               }
               if (c < PARTS - 1) {   // the products of these may start
                 pa_wait_st();

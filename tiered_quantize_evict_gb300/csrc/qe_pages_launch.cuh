@@ -13,11 +13,11 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeFn pages_encode_fn();
 
-template <int D, int NH, bool FP16, int MODE>
+template <int D, int NH, bool FP16, int MODE, bool REST = NH == 1>
 static cudaError_t halves_t(const PaParams& p, const CUtensorMap* maps, int device, cudaStream_t st) {
   static std::atomic<unsigned long long> ready{0};   // devices whose copy of the kernel has its attribute
   if (device >= 64 || !(ready.load() >> device & 1)) {
-    const cudaError_t e = cudaFuncSetAttribute(pages_attend_kernel<D, NH, FP16, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, PaShape<D>::SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(pages_attend_kernel<D, NH, FP16, MODE, REST>, cudaFuncAttributeMaxDynamicSharedMemorySize, PaShape<D>::SMEM);
     if (e != cudaSuccess) return e;
     if (device < 64) ready.fetch_or(1ull << device);
   }
@@ -31,7 +31,7 @@ static cudaError_t halves_t(const PaParams& p, const CUtensorMap* maps, int devi
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, pages_attend_kernel<D, NH, FP16, MODE>, p, maps[0], maps[1], maps[2]);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, pages_attend_kernel<D, NH, FP16, MODE, REST>, p, maps[0], maps[1], maps[2]);
   return e != cudaSuccess || !p.rec ? e : launch_pages_join(p, NH, FP16, st);   // (no rec: no tile is cut)
 }
 
@@ -151,6 +151,11 @@ static cudaError_t launch_pages_mode(const PagesAttendParams& a, const PagesWind
     if (rows <= 4) return few(std::integral_constant<int, 4>{});
     return rows <= 8 ? few(std::integral_constant<int, 8>{}) : few(std::integral_constant<int, 16>{});
   }
+  if constexpr (MODE == PA_SHARED)   // (chunks that an attention without groups takes with one half keep their bits in groups of any size)
+    if (!one && a.max_q_len > 0 && a.max_q_len <= fit) {
+      if (g.D == 128) return fp16 ? halves_t<128, 2, true, MODE, true>(p, maps, device, st) : halves_t<128, 2, false, MODE, true>(p, maps, device, st);
+      return fp16 ? halves_t<64, 2, true, MODE, true>(p, maps, device, st) : halves_t<64, 2, false, MODE, true>(p, maps, device, st);
+    }
   if (g.D == 128) {
     if (one) return fp16 ? halves_t<128, 1, true, MODE>(p, maps, device, st) : halves_t<128, 1, false, MODE>(p, maps, device, st);
     return fp16 ? halves_t<128, 2, true, MODE>(p, maps, device, st) : halves_t<128, 2, false, MODE>(p, maps, device, st);

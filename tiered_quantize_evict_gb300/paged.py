@@ -269,7 +269,7 @@ class PagePool:
             self._check(st)
         return q_out
 
-    def _attend(self, q, q_start, seqs, rows, scale, causal, hint, name, out, return_lse):
+    def _attend(self, q, q_start, seqs, rows, scale, causal, max_q_len, out, return_lse):
         """Checks what every attention takes; (out, lse, page table, chunks, args)."""
         total, hq = q.shape[:2] if q.dim() == 3 else (0, 0)
         qs = self._tokens("q", q, total, hq)
@@ -280,10 +280,10 @@ class PagePool:
             os = self._tokens("out", out, total, hq)
         lse = torch.empty(total, hq, dtype=torch.float32, device=self.device) if return_lse else None
         ref, c = self._seqs(seqs), self._chunks(q_start, rows, total)
-        if not 0 <= hint < 2 ** 31:
-            raise _bad(f"{name} {hint} out of range")
+        if not 0 <= max_q_len < 2 ** 31:
+            raise _bad(f"max_q_len {max_q_len} out of range")
         a = _ATTEND.pack(q.data_ptr(), out.data_ptr(), lse.data_ptr() if return_lse else 0, qs[0], qs[1], os[0], os[1], hq,
-                         1 if causal else 0, hint, self._scale if scale is None else scale)
+                         1 if causal else 0, max_q_len, self._scale if scale is None else scale)
         return out, lse, ref, c, a
 
     def _window(self, window, sinks):
@@ -298,7 +298,7 @@ class PagePool:
 
         With a window, qe_pages_attend_window: a token sees itself and the window - 1 tokens before it, and the row's first
         `sinks` tokens; pages that this leaves out may have been dropped."""
-        out, lse, ref, c, a = self._attend(q, q_start, seqs, rows, scale, causal, max_q_len, "max_q_len", out, return_lse)
+        out, lse, ref, c, a = self._attend(q, q_start, seqs, rows, scale, causal, max_q_len, out, return_lse)
         if window is not None:
             self._window(window, sinks)
             a = (a, window, sinks)
@@ -321,13 +321,16 @@ class PagePool:
 
     def attend_shared(self, layer: int, q: torch.Tensor, q_start: torch.Tensor, seqs: PageTable, group_start: torch.Tensor,
                       prefix_len: torch.Tensor, *, rows: Optional[torch.Tensor] = None, scale: Optional[float] = None, causal: bool = True,
-                      max_group_len: int = 0, out: Optional[torch.Tensor] = None, return_lse: bool = False):
+                      max_group_len: int = 0, out: Optional[torch.Tensor] = None, return_lse: bool = False, max_q_len: int = 0):
         """qe_pages_attend_shared: attend for sequences that share prefixes (forks), each read once for its group.
 
         group_start int32 [n_groups + 1]: group g is the call's sequences group_start[g] .. group_start[g + 1] - 1; prefix_len
         int32 [n_groups]: their first tokens, in the pages of the group's first sequence.  max_group_len: the most packed tokens
-        of a group, or 0 if it is not known.  Values that are not finite may reach the whole group."""
-        out, lse, ref, c, a = self._attend(q, q_start, seqs, rows, scale, causal, max_group_len, "max_group_len", out, return_lse)
+        of a group, or 0 if it is not known; max_q_len: the longest chunk, as of attend: where it is given, groups of any size have
+        the probabilities in as many bits as attend has them.  Values that are not finite may reach the whole group."""
+        out, lse, ref, c, a = self._attend(q, q_start, seqs, rows, scale, causal, max_q_len, out, return_lse)
+        if not 0 <= max_group_len < 2 ** 31:
+            raise _bad(f"max_group_len {max_group_len} out of range")
         n = _ints("prefix_len", prefix_len, self._index)
         if _ints("group_start", group_start, self._index) != n + 1:
             raise _bad("group_start must have one entry more than prefix_len")
