@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     while (left > 0 && ok) {
       const int tk = next.tok, h = cur.h, now = next.entry;
       const bool there = next.entry >= 0 && next.entry < p.pg.P;
-      if (!there && next.entry != INT_MIN) pages_report(p.pg, QE_PAGES_ERR_PAGE);
+      if (!there && next.valid != PA_NO_KEYS) pages_report(p.pg, QE_PAGES_ERR_PAGE);
       const int valid = there ? next.valid : 255;
       ++cur.b;
       if (--left == 0) {

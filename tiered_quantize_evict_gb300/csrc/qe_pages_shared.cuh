@@ -269,8 +269,9 @@ struct PaSharedCursor : PaSharedTile {
   }
 };
 
-// What the warp that copies keys and values knows of a piece of a page: the table's entry (INT_MIN: no keys here), the piece's first token in
-// the page, and how many of its tokens are the sequence's where not all of them are (255 else).
+// What the warp that copies keys and values knows of a piece of a page: the table's entry, the piece's first token in the page, and how
+// many of its tokens are the sequence's where not all of them are (255 else; PA_NO_KEYS: there are no keys here, and no entry).
+constexpr int PA_NO_KEYS = 256;
 struct PaPiece {
   int entry, tok, valid;
 };
@@ -282,7 +283,7 @@ struct PaSharedKeys {
   __device__ __forceinline__ PaSharedKeys() : z(0), h(-1) {}
   // the piece of block i that begins with its key `off` (of this lane); i does not decrease from call to call within a tile
   __device__ __forceinline__ PaPiece at(const PaParams& p, const PaSharedCursor<NH>& c, int i, int off) {
-    PaPiece r{INT_MIN, 0, 255};
+    PaPiece r{-1, 0, PA_NO_KEYS};
     int key = -1, row = -1, len = 0, v;
     const int zi = c.block(i, v);
     v += off;
@@ -329,7 +330,7 @@ struct PaSharedKeys {
     if (key >= 0 && key < len) {
       r.entry = p.t.table[(long long)row * p.t.stride + (key >> p.pg.lgS)];
       r.tok = key & (p.pg.S - 1);
-      if (len - key < (p.wide ? pa_piece(p) : 8)) r.valid = len - key;
+      r.valid = len - key < (p.wide ? pa_piece(p) : 8) ? len - key : 255;
     }
     return r;
   }

@@ -11,7 +11,8 @@ struct PaRowKeys {
   // the piece of block i that begins with its key `off` (of this lane)
   __device__ __forceinline__ PaPiece at(const PaParams& p, const PaCursor<NH, MODE>& c, int i, int off) const {
     const int v = i * PA_BN + off, key = MODE == PA_WINDOW && v >= p.sa ? v + c.shift(p) : v;
-    return PaPiece{key < c.q.s.len ? p.t.table[(long long)c.q.s.row * p.t.stride + (key >> p.pg.lgS)] : INT_MIN, key & (p.pg.S - 1), 255};
+    const bool some = key < c.q.s.len;
+    return PaPiece{some ? p.t.table[(long long)c.q.s.row * p.t.stride + (key >> p.pg.lgS)] : -1, key & (p.pg.S - 1), some ? 255 : PA_NO_KEYS};
   }
 };
 
