@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     }
   }
   if constexpr (MODE == PA_SHARED)
-    if (blockIdx.x == 0 && aux == 2) pa_check_shared(p);
+    if (aux == 2 && pa_checks_shared(p)) pa_check_shared(p);
   __syncthreads();
   if (aux == 3) {
     pa_fence_after();

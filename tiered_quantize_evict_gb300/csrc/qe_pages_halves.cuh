@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
     }
   }
   if constexpr (MODE == PA_SHARED)
-    if (blockIdx.x == 0 && aux == 3) pa_check_shared(p);
+    if (aux == 3 && pa_checks_shared(p)) pa_check_shared(p);
   __syncthreads();
   if (aux == 3) {
     pa_fence_after();
