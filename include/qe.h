@@ -501,7 +501,8 @@ enum {
   QE_PAGES_ERR_PAGE = 1,      /* a page index outside the pool, or a count of references that went wrong */
   QE_PAGES_ERR_ROW = 2,       /* a row index, length or q_start out of range, or a row named twice */
   QE_PAGES_ERR_NO_PAGES = 4,  /* not enough free pages: the call changed nothing */
-  QE_PAGES_ERR_TIMEOUT = 8    /* a bounded device wait expired: that call's outputs are undefined */
+  QE_PAGES_ERR_TIMEOUT = 8,   /* a bounded device wait expired: that call's outputs are undefined */
+  QE_PAGES_ERR_VALUE = 16     /* qe_pages_attend_shared: a result that is not finite */
 };
 
 /* The pool.  Element (layer, page, head, token, channel) of the keys is at
@@ -620,7 +621,8 @@ typedef struct {
  * kv_len - m of each of the group's chunks of m tokens (causal = 0: kv_len) and at most the first sequence's kv_len; one that is not, or a
  * group_start that decreases or leaves [0, n_seqs], sets QE_PAGES_ERR_ROW (a prefix is cut to the first sequence's length; a
  * chunk that begins inside its prefix sees all of it; sequences of no group are left alone).
- * Inputs are finite: a value that is not may reach all tokens of its group, those of the other sequences too.
+ * Inputs are finite: a value that is not may reach all tokens of its group, those of the other sequences too, and no other group.  A
+ * result that is not finite sets QE_PAGES_ERR_VALUE; qe_pages_attend then gives each of the sequences its own.
  * Sizes that can be served: (S + 1) max_pages page_size below 2^31, with S = min(n_seqs, 256 n_kv_heads / n_q_heads). */
 qe_status qe_pages_attend_shared(const qe_pages* pages, int layer, const qe_page_table* seqs, const qe_chunks* chunks,
                                  const qe_pages_attend_args* args, const qe_groups* groups, void* workspace, size_t bytes, void* stream);

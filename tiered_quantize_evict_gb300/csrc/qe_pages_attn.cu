@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(NT) pages_join_kernel(const __grid_constant__ 
   unsigned x[CH / 2];
 #pragma unroll
   for (int e = 0; e < CH / 2; ++e) x[e] = pa_pack<FP16>(o[2 * e] * inv, o[2 * e + 1] * inv);
+  if (p.gr.n > 0 && pa_strange<FP16, CH / 2>(x)) pages_report(p.pg, QE_PAGES_ERR_VALUE);
   uint16_t* dst = p.out + tok * p.ots + head * p.ohs + ch;
   if constexpr (CH == 16) pa_store32(dst, x);
   else if constexpr (CH == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);

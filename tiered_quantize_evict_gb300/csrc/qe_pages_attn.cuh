@@ -59,7 +59,7 @@ struct PaParams {
   int items;               // what the line is made of: sequences, or groups of them
   PagesWindow win;         // window: length, sinks,
   int sa;                  // and the sinks' whole pieces of pages in tokens
-  PagesGroups gr;          // shared prefixes
+  PagesGroups gr;          // shared prefixes (n = 0 without)
   float2* part_ml;         // [CTAs][2][NH][128]: reference, sum
   float* part_o;           // [CTAs][2][NH][D / 4][128][4]
 };
@@ -486,6 +486,17 @@ __device__ __forceinline__ unsigned pa_pack(float lo, float hi) {
   if constexpr (FP16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
+}
+
+// Whether one of N packed pairs is not finite: with shared prefixes such a value may be another sequence's (0 x inf), so a result that is
+// none is reported.  (An exponent of ones is the only one to which adding one carries out of it, into the sign's place.)
+template <bool FP16, int N>
+__device__ __forceinline__ bool pa_strange(const unsigned* x) {
+  constexpr unsigned EXP = FP16 ? 0x7C007C00u : 0x7F807F80u, ONE = FP16 ? 0x04000400u : 0x00800080u;
+  unsigned over = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) over |= (x[i] & EXP) + ONE;
+  return over & 0x80008000u;
 }
 
 template <bool FP16>

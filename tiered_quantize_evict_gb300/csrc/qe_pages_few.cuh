@@ -493,11 +493,16 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       uint16_t* dst = p.out + (long long)cur.tok(p) * p.ots + (long long)cur.head() * p.G * p.ohs + chan;
       float* po = p.part_o + (part * (D / 4) + chan / 4) * 512 + chan % 4;
       int g = 0;
+      unsigned strange = 0;
 #pragma unroll
       for (int c = 0; c < R; ++c)
         if (c < rows) {
           const float x = __uint_as_float(o[c]) + __uint_as_float(l[c]);
-          if (have && whole) *dst = (uint16_t)pa_pack<FP16>(x * s_inv[c], 0.f);
+          if (have && whole) {
+            const unsigned y = pa_pack<FP16>(x * s_inv[c], 0.f);
+            *dst = (uint16_t)y;
+            if (MODE == PA_SHARED) strange |= pa_strange<FP16, 1>(&y);
+          }
           if (have && !whole) po[c * 4] = x;
           dst += p.ohs;
           if (++g == p.G) {
@@ -505,6 +510,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             dst += p.ots - p.G * p.ohs;
           }
         }
+      if (MODE == PA_SHARED && strange) pages_report(p.pg, QE_PAGES_ERR_VALUE);
       pa_fence_before();
       pf_sync();   // O and the sums are read whole before the next tile's
     }

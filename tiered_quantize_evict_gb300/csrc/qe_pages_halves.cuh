@@ -640,6 +640,7 @@ __global__ void __launch_bounds__(PA_THREADS<NH>, 1)
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j)
                   u[j] = pa_pack<FP16>(__uint_as_float(o[4 * j + 2 * up]) * f, __uint_as_float(o[4 * j + 2 * up + 1]) * f);
+                if (MODE == PA_SHARED && to && pa_strange<FP16, D / 16>(u)) pages_report(p.pg, QE_PAGES_ERR_VALUE);
                 pa_quad_transpose<D / 64>(u);
                 if (to) {
                   uint16_t* dst = reinterpret_cast<uint16_t*>(to) + (lane & 3) * (D / 8);

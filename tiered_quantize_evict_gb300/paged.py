@@ -32,7 +32,7 @@ import torch
 
 from . import QE_ERR_DEVICE, QE_ERR_INVALID_ARG, QEError, load_library
 
-QE_PAGES_ERR_PAGE, QE_PAGES_ERR_ROW, QE_PAGES_ERR_NO_PAGES, QE_PAGES_ERR_TIMEOUT = 1, 2, 4, 8
+QE_PAGES_ERR_PAGE, QE_PAGES_ERR_ROW, QE_PAGES_ERR_NO_PAGES, QE_PAGES_ERR_TIMEOUT, QE_PAGES_ERR_VALUE = 1, 2, 4, 8, 16
 QE_PAGES_DROPPED = -2
 
 _P, _I, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
@@ -190,15 +190,16 @@ class PagePool:
         return buf
 
     def check(self):
-        """Waits for the current stream and raises if a call met a bad page, row or length, or ran out of pages;
-        clears the record."""
+        """Waits for the current stream and raises if a call met a bad page, row or length, ran out of pages, or shared a value that
+        is not finite; clears the record."""
         bits = int(self.err.item())
         if bits:
             self.err.zero_()
             names = [n for b, n in ((QE_PAGES_ERR_PAGE, "a page index or reference count out of range"),
                                     (QE_PAGES_ERR_ROW, "a row, length or q_start out of range, or a row named twice"),
                                     (QE_PAGES_ERR_NO_PAGES, "not enough free pages (nothing was changed)"),
-                                    (QE_PAGES_ERR_TIMEOUT, "a bounded device wait expired")) if bits & b]
+                                    (QE_PAGES_ERR_TIMEOUT, "a bounded device wait expired"),
+                                    (QE_PAGES_ERR_VALUE, "a result of attend_shared that is not finite (its group's others may be off)")) if bits & b]
             raise QEError(QE_ERR_DEVICE, "; ".join(names))
 
     def _seqs(self, seqs: PageTable):
@@ -327,7 +328,8 @@ class PagePool:
         group_start int32 [n_groups + 1]: group g is the call's sequences group_start[g] .. group_start[g + 1] - 1; prefix_len
         int32 [n_groups]: their first tokens, in the pages of the group's first sequence.  max_group_len: the most packed tokens
         of a group, or 0 if it is not known; max_q_len: the longest chunk, as of attend: where it is given, groups of any size have
-        the probabilities in as many bits as attend has them.  Values that are not finite may reach the whole group."""
+        the probabilities in as many bits as attend has them.  Values that are not finite may reach the whole group (and no other); `check` then
+        says so, and attend gives each sequence its own."""
         out, lse, ref, c, a = self._attend(q, q_start, seqs, rows, scale, causal, max_q_len, out, return_lse)
         if not 0 <= max_group_len < 2 ** 31:
             raise _bad(f"max_group_len {max_group_len} out of range")
