@@ -584,9 +584,14 @@ cudaError_t launch_pages_compact(const PagesView& pg, const TableView& t, int* t
 // A warp takes DROP_ENTRIES table entries of a row at a time.  Bound by its launch: what it moves is four bytes for each page of the rows,
 // and twice that for a page that goes.
 constexpr int DROP_ENTRIES = 256;
+// of the columns that a row can use
+__host__ __device__ __forceinline__ int drop_parts(const PagesView& pg, const TableView& t) {
+  const int most = (1 << 30) >> pg.lgS;
+  return ((t.cols < most ? t.cols : most) + DROP_ENTRIES - 1) / DROP_ENTRIES;
+}
 __global__ void __launch_bounds__(256) pages_drop_kernel(const PagesView pg, const TableView t, const int* rows, int n, const PagesWindow w) {
   griddep_wait();
-  const int lane = threadIdx.x & 31, parts = (t.cols + DROP_ENTRIES - 1) / DROP_ENTRIES;
+  const int lane = threadIdx.x & 31, parts = drop_parts(pg, t);
   const int first = (int)(((long long)w.sinks + pg.S - 1) >> pg.lgS);
   const long long units = (long long)n * parts;
   for (long long u = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += (long long)gridDim.x * 8) {
@@ -601,7 +606,7 @@ __global__ void __launch_bounds__(256) pages_drop_kernel(const PagesView pg, con
   }
 }
 cudaError_t launch_pages_drop(const PagesView& pg, const TableView& t, const int* rows, int n, const PagesWindow& w, int n_sm, cudaStream_t st) {
-  const long long blocks = ((long long)n * ((t.cols + DROP_ENTRIES - 1) / DROP_ENTRIES) + 7) / 8;
+  const long long blocks = ((long long)n * drop_parts(pg, t) + 7) / 8;
   return launch_after(pages_drop_kernel, (unsigned)(blocks < n_sm * 8 ? blocks : n_sm * 8), 256, st, pg, t, rows, n, w);
 }
 
