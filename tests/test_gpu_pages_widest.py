@@ -33,3 +33,15 @@ def test_drop(torch, env):
     assert seqs.table[0, :26].tolist() == [0, 1] + [qe.QE_PAGES_DROPPED] * 16 + list(range(18, 25)) + [-1]
     assert seqs.refs.tolist() == [1, 1] + [0] * 16 + [1] * 7 + [0] * 5
     assert torch.equal(seqs.table[0, -3:], last)       # (not the row's)
+
+
+def test_fork(torch, env):
+    """An empty row's copy: -1 in all columns."""
+    pool, seqs, ints = env
+    for a in (0, 2 ** 30, COLS - 3):
+        seqs.table[0, a:a + 3] = 5
+    pool.fork(seqs, ints(0), ints(0))
+    pool.check()
+    assert not seqs.refs.any() and seqs.kv_len.tolist() == [0]
+    for a in range(0, COLS, 2 ** 28):
+        assert (seqs.table[0, a:a + 2 ** 28] == -1).all()

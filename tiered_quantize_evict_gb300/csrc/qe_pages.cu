@@ -423,7 +423,8 @@ __device__ void apply_moves(const PagesView& pg, const TableView& t, int n, cons
     if (FORK) {
       const int* from = t.table + (long long)m.src * t.stride;
       const int full = m.new_len >> pg.lgS;
-      for (int j = tid; j < t.cols; j += TEAM) {
+      for (unsigned u = tid; u < (unsigned)t.cols; u += TEAM) {   // (up to 2^31 - 2 columns)
+        const int j = (int)u;
         int e = -1;
         if (j < full) {
           e = from[j];
