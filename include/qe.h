@@ -634,7 +634,7 @@ qe_status qe_pages_attend_shared_workspace(const qe_pages* pages, size_t* bytes)
  * they are.  Rows grow, are forked, cut, freed and compacted as before (a row that is cut back to inside of a dropped page is
  * reported where that page is needed: tokens taken back widen the window, so drop with a window that much larger).  Attention that
  * sees a dropped page, or gathering one, takes its keys as zeros and reports it, as any page that is not there.  A row may
- * be named twice.  Pages given back are free from the next call on. */
+ * be named twice; one whose length is out of range is left alone.  Pages given back are free from the next call on. */
 qe_status qe_pages_drop(const qe_pages* pages, const qe_page_table* seqs, const int* rows, int n, int window, int sinks, void* stream);
 
 /* Set the length of n rows (rows[i] to new_len[i], device int32): pages are taken (the lowest free

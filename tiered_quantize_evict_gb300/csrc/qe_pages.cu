@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(256) pages_drop_kernel(const PagesView pg, con
     const int i = (int)(u / parts), part = (int)(u - (long long)i * parts), row = rows[i];
     const int len = row_len(pg, t, row, part == 0 && lane == 0);
     const int end = min((max(len - w.window + 1, 0) >> pg.lgS), (part + 1) * DROP_ENTRIES);
-    if (len == 0) continue;
+    if (len == 0 || t.kv_len[row] != len) continue;   // (nothing goes by a length that is out of range)
     int* entry = t.table + (long long)row * t.stride;
     for (int j = max(first, part * DROP_ENTRIES) + lane; j < end; j += 32)
       // (exchanged: another entry of the call may name the row too)
