@@ -582,8 +582,9 @@ cudaError_t launch_pages_compact(const PagesView& pg, const TableView& t, int* t
 }
 
 // ---------------------------------------------------------------------------- drop
-// A warp takes DROP_ENTRIES table entries of a row at a time.  Bound by its launch: what it moves is four bytes for each page of the rows,
-// and twice that for a page that goes.
+// A warp takes DROP_ENTRIES table entries of a row at a time.  Where little goes it is bound by its launch: four bytes are read for each page
+// that the window has left (256 rows of up to 32K tokens with nothing to give back: 3.4 us in a graph).  A page that goes is a chain of three
+// accesses, and a lane has its 8 entries' one after the other: the same rows giving back 275102 pages, 4.4 MB, take 12 us.
 constexpr int DROP_ENTRIES = 256;
 // of the columns that a row can use
 __host__ __device__ __forceinline__ int drop_parts(const PagesView& pg, const TableView& t) {

@@ -4,7 +4,7 @@
 // channels) as the 128 rows of the tensor cores and the few query rows as N = 16 columns:
 //   S^T = K Q^T (128 keys x N),   O^T += V^T P^T (head_dim channels x 2 N, keys inner),
 // with the formulas and the split of the line of qe_pages_halves.cuh.  A block costs the tensor cores about 600 cycles instead of 1536,
-// and a thread 16 exponentials instead of 64 whatever the rows (decode step of 16 sequences of up to 32K tokens: 302 -> 287 us with
+// and a thread 4, 8 or 16 exponentials (as many as the tile has rows) instead of 64 (decode step of 16 sequences of up to 32K tokens: 302 -> 287 us with
 // 128 channels, 236 -> 171 us with 64).
 //  * P^T is written to shared memory in two parts per probability, rounded and remainder, as 2 N columns (about 17 significant bits
 //    for bf16); the output adds the two columns of a row.  A key's 2 N columns are 64 bytes; the P of odd blocks is the other half

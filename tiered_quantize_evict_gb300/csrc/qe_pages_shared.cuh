@@ -106,7 +106,7 @@ struct PaSharedTile {
 };
 
 // Places in shared memory: where the CTA's walk starts, where it ends, and with one half the tiles behind the first, as far as they are
-// kept: what a warp would have to gather of the arrays again, between two tiles (64 groups of 8 sequences 148.7 -> 143.3 us; the softmax of
+// kept: what a warp would have to gather of the arrays again, between two tiles (64 groups of 8 sequences 148 -> 142 us; the softmax of
 // two halves has no registers for it: 64 sequences 70 -> 88).
 constexpr int PA_KEPT = 3;
 template <int NH>
