@@ -27,8 +27,8 @@
 //    2^-32 of the reference's weight where that is more (P is taken 2^7 times as large, or it would be 2^-25); the sum is of the
 //    unrounded ones.  With NH = 1, where the tensor cores wait for memory anyway, what the rounding leaves is kept as
 //    a second operand and multiplied too: error against 64 bits 1.45 -> 1.0 times that of the result's own rounding.
-//    REST: with two halves of shared prefixes too, where the caller says that the chunks are short (a block of both halves is then 3072
-//    cycles of products, not 2048, and takes 2.0 us where reading it takes 1.4: 64 sequences behind a 32K prefix 69 -> 79 us, error 2.2e-3 -> 1.7e-3).
+//    REST: with two halves of shared prefixes too, where the caller says that the chunks are short (a block of both halves then has one and a
+//    half times the products and takes 2.0 us where reading it takes 1.4: 64 sequences behind a 32K prefix 69 -> 79 us, error 2.2e-3 -> 1.7e-3).
 // mbarriers.  Every wait is bounded, by 0.2 s and 10 us for each block that it may sit out; one that expires sets QE_PAGES_ERR_TIMEOUT
 // and an abort flag that ends all loops, and the CTA leaves after what it issued has landed: each warp that issues waits for its own
 // last, whether it or another warp gave up.
